@@ -9,7 +9,8 @@ every call raises.
 Entry points (same names as the C ABI, without the ``ds4x_`` prefix):
   indexer_score, topk, sparse_attn, index_and_attend, workspace_bytes, decode,
   decode_workspace_bytes, topk_workspace_bytes, topk_static_scratch, device_status,
-  selftest_bounded_wait, last_launch_count
+  selftest_bounded_wait, last_launch_count; the paged 4-bit cache: page_plan, kv4_append,
+  kv4_read, kv4_attn, kv4_attn_workspace_bytes
 """
 from __future__ import annotations
 
@@ -26,6 +27,9 @@ F16, BF16 = 0, 1
 MAX_KTOP = 1024
 MAX_WINDOW = 1024
 MAX_RATIO = 65536
+MAX_REQ = 4096
+MAX_PAGE_ROWS = 65536
+KV4_CODE_BYTES, KV4_SCALE_BYTES = 256, 16  # of one 512-dim row of the 4-bit cache
 EXPORTS = (
     "ds4x_indexer_score", "ds4x_topk", "ds4x_topk_workspace_bytes", "ds4x_sparse_attn",
     "ds4x_index_and_attend", "ds4x_workspace_bytes", "ds4x_status_string",
@@ -35,6 +39,7 @@ EXPORTS = (
     "ds4x_local_pooled_attn", "ds4x_index_and_attend_local", "ds4x_workspace_bytes_local",
     "ds4x_index_and_attend_local_host", "ds4x_index_and_attend_local_host_bytes", "ds4x_compress",
     "ds4x_decode_local", "ds4x_decode_local_workspace_bytes",
+    "ds4x_page_plan", "ds4x_kv4_append", "ds4x_kv4_read", "ds4x_kv4_attn", "ds4x_kv4_attn_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -95,7 +100,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.ds4x_last_launch_count.argtypes = []
         lib.ds4x_device_status.argtypes = [P, ctypes.c_int]
         lib.ds4x_selftest_bounded_wait.argtypes = [i64, P]
-        for f in ("ds4x_indexer_score", "ds4x_topk", "ds4x_sparse_attn", "ds4x_index_and_attend", "ds4x_decode",
+        lib.ds4x_page_plan.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P]
+        lib.ds4x_kv4_append.argtypes = [P, ctypes.c_int, P, i32, i32, P, P, i32, P]
+        lib.ds4x_kv4_read.argtypes = [P, P, i32, P, i32, i32, P, ctypes.c_int, P]
+        lib.ds4x_kv4_attn.argtypes = [P, ctypes.c_int, P, P, i32, P, P, i32, i32, i32, P, P, i32, P, P, i32, i32, i32,
+                                      i32, f32, P, P, P, sz, P]
+        lib.ds4x_kv4_attn_workspace_bytes.argtypes = [i32, i32]
+        lib.ds4x_kv4_attn_workspace_bytes.restype = sz
+        for f in ("ds4x_page_plan", "ds4x_kv4_append", "ds4x_kv4_read", "ds4x_kv4_attn", "ds4x_indexer_score", "ds4x_topk", "ds4x_sparse_attn", "ds4x_index_and_attend", "ds4x_decode",
                   "ds4x_index_and_attend_host", "ds4x_local_pooled_attn", "ds4x_index_and_attend_local",
                   "ds4x_index_and_attend_local_host", "ds4x_compress", "ds4x_decode_local",
                   "ds4x_last_launch_count", "ds4x_device_status", "ds4x_selftest_bounded_wait"):
@@ -535,6 +547,191 @@ def decode_local(q, w, q_attn, k, kv, S0: int, pos0: int, ratio: int, kv_raw, kv
                                   ctypes.byref(s_final), _stream(stream))
     _check("ds4x_decode_local", rc)
     return indices, out, lse, positions, int(s_final.value)
+
+
+# ----------------------------------------------------------------------- paged 4-bit cache
+class _On:
+    """Makes `device` current, and `stream` when one is given, so that what a call allocates belongs to
+    the stream that its kernels run on.  Gives that stream's address."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self._ctx = ()
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                               device=device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        if stream is not None:
+            self._ctx = (torch.cuda.device(device), torch.cuda.stream(stream))
+        elif torch.cuda.current_device() != device.index:
+            self._ctx = (torch.cuda.device(device),)
+        self._stream, self._device = stream, device
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        s = _torch().cuda.current_stream(self._device) if self._stream is None else self._stream
+        return s.cuda_stream
+
+    def __exit__(self, *e):
+        for c in reversed(self._ctx):
+            c.__exit__(*e)
+
+
+def _tensor(name, t, dtype, device=None, numel=None, shape=None):
+    """The address of a CUDA tensor after checking its dtype, device, layout and size (numel: at least)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be of shape {shape}, got {tuple(t.shape)}")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
+    return t.data_ptr()
+
+
+def _kv4_pool(codes, scales, device):
+    """Addresses of a pool's codes [..., 256] and scales [..., 16], and its number of slots."""
+    torch = _torch()
+    pc = _tensor("codes", codes, torch.uint8, device)
+    psc = _tensor("scales", scales, torch.uint8, device)
+    if codes.shape[-1] != KV4_CODE_BYTES or scales.shape[-1] != KV4_SCALE_BYTES:
+        raise ValueError(f"codes must end in {KV4_CODE_BYTES} bytes and scales in {KV4_SCALE_BYTES}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    n = codes.numel() // KV4_CODE_BYTES
+    if scales.numel() // KV4_SCALE_BYTES != n:
+        raise ValueError(f"codes hold {n} slots, scales {scales.numel() // KV4_SCALE_BYTES}")
+    return pc, psc, n
+
+
+def page_plan(seen, n_new, rows, tables, free_pages, n_free, ratio: int, page_rows: int, T_cap: int, R_cap: int,
+              positions=None, req=None, slots=None, seen_out=None, rows_out=None, n_free_out=None, totals=None,
+              stream=None):
+    """Positions, request ids, block tables and slots of one step of a batch, from its lengths, in one launch.
+    seen, n_new, rows [n_req] int32: positions before the step, new ones, pooled rows held; tables
+    [n_req, max_pages] int32, the new pages' entries are written in place; pages are taken from the end of
+    free_pages[:n_free] (n_free [1] int32).  Returns (positions [T_cap], req [T_cap], slots [R_cap], seen_out,
+    rows_out, n_free_out, totals [4] = tokens, completed rows, rows with a slot, pages taken); the packed
+    outputs end in -1.  An output may be passed in; seen_out, rows_out and n_free_out may be their inputs."""
+    torch = _torch()
+    i32, dev = torch.int32, seen.device
+    B = seen.numel()
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError(f"tables must be [{B}, max_pages], got {tuple(tables.shape)}")
+    max_pages = tables.shape[1]
+    a = [_tensor("seen", seen, i32), _tensor("n_new", n_new, i32, dev, B), _tensor("rows", rows, i32, dev, B),
+         _tensor("tables", tables, i32, dev), _tensor("free_pages", free_pages, i32, dev)]
+    pf = _tensor("n_free", n_free, i32, dev, 1)
+    with _On(dev, stream) as st:
+        def out(name, t, n):
+            if t is None:
+                t = torch.empty((n,), dtype=i32, device=dev)
+            return t, _tensor(name, t, i32, dev, n)
+        positions, p0 = out("positions", positions, T_cap)
+        req, p1 = out("req", req, T_cap)
+        slots, p2 = out("slots", slots, R_cap)
+        seen_out, p3 = out("seen_out", seen_out, B)
+        rows_out, p4 = out("rows_out", rows_out, B)
+        n_free_out, p5 = out("n_free_out", n_free_out, 1)
+        totals, p6 = out("totals", totals, 4)
+        rc = load().ds4x_page_plan(*a, free_pages.numel(), pf, B, max_pages, page_rows, ratio, T_cap, R_cap,
+                                   p0, p1, p2, p3, p4, p5, p6, st)
+    _check("ds4x_page_plan", rc)
+    return positions, req, slots, seen_out, rows_out, n_free_out, totals
+
+
+def kv4_append(rows, slots, codes, scales, stream=None):
+    """Quantises rows [n, 512] (fp16 or bf16) and writes row i to slot slots[i] of the pool codes [..., 256],
+    scales [..., 16]; a slot outside the pool (the -1 of page_plan) skips its row.  Slots must be distinct."""
+    torch = _torch()
+    dt, dev = _kv_dtype(rows), rows.device
+    n, Dkv = rows.shape
+    pr = _tensor("rows", rows, rows.dtype)
+    ps = _tensor("slots", slots, torch.int32, dev, n)
+    pc, psc, n_slots = _kv4_pool(codes, scales, dev)
+    with _On(dev, stream) as st:
+        rc = load().ds4x_kv4_append(pr, dt, ps, n, Dkv, pc, psc, n_slots, st)
+    _check("ds4x_kv4_append", rc)
+
+
+def kv4_read(codes, scales, slots, dtype, out=None, stream=None):
+    """The rows at slots [n] int32 of the pool as [n, 512] of `dtype` (float16 or bfloat16); zeros for a slot
+    outside the pool."""
+    torch = _torch()
+    dev = codes.device
+    pc, psc, n_slots = _kv4_pool(codes, scales, dev)
+    n, Dkv = slots.numel(), 2 * KV4_CODE_BYTES
+    ps = _tensor("slots", slots, torch.int32, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((n, Dkv), dtype=dtype, device=dev)
+        po = _tensor("out", out, dtype, dev, shape=(n, Dkv))
+        rc = load().ds4x_kv4_read(pc, psc, n_slots, ps, n, Dkv, po, _kv_dtype(out), st)
+    _check("ds4x_kv4_read", rc)
+    return out
+
+
+def kv4_attn_workspace_bytes(T: int, max_rows: int) -> int:
+    """Workspace of kv4_attn: max_rows = k_top, or max_pages * page_rows without indices."""
+    return int(load().ds4x_kv4_attn_workspace_bytes(T, max_rows))
+
+
+def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, positions=None, ratio: int = 1,
+             indices=None, counts=None, scale: float | None = None, out=None, lse=None, workspace=None,
+             want_lse: bool = True, stream=None):
+    """64-head MQA of q_attn [T, 64, 512] over rows of the paged 4-bit cache.  Token t belongs to request
+    req[t] (None: request t), which holds rows[b] rows through tables[b] [max_pages].  With indices
+    [T, k_top] it attends to those rows (the first counts[t] entries; -1 and rows not held are skipped),
+    without to every row visible at positions[t] (None: all held).  Returns (out, lse)."""
+    torch = _torch()
+    i32, dev = torch.int32, q_attn.device
+    dt = _kv_dtype(q_attn)
+    T, Hq, Dkv = q_attn.shape
+    pq = _tensor("q_attn", q_attn, q_attn.dtype)
+    pc, psc, n_slots = _kv4_pool(codes, scales, dev)
+    n_req = rows.numel()
+    prow = _tensor("rows", rows, i32, dev)
+    if tables.dim() != 2 or tables.shape[0] != n_req:
+        raise ValueError(f"tables must be [{n_req}, max_pages], got {tuple(tables.shape)}")
+    max_pages = tables.shape[1]
+    ptab = _tensor("tables", tables, i32, dev)
+    preq = None if req is None else _tensor("req", req, i32, dev, T)
+    ppos = None if positions is None else _tensor("positions", positions, i32, dev, T)
+    k_top, pidx, pcnt, max_rows = 0, None, None, max_pages * page_rows
+    if indices is not None:
+        if indices.dim() != 2 or indices.shape[0] != T:
+            raise ValueError(f"indices must be [{T}, k_top], got {tuple(indices.shape)}")
+        k_top = max_rows = indices.shape[1]
+        pidx = _tensor("indices", indices, i32, dev)
+        pcnt = None if counts is None else _tensor("counts", counts, i32, dev, T)
+    elif counts is not None:
+        raise ValueError("counts belong to indices")
+    scale = 1.0 / math.sqrt(Dkv) if scale is None else scale
+    lib = load()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(q_attn)
+        if lse is None and want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        po = _tensor("out", out, q_attn.dtype, dev, shape=(T, Hq, Dkv))
+        pl = None if lse is None else _tensor("lse", lse, torch.float32, dev, shape=(T, Hq))
+        if workspace is None:
+            need = lib.ds4x_kv4_attn_workspace_bytes(T, max_rows)
+            if need > 0:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        pw, wbytes = None, 0
+        if workspace is not None:
+            pw, wbytes = _tensor("workspace", workspace, workspace.dtype, dev), workspace.nbytes
+        rc = lib.ds4x_kv4_attn(pq, dt, pc, psc, n_slots, ptab, prow, n_req, max_pages, page_rows, preq, ppos, ratio,
+                               pidx, pcnt, T, Hq, Dkv, k_top, scale, po, pl, pw, wbytes, st)
+    _check("ds4x_kv4_attn", rc)
+    return out, lse
 
 
 def device_status(stream=None, clear: bool = True) -> int:

@@ -141,6 +141,29 @@ struct CompressArgs {
 };
 int launch_compress(const CompressArgs& a, cudaStream_t stream);
 
+struct Kv4AttnArgs {
+  const void* q_attn;  // [T, 64, 512]
+  int bf16;
+  const uint8_t* codes;   // [n_slots, 256]
+  const uint8_t* scales;  // [n_slots, 16]
+  int n_slots;
+  const int32_t* tables;  // [n_req, max_pages]
+  const int32_t* rows;    // [n_req]
+  int n_req, max_pages, log_page;
+  const int32_t* req;        // [T] or NULL (token t = request t)
+  const int32_t* positions;  // [T] or NULL, read without indices only
+  int ratio;
+  const int32_t* indices;  // [T, k_top] or NULL (every visible row)
+  const int32_t* counts;   // [T] or NULL
+  int T, k_top;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;  // at least kv4_attn_workspace_bytes(T, max_rows)
+};
+size_t kv4_attn_workspace_bytes(int T, int max_rows);
+int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream);
+
 // The fused path (score -> top-k -> attention, Hq = 64, Dkv = 512) on validated arguments, and
 // the workspace it needs: [scores T x S fp32 | top-k scratch | split-attention scratch].
 size_t fused_workspace_bytes(int T, int S, int k_top, int window = 0);

@@ -348,6 +348,110 @@ int ds4x_decode_local(const void* q, const void* w, const void* q_attn, void* k,
                       size_t workspace_bytes, int32_t* S_final, void* stream);
 size_t ds4x_decode_local_workspace_bytes(int32_t capacity, int32_t k_top, int32_t window);
 
+/* ---------------------------------------------------------------------------
+ * The paged 4-bit cache: pooled rows of many requests in one pool of pages.
+ * No counterpart on the pages: the serving form of the row cache that ds4x_decode keeps for one
+ * sequence in 16 bits.
+ *
+ *   A row (Dkv = 512) is held as 256 bytes of codes and 16 bytes of scales, in two arrays
+ *     codes  [n_slots, 256] uint8    element 2i in the low nibble of byte i, 2i+1 in the high one
+ *     scales [n_slots, 16]  uint8    one byte b for each group of 32 elements
+ *   A code is e2m1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *   negatives); the element is code * 2^(b - 127).  b = 255 marks a group that held a NaN: all of
+ *   its elements read as NaN.  The library writes 104 <= b <= 140 otherwise, where every element is
+ *   exact in fp16 and in bf16.  A 16-bit row needs 1024 bytes, this one 272.
+ *
+ *   Pages hold page_rows consecutive slots (a power of two, at most DS4X_MAX_PAGE_ROWS): page g is
+ *   slots g*page_rows .. g*page_rows + page_rows - 1.  Row r of request b is at slot
+ *     tables[b, r / page_rows] * page_rows + r % page_rows
+ *   with tables [n_req, max_pages] int32 (a negative entry: no such row).
+ *
+ *   The int32 arrays of these entries need 4-byte alignment only (so per-request slices of the
+ *   slots can be passed); codes, scales and 16-bit tensors need 16.
+ * ------------------------------------------------------------------------- */
+#define DS4X_MAX_REQ 4096
+#define DS4X_MAX_PAGE_ROWS 65536
+
+/* ---------------------------------------------------------------------------
+ * ds4x_page_plan — positions, request ids, block tables and slots of one step of a batch, built on
+ * the GPU from the requests' lengths in one launch.
+ *
+ *   Request b has seen[b] positions, holds rows[b] pooled rows and takes n_new[b] more positions
+ *   (negative values count as 0; rows are clipped to max_pages * page_rows, positions to INT32_MAX).
+ *   It completes  done_b = (seen+new)/ratio - seen/ratio  rows, the rows that ds4x_compress emits.
+ *   Pages for them are taken from the END of free_pages[0 .. *n_free - 1], in request order; a page
+ *   that is partly filled is filled up first.  When the list runs out, or a request's table row is
+ *   full, the request's remaining rows get no slot.
+ *
+ *   positions, req [T_cap]: the step's tokens packed in request order: position and request id of
+ *       each; -1 behind the last one.
+ *   slots [R_cap]: the completed rows packed in request order (done_b of each request): the slot
+ *       each goes to, -1 for a row without a page; -1 behind the last one.
+ *   tables [n_req, max_pages], updated in place: the entries of the pages taken are written.
+ *   seen_out, rows_out [n_req], n_free_out [1]: the state after the step (NULL: not wanted; each may
+ *       be its input itself: then the call advances the state, and a captured call can be replayed).
+ *       rows_out counts the rows that have a slot.
+ *   totals [4] (or NULL): tokens, completed rows, rows with a slot, pages taken (each at most
+ *       INT32_MAX).  Tokens or rows beyond T_cap / R_cap are left out of the packed outputs only.
+ *   free_pages [free_capacity], n_free [1] on the device (*n_free is clipped to the capacity).
+ *   n_req <= DS4X_MAX_REQ and max_pages * page_rows <= INT32_MAX, else DS4X_ERR_UNSUPPORTED.
+ *   Apart from the three state pairs the outputs overlap nothing.  To retire a request, put the first
+ *   ceil(rows / page_rows) entries of its table row back on the list and set its seen and rows to 0.
+ * ------------------------------------------------------------------------- */
+int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* rows, int32_t* tables,
+                   const int32_t* free_pages, int32_t free_capacity, const int32_t* n_free, int32_t n_req,
+                   int32_t max_pages, int32_t page_rows, int32_t ratio, int32_t T_cap, int32_t R_cap,
+                   int32_t* positions, int32_t* req, int32_t* slots, int32_t* seen_out, int32_t* rows_out,
+                   int32_t* n_free_out, int32_t* totals, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ds4x_kv4_append — quantises n rows and writes row i to slot slots[i].
+ *
+ *   Per group of 32 elements: e = the least exponent with max|x| <= 6 * 2^e, kept in [-23, 13];
+ *   code = x * 2^-e to the nearest e2m1 value, ties to the even code; the scale byte is e + 127.
+ *   Larger magnitudes (and infinities) saturate at 6 * 2^13 = 49152; a group with a NaN gets b = 255.
+ *   rows [n, Dkv] of `dtype`, slots [n] int32: a slot outside [0, n_slots) skips its row (the -1 of
+ *   ds4x_page_plan).  The slots in range must be distinct.  Dkv = 512.
+ * ------------------------------------------------------------------------- */
+int ds4x_kv4_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, int32_t n, int32_t Dkv,
+                    uint8_t* codes, uint8_t* scales, int32_t n_slots, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ds4x_kv4_read — out[i, :] = the elements of slot slots[i] in `dtype` (exact for what
+ * ds4x_kv4_append wrote), zeros for a slot outside [0, n_slots): rows of the cache for the entries
+ * that take 16-bit rows.  Slots may repeat.  out [n, Dkv], Dkv = 512.
+ * ------------------------------------------------------------------------- */
+int ds4x_kv4_read(const uint8_t* codes, const uint8_t* scales, int32_t n_slots, const int32_t* slots,
+                  int32_t n, int32_t Dkv, void* out, ds4x_dtype dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ds4x_kv4_attn — ds4x_sparse_attn over the paged 4-bit cache, for tokens of many requests.
+ *
+ *   Token t belongs to request b = req[t] (req = NULL: b = t, which needs T <= n_req; a request
+ *   outside [0, n_req) has no rows) and attends to these rows of it, all below
+ *   held = min(rows[b], max_pages * page_rows):
+ *     indices given: rows indices[t, j] for j < counts[t] (counts = NULL: j < k_top) with
+ *                    0 <= indices[t, j] < held; others are skipped, repeated ones count again
+ *     indices NULL:  every visible row: 0 .. min(held, floor((positions[t]+1)/ratio)) - 1
+ *                    (positions = NULL: 0 .. held - 1).  k_top and counts are not used then.
+ *   A row whose table entry is negative or whose slot is not below n_slots is skipped.
+ *   out[t,h,:] and lse[t,h] as in ds4x_sparse_attn over those rows; a token without any gets out = 0
+ *   and lse = -INFINITY.
+ *
+ *   q_attn, out [T, Hq, Dkv] of `dtype`; lse [T, Hq] fp32 or NULL; indices [T, k_top], counts [T],
+ *   req [T], positions [T], rows [n_req] int32.  Hq = 64, Dkv = 512, 1 <= k_top <= DS4X_MAX_KTOP.
+ *   workspace: at least ds4x_kv4_attn_workspace_bytes(T, max_rows) bytes, max_rows = k_top, or
+ *   max_pages * page_rows without indices (may be NULL when that is 0).  Nothing is kept in it
+ *   between calls; calls that may overlap on the GPU need one each.
+ * ------------------------------------------------------------------------- */
+int ds4x_kv4_attn(const void* q_attn, ds4x_dtype dtype, const uint8_t* codes, const uint8_t* scales,
+                  int32_t n_slots, const int32_t* tables, const int32_t* rows, int32_t n_req,
+                  int32_t max_pages, int32_t page_rows, const int32_t* req, const int32_t* positions,
+                  int32_t ratio, const int32_t* indices, const int32_t* counts, int32_t T, int32_t Hq,
+                  int32_t Dkv, int32_t k_top, float scale, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream);
+size_t ds4x_kv4_attn_workspace_bytes(int32_t T, int32_t max_rows);
+
 /* Human-readable name of a ds4x_status value (static storage, never NULL). */
 const char* ds4x_status_string(int status);
 

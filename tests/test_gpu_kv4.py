@@ -1,0 +1,553 @@
+"""The paged 4-bit cache on the GPU against its plain implementation in 64 bits (oracle/kv4.py)."""
+import numpy as np
+import pytest
+import torch
+
+import deepseek_v4_sparse_gb300 as ds4x
+from oracle import kv4
+
+pytestmark = pytest.mark.gpu
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+I32 = torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from deepseek_v4_sparse_gb300 import build
+    build.build()
+    ds4x.load()
+    yield
+    torch.cuda.synchronize()
+    assert ds4x.device_status() == ds4x.OK
+
+
+def gpu(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def i32(a):
+    return gpu(np.asarray(a, dtype=np.int32))
+
+
+def rows_of(rng, n, dtype):
+    x = rng.standard_normal((n, 512)) * np.exp2(rng.integers(-4, 3, (n, 1)).astype(float))
+    return torch.from_numpy(x).to(DT[dtype])
+
+
+# ------------------------------------------------------------------------------- append and read
+def special_rows(dtype):
+    """Ties, zeros of both signs, least and largest values, infinities and NaN in groups of their own."""
+    x = torch.zeros((6, 512), dtype=torch.float64)
+    grid = torch.arange(-32, 33, dtype=torch.float64) / 4               # quarter steps: every tie of e = 0
+    x[0, :65], x[0, 96] = grid, 6.0
+    x[0, 64:128:2] = -0.0
+    for k, e in enumerate((-24, -14, -3, 5, 12)):
+        x[1, 64 * k:64 * k + 65] = grid * 2.0 ** e
+    x[2] = torch.finfo(DT[dtype]).tiny * torch.linspace(-3, 3, 512, dtype=torch.float64)
+    x[3] = torch.finfo(DT[dtype]).max * torch.linspace(-1, 1, 512, dtype=torch.float64)
+    x[4, 7], x[4, 40], x[4, 41] = float("inf"), float("-inf"), 1e4
+    x[5, 3], x[5, 511], x[5, 510] = float("nan"), float("nan"), float("inf")
+    x[5, 100] = 3.0
+    return x.to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [0, 1, 6, 7, 300, 20001])
+def test_append_read(n, dtype):
+    rng = np.random.default_rng(n)
+    x = special_rows(dtype) if n == 6 else rows_of(rng, n, dtype)
+    n_slots = n + 11
+    slots = rng.permutation(n_slots)[:n].astype(np.int32)
+    if n >= 7:
+        slots[::5] = -1
+        slots[1] = n_slots           # behind the pool
+        slots[3] = 2 ** 31 - 1
+    codes = rng.integers(0, 256, (n_slots, 256), dtype=np.uint8)
+    scales = rng.integers(104, 141, (n_slots, 16), dtype=np.uint8)
+    dc, dsc = gpu(codes), gpu(scales)
+    ds4x.kv4_append(x.cuda(), i32(slots), dc, dsc)
+    m = min(n, 700)                  # the plain form is slow: the first rows bit by bit
+    pick = rng.permutation(n)[:m]
+    rc, rs = kv4.quantise(x[pick].double().numpy())
+    ok = (slots[pick] >= 0) & (slots[pick] < n_slots)
+    got_c, got_s = dc.cpu().numpy(), dsc.cpu().numpy()
+    at = slots[pick][ok]
+    assert np.array_equal(got_s[at], rs[ok])
+    codes_count = np.repeat(rs[ok] != 255, 16, axis=1)
+    assert np.array_equal(got_c[at][codes_count], rc[ok][codes_count])
+    kept = np.setdiff1d(np.arange(n_slots), slots)   # rows of other slots are as they were
+    assert np.array_equal(got_c[kept], codes[kept]) and np.array_equal(got_s[kept], scales[kept])
+    # read: exact, zeros without a slot, slots may repeat
+    again = np.concatenate([slots, slots[:2], [-5]]).astype(np.int32)
+    out = ds4x.kv4_read(dc, dsc, i32(again), DT[dtype]).double().cpu().numpy()
+    live = (again >= 0) & (again < n_slots)
+    ref = np.zeros((len(again), 512))
+    ref[live] = kv4.values(got_c[again[live]], got_s[again[live]])
+    assert np.array_equal(out, ref, equal_nan=True)
+
+
+def test_append_takes_slices_of_slots():
+    rng = np.random.default_rng(5)
+    x = rows_of(rng, 9, "bf16").cuda()
+    slots = i32([0, 7, 3, 5, 1, 6, 2, 8, 4])
+    pool = torch.zeros((9, 256), dtype=torch.uint8, device="cuda"), torch.zeros((9, 16), dtype=torch.uint8, device="cuda")
+    for a, b in ((0, 1), (1, 4), (4, 9)):              # 4-byte aligned starts
+        ds4x.kv4_append(x[a:b], slots[a:b], *pool)
+    c, s = kv4.quantise(x.double().cpu().numpy())
+    assert np.array_equal(pool[0][slots.long()].cpu().numpy(), c)
+    assert np.array_equal(pool[1][slots.long()].cpu().numpy(), s)
+
+
+# ------------------------------------------------------------------------------------- step plan
+def plan_case(rng, B, max_pages, ps, ratio, hi_new, spare, T_cap=None, R_cap=None):
+    cap = max_pages * ps
+    seen = rng.integers(0, cap * ratio + 1, B)
+    rows = np.minimum(seen // ratio, cap)
+    new = rng.integers(-1, hi_new + 1, B)
+    held = -(-rows // ps)
+    pages = rng.permutation(int(held.sum()) + max(spare, 1)).astype(np.int32)
+    tables = np.full((B, max_pages), -1, dtype=np.int32)
+    k = 0
+    for b in range(B):
+        tables[b, :held[b]] = pages[k:k + held[b]]
+        k += held[b]
+    T_cap = int(np.maximum(new, 0).sum()) + 3 if T_cap is None else T_cap
+    R_cap = int(np.maximum(new, 0).sum()) // ratio + B if R_cap is None else R_cap
+    return [seen.astype(np.int32), new.astype(np.int32), rows.astype(np.int32), tables, pages[k:], np.int32(spare),
+            ratio, ps, T_cap, R_cap]
+
+
+def run_plan(c, **kw):
+    seen, new, rows, tables, free, n_free, ratio, ps, T_cap, R_cap = c
+    dt = i32(tables)
+    out = ds4x.page_plan(i32(seen), i32(new), i32(rows), dt, i32(free), i32([n_free]), ratio, ps, T_cap, R_cap, **kw)
+    p, r, s, se, ro, nf, to = (x.cpu().numpy() for x in out)
+    return p, r, s, dt.cpu().numpy(), se, ro, nf[0], to
+
+
+def check_plan(got, ref):
+    for name, g, r in zip(("positions", "req", "slots", "tables", "seen", "rows", "n_free", "totals"), got, ref):
+        assert np.array_equal(g, r), name
+
+
+@pytest.mark.parametrize("B,max_pages,ps,ratio,hi_new,spare", [
+    (1, 1, 1, 1, 1, 1), (1, 5, 8, 4, 1, 3), (3, 4, 16, 1, 40, 2), (64, 9, 64, 4, 1, 64), (65, 3, 8, 3, 200, 30),
+    (1000, 6, 4, 7, 60, 4000), (4096, 2, 32, 4, 9, 100), (33, 7, 16, 128, 3000, 0), (1025, 2, 2, 1, 5, 777),
+])
+def test_page_plan(B, max_pages, ps, ratio, hi_new, spare):
+    rng = np.random.default_rng(B * 131 + ps)
+    c = plan_case(rng, B, max_pages, ps, ratio, hi_new, spare)
+    check_plan(run_plan(c), kv4.page_plan(*c))
+
+
+def test_page_plan_short_outputs_and_odd_state():
+    rng = np.random.default_rng(3)
+    c = plan_case(rng, 40, 3, 8, 4, 50, 20, T_cap=100, R_cap=13)          # packed outputs cut off
+    check_plan(run_plan(c), kv4.page_plan(*c))
+    c[0] = c[0] - 20                                                       # negative seen counts as 0
+    c[2] = c[2] * 3 - 10                                                   # rows outside 0 .. cap are clipped
+    c[5] = np.int32(10 ** 6)                                               # more free pages than the list holds
+    check_plan(run_plan(c), kv4.page_plan(*c))
+    c[8], c[9] = 0, 0
+    check_plan(run_plan(c), kv4.page_plan(*c))
+
+
+def test_page_plan_counts_that_pass_32_bits():
+    big = 2 ** 31 - 1
+    B = 5
+    c = [np.array([0, 7, big - 3, big, 100], dtype=np.int32), np.full(B, big, dtype=np.int32),
+         np.array([0, 7, 30, 32, 2], dtype=np.int32), np.full((B, 4), -1, dtype=np.int32),
+         np.arange(20, dtype=np.int32), np.int32(20), 1, 8, 50, 50]
+    check_plan(run_plan(c), kv4.page_plan(*c))
+    c[3][:, 0] = 2 ** 30                                                   # a page beyond any slot number
+    check_plan(run_plan(c), kv4.page_plan(*c))
+
+
+def test_page_plan_steps_in_place_and_captured():
+    """A decode loop that advances its own state, replayed as a graph."""
+    B, ps, ratio, max_pages = 37, 4, 2, 6
+    rng = np.random.default_rng(9)
+    ref = [np.zeros(B, np.int32), rng.integers(0, 3, B).astype(np.int32), np.zeros(B, np.int32),
+           np.full((B, max_pages), -1, np.int32), rng.permutation(150).astype(np.int32), np.int32(150)]
+    d = [i32(x) for x in ref[:5]] + [i32([150])]
+    T_cap, R_cap = 2 * B, 2 * B
+    outs = [torch.empty(n, dtype=I32, device="cuda") for n in (T_cap, T_cap, R_cap)]
+
+    def step():
+        return ds4x.page_plan(*d, ratio, ps, T_cap, R_cap, *outs, seen_out=d[0], rows_out=d[2], n_free_out=d[5])
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        totals = step()[-1]
+    for i in range(30):
+        if i > 0:
+            g.replay()
+        want = kv4.page_plan(*ref, ratio, ps, T_cap, R_cap)
+        got = [x.cpu().numpy() for x in outs] + [d[3].cpu().numpy(), d[0].cpu().numpy(), d[2].cpu().numpy(),
+                                                 d[5].cpu().numpy()[0]]
+        check_plan(got, want)
+        if i > 0:
+            assert np.array_equal(totals.cpu().numpy(), want[-1])
+        ref[0], ref[2], ref[3], ref[5] = want[4], want[5], want[3], want[6]
+
+
+# ------------------------------------------------------------------------------------- attention
+class Pool:
+    """A pool of random rows with every page behind the requests' rows poisoned (NaN groups)."""
+
+    def __init__(self, rng, rows, ps, n_req=None, loud=1.0):
+        self.rows, self.ps = np.asarray(rows, dtype=np.int32), ps
+        B = len(self.rows)
+        held = -(-self.rows // ps)
+        self.max_pages = max(1, int(held.max(initial=0)))
+        n_pages = int(held.sum()) + 3
+        self.n_slots = n_pages * ps
+        pages = rng.permutation(n_pages)
+        self.tables = np.full((B, self.max_pages), -1, dtype=np.int32)
+        self.codes = rng.integers(0, 256, (self.n_slots, 256), dtype=np.uint8)
+        self.scales = np.full((self.n_slots, 16), 255, dtype=np.uint8)     # what nobody holds reads as NaN
+        k = 0
+        for b in range(B):
+            self.tables[b, :held[b]] = pages[k:k + held[b]]
+            k += held[b]
+            for pg in range(held[b]):
+                n = min(ps, self.rows[b] - pg * ps)
+                at = self.tables[b, pg] * ps
+                self.scales[at:at + n] = rng.integers(124, 127, (n, 16)) if loud == 1.0 else \
+                    rng.integers(127, 131, (n, 16))
+        self.dev = gpu(self.codes), gpu(self.scales), i32(self.tables), i32(self.rows)
+
+    def values(self):
+        return kv4.values(self.codes, self.scales)
+
+
+def tolerance(q, kv, out, scale, dtype):
+    """How far out [64, 512] and lse [64] of one token over rows kv [n, 512] may be.
+
+    Logits: 512 exact products summed in fp32; each of the sum's steps is off by at most 2^-23 (a
+    truncating adder) of the sum of magnitudes, and the 32 matrix steps add 16 products each; with the
+    products' own inner sums 64 steps cover it: ex = 64 * 2^-23 * scale * sum |q||kv|, plus 2^-20 for
+    2^x and its argument (2^-22 and |x| 2^-24 with |x| < 100).
+    Weights: 2 ex relative, and rounded to 16 bits (half a step of fp16, 2^-11) once, in numerator and
+    normaliser alike: a normalised weight moves by at most eta = 2 (2^-11 + 2 ex) relative, and
+    |out - ref| <= eta * sum_j w_j |kv_j - ref|.  Weights below fp16's normal range (the largest is at
+    least 2^-8 times 2^7) are off by 2^-25 absolutely, n of them against a sum of at least 2^-1.
+    The output is rounded once: half a step of its type, 2^-25 below fp16's normal range."""
+    x = (q @ kv.T) * scale
+    ex = 64 * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(kv).T).max(axis=1) + 2.0 ** -20
+    w = np.exp(x - x.max(axis=1, keepdims=True))
+    w /= w.sum(axis=1, keepdims=True)
+    spread = np.stack([w[h] @ np.abs(kv - out[h][None, :]) for h in range(q.shape[0])])
+    eta = 2 * (2.0 ** -11 + 2 * ex)
+    half = torch.finfo(DT[dtype]).eps / 2
+    tiny = kv.shape[0] * 2.0 ** -24 * np.abs(kv).max()
+    return (eta[:, None] * spread + tiny + half * np.abs(out) * 1.01 + 2.0 ** -25,
+            2 * ex + 2.0 ** -20 * (1 + np.abs(x).max(axis=1)))
+
+
+def check_attn(q, pool, got, lse, scale, dtype, lists):
+    vals = pool.values()
+    qd = q.double().cpu().numpy()
+    tabs = dict(tables=pool.tables, rows=pool.rows, page_rows=pool.ps)
+    ref, rlse = kv4.attn(qd, vals, scale, **tabs, **lists)
+    g, gl = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    for t in range(q.shape[0]):
+        at = kv4.attended_slots(t, n_slots=pool.n_slots, **tabs, **lists)
+        if not at:
+            assert np.all(g[t] == 0) and np.all(np.isneginf(gl[t])), t
+            continue
+        tol, ltol = tolerance(qd[t], vals[at], ref[t], scale, dtype)
+        assert np.all(np.isfinite(g[t])), t
+        worst = (np.abs(g[t] - ref[t]) / tol).max()
+        assert worst <= 1, (t, len(at), worst)
+        assert np.all(np.abs(gl[t] - rlse[t]) <= ltol), (t, np.abs(gl[t] - rlse[t]).max())
+
+
+def queries(rng, T, dtype, size=1.0):
+    return torch.from_numpy(rng.standard_normal((T, 64, 512)) * size).to(DT[dtype]).cuda()
+
+
+def run_attn(q, pool, scale=None, **lists):
+    kw = {k: (v if k == "ratio" or v is None else i32(v)) for k, v in lists.items()}
+    return ds4x.kv4_attn(q, *pool.dev, pool.ps, scale=scale, **kw)
+
+
+SCALE = 512 ** -0.5
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,rows,ps,k_top", [
+    (1, [700], 64, 512), (1, [40], 8, 512), (3, [65, 1, 200], 16, 64), (7, [1000] * 7, 32, 333),
+    (5, [64, 63, 65, 128, 0], 1, 100), (2, [2000, 1500], 256, 1024), (150, [300] * 150, 64, 70), (1, [1], 128, 1),
+])
+def test_attn_selected(T, rows, ps, k_top, dtype):
+    rng = np.random.default_rng(T * 7 + k_top)
+    pool = Pool(rng, rows, ps)
+    idx = np.full((T, k_top), -1, dtype=np.int32)
+    counts = np.zeros(T, dtype=np.int32)
+    for t in range(T):
+        n = min(k_top, rows[t])
+        idx[t, :n] = np.sort(rng.permutation(rows[t])[:n])
+        counts[t] = n
+    q = queries(rng, T, dtype)
+    for lists in (dict(indices=idx), dict(indices=idx, counts=counts)):
+        out, lse = run_attn(q, pool, **lists)
+        check_attn(q, pool, out, lse, SCALE, dtype, lists)
+
+
+def test_attn_selected_odd_lists():
+    """Lists with holes, repeats, rows that are not held, and rows without a page; a request that is none."""
+    rng = np.random.default_rng(4)
+    pool = Pool(rng, [150, 90, 30, 1], 16)
+    pool.tables[1, 2] = -7                                     # rows 32..47 of request 1 have no page
+    pool.tables[2, 0] = pool.n_slots // 16                     # rows 0..15 of request 2 are behind the pool
+    pool.tables[3, 0] = 2 ** 31 - 1
+    pool.dev = *pool.dev[:2], i32(pool.tables), pool.dev[3]
+    req = np.array([1, 0, 2, 0, -1, 4, 3, 1, 2 ** 31 - 1], dtype=np.int32)
+    T = len(req)
+    idx = rng.integers(-40, 200, (T, 200)).astype(np.int32)
+    idx[1] = 149                                               # one row, 200 times
+    idx[3] = -1
+    idx[7, :] = 2 ** 31 - 1
+    counts = np.array([200, 199, 65, 64, 200, 10, 200, -3, 0], dtype=np.int32)
+    q = queries(rng, T, "bf16")
+    for lists in (dict(req=req, indices=idx), dict(req=req, indices=idx, counts=counts),
+                  dict(req=req, indices=idx, counts=counts * 1000)):
+        out, lse = run_attn(q, pool, **lists)
+        check_attn(q, pool, out, lse, SCALE, "bf16", lists)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,ps,req,ratio,back", [
+    ([1], 64, [0], 1, 0), ([64], 16, [0], 4, 0), ([65], 16, [0], 4, 0), ([5000], 64, [0], 128, 0),
+    ([0, 3, 127, 128, 129, 700], 32, [0, 1, 2, 3, 4, 5], 128, 0),
+    ([300, 77], 8, [0] * 20 + [1] * 13, 4, 37), ([40], 1, [0] * 170, 1, 169),
+    ([2500, 10, 900], 128, [2, 0, 1, 0, 2], 7, 3),
+])
+def test_attn_all_visible(rows, ps, req, ratio, back, dtype):
+    rng = np.random.default_rng(len(req) * 11 + ps)
+    pool = Pool(rng, rows, ps)
+    req = np.array(req, dtype=np.int32)
+    # positions up to the last one; the first tokens may see nothing, or be before the sequence
+    positions = (np.array(rows)[req] * ratio - 1 - rng.integers(0, back + 1, len(req)) * max(1, ratio // 2)).astype(np.int32)
+    q = queries(rng, len(req), dtype)
+    for lists in (dict(req=req, positions=positions, ratio=ratio), dict(req=req)):
+        out, lse = run_attn(q, pool, **lists)
+        check_attn(q, pool, out, lse, SCALE, dtype, lists)
+
+
+def test_attn_request_of_a_token_is_its_number():
+    rng = np.random.default_rng(12)
+    pool = Pool(rng, [10, 200, 64], 64)
+    q = queries(rng, 2, "f16")
+    out, lse = run_attn(q, pool)
+    check_attn(q, pool, out, lse, SCALE, "f16", {})
+    none = Pool(rng, [0, 0], 8)
+    out, lse = run_attn(q, none)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size,loud", [(1e-4, 1.0), (30.0, 1.0), (1.0, 8.0), (60.0, 8.0)])
+def test_attn_small_and_large_logits(size, loud, dtype):
+    """Uniform weights, and one row that takes all: the running maximum has to move, late rows included."""
+    rng = np.random.default_rng(int(size * 10))
+    pool = Pool(rng, [900, 333], 32, loud=loud)
+    q = queries(rng, 2, dtype, size)
+    q[0, 0] = 0
+    q[0, 1, 1:] = 0
+    # the row with the largest logit of some heads comes last
+    q[1, 5] = torch.from_numpy(pool.values()[kv4.attended_slots(1, pool.tables, pool.rows, 32, pool.n_slots)[-1]]).to(DT[dtype])
+    lists = dict(req=np.array([0, 1], dtype=np.int32))
+    out, lse = run_attn(q, pool, **lists)
+    check_attn(q, pool, out, lse, SCALE, dtype, lists)
+
+
+def test_attn_extreme_queries():
+    """bf16 queries beyond fp16's range, heads of very different sizes."""
+    rng = np.random.default_rng(77)
+    pool = Pool(rng, [130, 64], 16)
+    q = queries(rng, 2, "bf16")
+    for h, e in enumerate(range(-100, 100, 4)):
+        q[:, h] *= 2.0 ** e
+    q[0, 50], q[1, 51, ::2] = 0, 2.0 ** -126
+    for scale in (SCALE, 2.0 ** -96, -0.02):
+        lists = dict(req=np.array([0, 1], dtype=np.int32))
+        out, lse = run_attn(q, pool, scale=scale, **lists)
+        qd, vals = q.double().cpu().numpy(), pool.values()
+        tabs = dict(tables=pool.tables, rows=pool.rows, page_rows=16)
+        ref, rlse = kv4.attn(qd, vals, scale, **tabs, **lists)
+        for t in range(2):
+            at = kv4.attended_slots(t, n_slots=pool.n_slots, **tabs, **lists)
+            x = (qd[t] @ vals[at].T) * scale
+            size = abs(scale) * (np.abs(qd[t]) @ np.abs(vals[at]).T).max(axis=1)
+            calm = size < 2000                 # beyond, fp32 logits do not decide between near rows
+            tol, ltol = tolerance(qd[t], vals[at], ref[t], abs(scale), "bf16")
+            g = out[t].double().cpu().numpy()
+            assert np.all(np.abs(g - ref[t])[calm] <= tol[calm])
+            assert np.all(np.abs(lse[t].double().cpu().numpy() - rlse[t])[calm] <= ltol[calm])
+            assert np.isfinite(g[np.abs(x).max(axis=1) < 1e30]).all()
+
+
+def test_attn_nan_rows_reach_only_those_who_attend():
+    rng = np.random.default_rng(31)
+    pool = Pool(rng, [100, 100], 16)
+    bad = int(pool.tables[0, 2]) * 16 + 5                     # row 37 of request 0
+    pool.scales[bad, 3] = 255
+    pool.dev = pool.dev[0], gpu(pool.scales), *pool.dev[2:]
+    q = queries(rng, 3, "f16")
+    idx = np.stack([np.arange(100), np.arange(100), np.arange(100)]).astype(np.int32)
+    idx[1, 37] = -1
+    req = np.array([0, 0, 1], dtype=np.int32)
+    out, lse = run_attn(q, pool, req=req, indices=idx)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.isfinite(out[1:]).all() and torch.isfinite(lse[1:]).all()
+
+
+def test_attn_outputs_streams_and_neighbours():
+    """Into slices of larger buffers, on another stream, without lse; what lies around stays."""
+    rng = np.random.default_rng(6)
+    pool = Pool(rng, [500, 70, 9], 32)
+    req = np.array([0, 2, 1, 0, 1], dtype=np.int32)
+    q = queries(rng, 5, "bf16")
+    want, wlse = run_attn(q, pool, req=req)
+    big = torch.full((9, 64, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    blse = torch.full((9, 64), 3.0, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ds4x.kv4_attn(q, *pool.dev, 32, req=i32(req), out=big[2:7], lse=blse[2:7], stream=s)
+    only, none = ds4x.kv4_attn(q, *pool.dev, 32, req=i32(req), want_lse=False, stream=s.cuda_stream)
+    s.synchronize()
+    assert none is None and torch.equal(only, want)
+    assert torch.equal(big[2:7], want) and torch.equal(blse[2:7], wlse)
+    assert (big[:2] == 3).all() and (big[7:] == 3).all() and (blse[:2] == 3).all() and (blse[7:] == 3).all()
+
+
+def test_attn_two_graphs_share_a_workspace():
+    rng = np.random.default_rng(8)
+    pool = Pool(rng, [3000, 40, 600], 64)
+    need = ds4x.kv4_attn_workspace_bytes(6, pool.max_pages * 64)
+    ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")   # nothing is read before it is written
+    cases = []
+    for req in ([0], [1, 2, 0, 0, 2, 1]):
+        q, r = queries(rng, len(req), "f16"), i32(req)
+        want = ds4x.kv4_attn(q, *pool.dev, 64, req=r)
+        out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ds4x.kv4_attn(q, *pool.dev, 64, req=r, out=out, lse=lse, workspace=ws)
+        cases.append((g, q, r, want, out, lse))
+    for k in (0, 1, 1, 0, 1):
+        g, _, _, want, out, lse = cases[k]
+        out.zero_(), lse.zero_()
+        g.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_attn_is_the_same_twice_and_per_token():
+    """Same bits on every run; a token's result is near that of the token alone."""
+    rng = np.random.default_rng(13)
+    pool = Pool(rng, rng.integers(1, 1500, 40), 32)
+    req = rng.integers(0, 40, 333).astype(np.int32)
+    q = queries(rng, 333, "f16")
+    out, lse = run_attn(q, pool, req=req)
+    for _ in range(3):
+        o2, l2 = run_attn(q, pool, req=req)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    for t in (0, 100, 332):
+        o1, l1 = run_attn(q[t:t + 1].clone(), pool, req=req[t:t + 1])
+        # two results within the tolerance each; unit-size values, far from it in practice
+        assert (o1[0].float() - out[t].float()).abs().max() < 4e-3
+        assert (l1[0] - lse[t]).abs().max() < 1e-4
+
+
+def test_attn_many_tokens():
+    """More tokens than one launch plans for; sampled against the plain form."""
+    rng = np.random.default_rng(21)
+    pool = Pool(rng, rng.integers(0, 90, 50), 16)
+    T = 5003
+    req = rng.integers(-1, 51, T).astype(np.int32)
+    q = queries(rng, 64, "bf16").repeat((T + 63) // 64, 1, 1)[:T].contiguous()
+    out, lse = run_attn(q, pool, req=req)
+    some = np.unique(np.concatenate([rng.integers(0, T, 40), [0, 2047, 2048, 2049, 4095, 4096, T - 1]]))
+    check_attn(q[some], pool, out[some], lse[some], SCALE, "bf16", dict(req=req[some]))
+
+
+# ------------------------------------------------------------------------------ a run of them all
+def test_serving_steps_end_to_end():
+    """Steps of a batch as a server runs them: plan, compress, append, score and top-k, attention; the
+    16-bit path over the rows read back gives the same."""
+    rng = np.random.default_rng(40)
+    B, ratio, ps, max_pages, k_top = 3, 4, 16, 12, 24
+    lens = [(50, 300, 7), (1, 1, 1), (3, 0, 200), (1, 1, 1)]
+    dev = "cuda"
+    seen, rows = i32([0] * B), i32([0] * B)
+    tables, free, n_free = i32(np.full((B, max_pages), -1)), i32(rng.permutation(40)), i32([40])
+    pool = (torch.zeros((40, ps, 256), dtype=torch.uint8, device=dev), torch.zeros((40, ps, 16), dtype=torch.uint8, device=dev))
+    k_rows = [torch.zeros((max_pages * ps, 128), dtype=torch.float16, device=dev) for _ in range(B)]
+    frontier = [(None, None)] * B
+    kv_all = [[] for _ in range(B)]
+    bias = torch.zeros((ratio, 512), device=dev)
+    for new in lens:
+        T = sum(new)
+        R_cap = T // ratio + B
+        before = rows.cpu().tolist()
+        positions, req, slots, seen, rows, n_free, totals = ds4x.page_plan(
+            seen, i32(new), rows, tables, free, n_free, ratio, ps, T, R_cap)
+        at = 0
+        for b in range(B):
+            x, g = (torch.from_numpy(rng.standard_normal((new[b], 512))).to(torch.bfloat16).cuda() for _ in range(2))
+            out, fx, fg = ds4x.compress(x, g, bias, ratio, *frontier[b]) if new[b] else (x, *frontier[b])
+            frontier[b] = (fx, fg) if fx is not None and fx.shape[0] else (None, None)
+            n = out.shape[0]
+            ds4x.kv4_append(out, slots[at:at + n], *pool)
+            k_rows[b][before[b]:before[b] + n] = torch.from_numpy(rng.standard_normal((n, 128))).half().cuda()
+            kv_all[b].append(out)
+            at += n
+        held = rows.cpu().tolist()
+        assert totals.cpu().tolist()[:3] == [T, at, at]
+        q = queries(rng, T, "bf16")
+        qi = torch.from_numpy(rng.standard_normal((T, 16, 128))).half().cuda()
+        w = torch.from_numpy(rng.random((T, 16))).half().cuda()
+        idx = torch.empty((T, k_top), dtype=I32, device=dev)
+        counts = torch.empty((T,), dtype=I32, device=dev)
+        t0 = 0
+        for b in range(B):                                   # scores and top-k of each request's tokens
+            if new[b] == 0:
+                continue
+            sl = slice(t0, t0 + new[b])
+            S = max(1, held[b])
+            p = positions[sl].clone()
+            sc = ds4x.indexer_score(qi[sl].clone(), w[sl].clone(), k_rows[b], p, ratio, S=S)
+            i, c = ds4x.topk(sc, p, min(S, held[b]) if held[b] else 0, ratio, k_top) if held[b] else \
+                (torch.full((new[b], k_top), -1, dtype=I32, device=dev), torch.zeros(new[b], dtype=I32, device=dev))
+            idx[sl], counts[sl] = i, c
+            t0 += new[b]
+        for lists in (dict(indices=idx, counts=counts), dict(positions=positions, ratio=ratio)):
+            out, lse = ds4x.kv4_attn(q, *pool, tables, rows, ps, req=req, **lists)
+            t0 = 0
+            for b in range(B):
+                if new[b] == 0:
+                    continue
+                r = torch.arange(max(1, held[b]), device=dev)
+                own = tables[b][r // ps] * ps + r.int() % ps
+                kv = ds4x.kv4_read(*pool, own.int(), torch.bfloat16)
+                if held[b]:
+                    c, s = kv4.quantise(torch.cat(kv_all[b]).double().cpu().numpy())
+                    assert np.array_equal(kv.double().cpu().numpy(), kv4.values(c, s))
+                sl = slice(t0, t0 + new[b])
+                if "indices" in lists:
+                    i16 = idx[sl].clone()
+                else:
+                    n = (positions[sl] + 1) // ratio
+                    i16 = torch.where(torch.arange(192, device=dev)[None, :] < n[:, None], torch.arange(192, device=dev)[None, :], -1).int()
+                ref, rlse = ds4x.sparse_attn(q[sl].clone(), kv, i16, S=held[b])
+                # the 16-bit path rounds its weights to bf16 (2^-8, values below 6): 2 * 2^-8 * 6
+                assert (out[sl].float() - ref.float()).abs().max() <= 0.05
+                fin = torch.isfinite(rlse)
+                assert torch.equal(fin, torch.isfinite(lse[sl]))
+                assert (lse[sl][fin] - rlse[fin]).abs().max() <= 2.0 ** -7 if fin.any() else True
+                t0 += new[b]
