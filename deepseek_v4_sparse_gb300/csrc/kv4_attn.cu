@@ -5,9 +5,9 @@
 // over the rows j that a token selected (indices) or over every row of its request that it can see.
 //
 // The products run on the tensor cores in fp16, whatever the type of q: a row's values (code times a
-// power of two, kv4_common.cuh) are exact in fp16, q is made so by a power of two a head (which moves its
-// largest magnitude to [2^14, 2^15); what falls below fp16's range then is under 2^-39 of the largest),
-// and the softmax weights keep eleven bits instead of bf16's eight.
+// power of two, kv4_common.cuh) are exact in fp16, a bf16 q is made so by a power of two a head (which
+// moves its largest magnitude to [2^14, 2^15); what is under 2^-28 of the largest reads as 0), and the
+// softmax weights keep eleven bits instead of bf16's eight.
 //
 // One block an SM.  The tokens' rows are cut into chunks of 64; all chunks of all tokens form one
 // sequence, and each block takes an equal, contiguous part of it.  A token whose chunks lie in several
@@ -17,16 +17,29 @@
 //   O^T [512 x 64 heads]    += V^T . P^T     tcgen05, M = 128 (dims), A MN-major, B K-major
 // with K = V = the chunk, decoded once into 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
 //
-// Warps: 0-7 fetch and decode rows, 8-11 softmax (heads 16*(warp-8) .. +15, 4 threads a head), 12-15
-// convert q and write the output (O^T lanes by quadrant), 16 issues the S products, 17 the O^T products.
-// A fetching thread owns 32 values (one scale group) of a row in each quarter of the dims: the codes of
-// the next chunk are in its registers while it decodes this one, the table entries of the one after and
-// the indices of the third are on their way.  Buffers are released in quarters, O^T rotates over six
-// 64-column TMEM slots (a token uses four), so neighbouring tokens overlap.
+// Warps: 0-15 fetch and decode rows and convert q, 16-19 softmax (heads 16*(warp-16) .. +15, 4 threads a
+// head), 20-23 write the output (O^T lanes by quadrant), 24 issues the S products, 25 the O^T products,
+// 26 looks up the rows' slots a few chunks ahead.  A fetching thread owns 32 values (one scale group) of
+// two rows: it decodes the chunk into registers, has the codes of the next one on their way and then waits
+// for the buffer.  Buffers are released in halves of the dims, O^T rotates over six 64-column TMEM slots
+// (a token uses four), so neighbouring tokens overlap.  q of a token goes in before its first chunk is
+// decoded: the fetching warps wait for a buffer then, and have it converted when the products of the token
+// before are done with theirs.  It is brought to L2 an item ahead.
 //
-// The running maximum of a head moves only when a logit exceeds it by more than 2^8 (O^T's column and
-// the sums are rescaled then); weights are 2^7 times 2^(x - m), which keeps them below fp16's largest
-// value and small ones away from its least.  Statistics and sums are fp32.
+// What bounds it: the data path of L1 and shared memory, one 128-byte access a clock for the products and
+// the warps together.  A chunk of a 2048-token prefill takes 1790 accesses of the products (128 KB of S
+// operands, 96 KB of O^T operands) and 1890 of the warps (512 of them the decoded stores), 92 % of its
+// time: 224 us for 2048 tokens of 512 rows (613 TFLOP/s, 32 % of the measured peak; a gather that reads a
+// row's codes in 16 lines instead of whole 128-byte lines, and looks the slots up in every warp: 247 us).
+// Three buffers of 48 rows, a shorter chain a chunk but a third more S time a row, took 272 us.
+//
+// The running maximum of a head moves only when a logit exceeds it by more than 2^11 (O^T's column and
+// the sums are rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them
+// below fp16's largest value and small ones away from its least.  Statistics and sums are fp32.
+//
+// The roles share the SM's instruction caches: every loop that need not be unrolled for its registers is
+// kept rolled, and the waits' failure path is short.  (Unrolled throughout, the kernel was 152 KB of code
+// and a 2048-token chunk took 377 us, a third of the warps' time waiting for instructions.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,31 +56,38 @@ constexpr int kHq = 64;
 constexpr int kRows = 64;                        // rows per chunk
 constexpr int kSlots = kKv4Dim / 64;             // 8 slots of 64 dims
 constexpr int kPairs = kSlots / 2;               // quarters of 128 dims
+constexpr int kHalves = 2;                       // of the dims: what is fetched and released together
 constexpr int kSlotBytes = kRows * 128;          // 8 KB
 constexpr int kBufBytes = kSlots * kSlotBytes;   // 64 KB a chunk
 constexpr int kQBlockBytes = kHq * 128;          // 8 KB (64 heads x 64 dims)
 constexpr int kQBytes = kSlots * kQBlockBytes;   // 64 KB
 constexpr int kPBytes = kHq * 128;               // 8 KB: P[h][j]
 constexpr int kTokens = 2048;                    // tokens a launch plans for
-constexpr int kDecWarps = 8, kSoftWarp = 8, kOutWarp = 12, kSWarp = 16, kOWarp = 17;
-constexpr int kWarps = 18, kThreads = 32 * kWarps;
+constexpr int kDecWarps = 16, kSoftWarp = 16, kOutWarp = 20, kSWarp = 24, kOWarp = 25, kSlotWarp = 26;
+constexpr int kWarps = 28, kThreads = 32 * kWarps;  // whole warpgroups; the last warp only takes part in the scan
+// registers a thread: 72 at launch; the sum over the seven warpgroups stays what it was
+constexpr int kLaunchRegs = 72, kDecRegs = 72, kMmaRegs = 40, kSoftRegs = 88, kOutRegs = 80;
+static_assert(kThreads * kLaunchRegs <= 65536 && 4 * kDecRegs + kMmaRegs + kSoftRegs + kOutRegs <= 7 * kLaunchRegs, "registers");
+constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
+constexpr int kItems = 4;                        // items whose logit factors are kept
 constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
 constexpr int kOffP = kOffKV + 2 * kBufBytes;
 constexpr int kOffAlpha = kOffP + 2 * kPBytes;   // float[64]: rescale factors of one chunk
 constexpr int kOffLM = kOffAlpha + kHq * 4;      // float[2 items][4][64]: sum of rounded weights, sum, m, 1 / first
-constexpr int kOffCq = kOffLM + 2 * 4 * kHq * 4; // float[2 items][2][64]: logit factor, q factor of a head
-constexpr int kOffRows = kOffCq + 2 * 2 * kHq * 4;  // int[kTokens]: rows of each token's list
-constexpr int kOffMask = kOffRows + kTokens * 4; // uint16[2 buffers][4]: rows of the chunk that count
-constexpr int kOffScan = kOffMask + 16;          // int64[18] warp sums, then int[4]: the block's part
-constexpr int kOffBars = kOffScan + 18 * 8 + 16;
-constexpr int kNumBars = 2 * kPairs + 2 * 2 * kPairs + 4 * 2 + 2 * kOSlots + 2 * 2;
+constexpr int kOffCq = kOffLM + 2 * 4 * kHq * 4; // float[kItems][64]: logit factor of a head
+constexpr int kOffRows = kOffCq + kItems * kHq * 4;  // int[kTokens]: rows of each token's list
+constexpr int kOffMask = kOffRows + kTokens * 4; // uint32[kMaskRing][2]: rows of the chunk that count
+constexpr int kOffSlots = kOffMask + kMaskRing * 8;  // int[kRing][64]: slot of each row of the chunk, -1 for none
+constexpr int kOffScan = kOffSlots + kRing * kRows * 4;         // int64[kWarps] warp sums, then int[4]: the block's part
+constexpr int kOffBars = kOffScan + kWarps * 8 + 16;
+constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 4 * 2 + 2 * kOSlots + 2 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kColO = 128;  // S in columns [0, 128), O^T from 128
-constexpr float kRescaleLog2 = 8.0f, kWeightLog2 = 7.0f;
-constexpr int kSoftBar = 1, kEpiBar = 2, kGroupThreads = 128;
+constexpr float kRescaleLog2 = 11.0f, kWeightLog2 = 4.0f;
+constexpr int kSoftBar = 1, kGroupThreads = 128;
 constexpr int kPartFloats = kHq * kKv4Dim;        // unnormalised sums of a part, then its statistics
 constexpr int kStatFloats = 3 * kHq;              // sum of rounded weights, sum, m
 
@@ -85,6 +105,34 @@ struct Params {
   float scale;
 };
 
+// Bounded waits.  A try suspends the thread for up to a microsecond, so the limit lies between a tenth of
+// a second and a few seconds.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* status, int site) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < (1 << 22); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  report_timeout(status, site);
+  return false;
+}
+// The same outcome in every lane of the (converged) warp.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, int* status, int site) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, site));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ int request_of(const Params& p, int t) { return p.req ? __ldg(p.req + t) : p.t0 + t; }
 
 // Rows in the list of token t (selected: list entries; else visible rows).
@@ -95,43 +143,50 @@ __device__ __forceinline__ int token_rows(const Params& p, int t) {
   const int held = min(max(__ldg(p.rows + b), 0), p.max_pages << p.log_page);
   if (!p.positions) return held;
   const int pos = __ldg(p.positions + t);
-  return pos < 0 ? 0 : (int)min((int64_t)held, ((int64_t)pos + 1) / p.ratio);
+  return pos < 0 ? 0 : (int)min((uint32_t)held, ((uint32_t)pos + 1u) / (uint32_t)p.ratio);
 }
 __device__ __forceinline__ int chunks_of(int rows) { return rows > kRows ? (rows - 1) / kRows + 1 : 1; }
 
-// A block's part of the chunk sequence, walked token by token: chunks [c0, c1) of token t.
+// A block's part of the chunk sequence, walked token by token: chunks [c0, c1) of token t.  What is read
+// from shared memory goes through a warp reduction, whose result is a uniform register: the loops over it
+// are then known to be the same in every lane, and the issuing warps' operands stay in such registers.
 struct Walk {
   int t, c0, c1, left;
   const int* rows;
-  __device__ __forceinline__ Walk(const int* rows_s, const int* start) : t(start[0]), c0(start[1]), left(start[2]), rows(rows_s) {
-    c1 = left > 0 ? min(chunks_of(rows[t]), c0 + left) : c0;
+  __device__ __forceinline__ static int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+  __device__ __forceinline__ Walk(const int* rows_s, const int* start)
+      : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), rows(rows_s) {
+    c1 = left > 0 ? min(chunks_of(uniform(rows[t])), c0 + left) : c0;
   }
   __device__ __forceinline__ void next() {
     left -= c1 - c0;
     ++t;
     c0 = 0;
-    c1 = left > 0 ? min(chunks_of(rows[t]), left) : 0;
+    c1 = left > 0 ? min(chunks_of(uniform(rows[t])), left) : 0;
   }
 };
 
 template <bool kBf16>
-__device__ __forceinline__ uint16_t to16(float x) {
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
   if constexpr (kBf16) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    return *reinterpret_cast<const uint16_t*>(&h);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const __half h = __float2half_rn(x);
-    return *reinterpret_cast<const uint16_t*>(&h);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// Two 16-bit values as fp32, times f, as fp16.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t scaled2(uint32_t u, float f) {
-  float2 v;
-  if constexpr (kBf16) v = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  else v = __half22float2(*reinterpret_cast<const __half2*>(&u));
-  const __half2 h = __floats2half2_rn(v.x * f, v.y * f);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Two bf16 values as fp16, their exponents lowered by the head's offset (twice in `bias`, in place): what
+// falls to fp16's least exponent or below it is at most 2^-28 of the head's largest magnitude.
+__device__ __forceinline__ uint32_t bf16_to_fp16(uint32_t u, uint32_t bias) {
+  const uint32_t a = __vmaxu2(u & 0x7fff7fffu, bias);
+  return (a * 8u - bias * 8u) | (u & 0x80008000u);
+}
+// r + the two halves of v
+__device__ __forceinline__ void add_halves(float& r, __half2 v) {
+  const __half_raw lo = __low2half(v), hi = __high2half(v);
+  asm("add.f32.f16 %0, %1, %0;" : "+f"(r) : "h"(lo.x));
+  asm("add.f32.f16 %0, %1, %0;" : "+f"(r) : "h"(hi.x));
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), s);
@@ -154,14 +209,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
   float* lm = reinterpret_cast<float*>(smem + kOffLM);
   float* cq = reinterpret_cast<float*>(smem + kOffCq);
   int* rows_s = reinterpret_cast<int*>(smem + kOffRows);
-  uint16_t* mask_s = reinterpret_cast<uint16_t*>(smem + kOffMask);
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + kOffMask);
+  int* slot_s = reinterpret_cast<int*>(smem + kOffSlots);
   long long* scan = reinterpret_cast<long long*>(smem + kOffScan);
-  int* start = reinterpret_cast<int*>(smem + kOffScan + 18 * 8);
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + kOffBars);  // [quarter]
-  uint64_t* qempty = qfull + kPairs;        // [quarter]
-  uint64_t* kvfull = qempty + kPairs;       // [buffer][quarter]
-  uint64_t* kvempty = kvfull + 2 * kPairs;  // [buffer][quarter]
-  uint64_t* sfull = kvempty + 2 * kPairs;
+  int* start = reinterpret_cast<int*>(smem + kOffScan + kWarps * 8);
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + kOffBars);
+  uint64_t* qempty = qfull + 1;
+  uint64_t* slfull = qempty + 1;            // [ring] slots of a chunk
+  uint64_t* slempty = slfull + kRing;
+  uint64_t* kvfull = slempty + kRing;       // [buffer][half]
+  uint64_t* kvempty = kvfull + 2 * kHalves; // [buffer][half]
+  uint64_t* sfull = kvempty + 2 * kHalves;
   uint64_t* sempty = sfull + 2;
   uint64_t* pfull = sempty + 2;
   uint64_t* pempty = pfull + 2;
@@ -175,12 +233,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
   auto oslot = [](uint32_t item, int db) { return (int)((4u * (item % 3u) + (uint32_t)db) % kOSlots); };
 
   if (tid == 0) {
-    for (int i = 0; i < kPairs; ++i) {
-      mbar_init(&qfull[i], 4);
-      mbar_init(&qempty[i], 1);
+    mbar_init(qfull, kDecWarps);
+    mbar_init(qempty, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&slfull[i], 1);
+      mbar_init(&slempty[i], kDecWarps);
     }
-    for (int i = 0; i < 2 * kPairs; ++i) {
-      mbar_init(&kvfull[i], kDecWarps);
+    for (int i = 0; i < 2 * kHalves; ++i) {
+      mbar_init(&kvfull[i], kDecWarps / 2);
       mbar_init(&kvempty[i], 1);
     }
     for (int i = 0; i < kOSlots; ++i) {
@@ -203,18 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
 
   // --------------------------------------------------- every token's rows; this block's part
   {
-    constexpr int kPer = (kTokens + kThreads - 1) / kThreads;
     const int per = (p.T + kThreads - 1) / kThreads;
-    int n[kPer];
+    const int first = tid * per, last = min(first + per, p.T);
     long long sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = tid * per + i;
-      n[i] = (i < per && t < p.T) ? token_rows(p, t) : -1;
-      if (n[i] >= 0) {
-        rows_s[t] = n[i];
-        sum += chunks_of(n[i]);
-      }
+#pragma unroll 1
+    for (int t = first; t < last; ++t) {
+      const int n = token_rows(p, t);
+      rows_s[t] = n;
+      sum += chunks_of(n);
     }
     long long incl = sum;
 #pragma unroll
@@ -226,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     if (tid == 0) start[2] = 0;
     __syncthreads();
     long long before = incl - sum, total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       const long long v = scan[w];
       if (w < warp) before += v;
@@ -236,15 +292,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     const long long g0 = quota * blockIdx.x, g1 = min(total, g0 + quota);
     if (g0 < total) {
       long long at = before;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (n[i] < 0) continue;
-        const int nch = chunks_of(n[i]);
+#pragma unroll 1
+      for (int t = first; t < last; ++t) {
+        const int nch = chunks_of(rows_s[t]);
         if (at <= g0 && g0 < at + nch) {
-          start[0] = tid * per + i;
+          start[0] = t;
           start[1] = (int)(g0 - at);
           start[2] = (int)(g1 - g0);
-          p.parts_of[blockIdx.x] = make_int4(tid * per + i, (int)(g0 - at), nch, (int)quota);
+          p.parts_of[blockIdx.x] = make_int4(t, (int)(g0 - at), nch, (int)quota);
         }
         at += nch;
       }
@@ -259,168 +314,230 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
 
   if (warp < kDecWarps) {
     // --------------------------------------------------------------------- fetch and decode
-    // row 16 (warp % 4) + lane % 16 of the chunk; in each quarter of the dims the 32 values of slot
-    // warp / 4, half lane / 16.  Eight neighbouring lanes store to eight rows of one 16-byte column:
-    // the swizzle puts them in different banks; the two halves of a row share its 32-byte sectors.
-    const int r = 16 * (warp & 3) + (lane & 15);
-    const int sub = 2 * (warp >> 2) + (lane >> 4);  // group within a quarter
+    // the dims' half warp / 8 of rows 8 (warp % 8) .. + 7 of the chunk, four rows at a time: lane / 8 the row,
+    // lane % 8 the group of 32.  Eight neighbouring lanes read a 128-byte line and store, in step k, the
+    // 16-byte columns k ^ slot of their groups: four slots by two groups, all in different banks.
+    const int half = warp >> 3, lr = lane >> 3, gi = lane & 7;
+    const int ss = gi >> 1;                     // slot of 64 dims within the half
+    // step k of the first row; of the second, 4 rows on: ^ 64, + 512
     uint32_t st_off[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      st_off[k] = (uint32_t)((warp >> 2) * kSlotBytes + r * 128 + ((((lane >> 4) * 4 + k) ^ (r & 7)) << 4));
-    const bool listed = p.indices != nullptr;
-    // cursor: the next chunk whose row number is to be fetched
-    int t = start[0], c = start[1], left = start[2];
-    int row_a = -1, b_a = 0;                       // stage a: row number and request on their way
-    int row_b = -1, page_b = -1, held_b = 0;       // stage b: table entry (and rows held) on their way
-    auto fetch_row = [&]() {
-      row_a = -1;
-      if (left > 0) {
-        const int j = c * kRows + r, n = rows_s[t];
-        b_a = request_of(p, t);
-        if (j < n) row_a = listed ? __ldg(p.indices + (int64_t)t * p.k_top + j) : j;
-        --left;
-        if (++c >= chunks_of(n)) {
-          c = 0;
-          ++t;
+      st_off[k] = smem_u32(skv) + (uint32_t)((4 * half + ss) * kSlotBytes + (8 * (warp & 7) + lr) * 128 +
+                                             ((((gi & 1) * 4 + (k ^ ss)) ^ lr) << 4));
+    const uint8_t* codes = p.codes + half * 128 + gi * 16;
+    const uint8_t* scales = p.scales + half * 8 + gi;
+    uint4 d[2];
+    uint32_t sc[2];
+    // codes and scales of chunk x: a row without a slot reads slot 0 with a scale of 0
+    auto load = [&](uint32_t x) {
+      const bool got = wait_bar_warp(&slfull[x % kRing], (x / kRing) & 1, p.status, 60);
+      const int* sl = slot_s + (x % kRing) * kRows + 8 * (warp & 7) + lr;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = sl[4 * i];
+        d[i] = make_uint4(0, 0, 0, 0);
+        sc[i] = 0;
+        if (p.n_slots > 0) {
+          d[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)max(at, 0) * kKv4CodeBytes));
+          sc[i] = at < 0 ? 0u : __ldg(scales + (int64_t)at * kKv4ScaleBytes);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&slempty[x % kRing]);
+      return got;
     };
-    auto fetch_page = [&]() {
-      row_b = row_a;
-      page_b = -1;
-      if (row_a >= 0 && (row_a >> p.log_page) < p.max_pages) {
-        page_b = __ldg(p.tables + (int64_t)b_a * p.max_pages + (row_a >> p.log_page));
-        held_b = listed ? __ldg(p.rows + b_a) : 0x7fffffff;
+    // q of token t as fp16 into the operand's layout; each warp 4 heads, 16-byte units lane and lane + 32
+    auto put_q = [&](int qt, uint32_t qi) {
+      const int h = warp * 4;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qt * kHq + h) * kKv4Dim) + lane;
+      uint4 u[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u[i][0] = __ldg(src + i * (kKv4Dim / 8));
+        u[i][1] = __ldg(src + i * (kKv4Dim / 8) + 32);
       }
-    };
-    const uint8_t* src = nullptr;   // codes of the chunk to load next; nullptr: the row does not count
-    uint4 d[kPairs], sc = make_uint4(0, 0, 0, 0);
-    auto resolve = [&]() {
-      const int64_t slot = ((int64_t)page_b << p.log_page) + (row_b & ((1 << p.log_page) - 1));
-      const bool ok = page_b >= 0 && slot < p.n_slots && row_b < held_b;
-      src = ok ? p.codes + slot * kKv4CodeBytes + sub * 16 : nullptr;
-      return ok ? p.scales + slot * kKv4ScaleBytes : nullptr;
-    };
-    auto load_quarter = [&](int pr) {
-      d[pr] = src ? __ldg(reinterpret_cast<const uint4*>(src + pr * 64)) : make_uint4(0, 0, 0, 0);
-    };
-    const int chunks = left;
-    fetch_row();
-    fetch_page();
-    fetch_row();
-    {
-      const uint8_t* s = resolve();
-      sc = s ? __ldg(reinterpret_cast<const uint4*>(s)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int pr = 0; pr < kPairs; ++pr) load_quarter(pr);
-    }
-    bool live = src != nullptr;
-    fetch_page();
-    fetch_row();
-    bool ok = true;
-    for (int g = 0; g < chunks && ok; ++g) {
-      const int b = g & 1;
-      const uint32_t ph = ((g >> 1) & 1) ^ 1;
-      const uint8_t* s_next = resolve();  // of chunk g + 1
-      const bool live_next = src != nullptr;
-      const uint4 sc_now = sc;
-      sc = s_next ? __ldg(reinterpret_cast<const uint4*>(s_next)) : make_uint4(0, 0, 0, 0);
-      fetch_page();  // of g + 2
-      fetch_row();   // of g + 3
-      const uint32_t live_bits = __ballot_sync(0xffffffffu, live);
-      const uint32_t base = smem_u32(skv) + b * kBufBytes;
+      for (int i = 0; i < 4; ++i) {
+        float f = p.scale * 1.4426950408889634f;
+        if constexpr (kBf16) {
+          // a head's exponent offset, from its largest magnitude (compared as bits); a logit in log2
+          // units is the product times scale log2(e) 2^(offset - 112)
+          uint32_t m = 0;
 #pragma unroll
-      for (int pr = 0; pr < kPairs; ++pr) {
-        const uint4 now = d[pr];
-        load_quarter(pr);
-        const uint32_t word = pr == 0 ? sc_now.x : pr == 1 ? sc_now.y : pr == 2 ? sc_now.z : sc_now.w;
-        const __half2 s2 = __float2half2_rn(kv4_scale((word >> (8 * sub)) & 255u));
-        if (!mbar_wait(&kvempty[b * kPairs + pr], ph, p.status, 61)) {
-          ok = false;
-          break;
+          for (int k = 0; k < 2; ++k)
+            m = __vmaxu2(__vmaxu2(__vmaxu2(m, u[i][k].x & 0x7fff7fffu), __vmaxu2(u[i][k].y & 0x7fff7fffu, u[i][k].z & 0x7fff7fffu)),
+                         u[i][k].w & 0x7fff7fffu);
+          const uint32_t ex = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) >> 7;
+          // the largest exponent field becomes 29; infinities and NaN stay what they are (field 31)
+          const uint32_t off = ex == 255u ? 224u : ex > 29u ? ex - 29u : 0u;
+          const uint32_t bias = (off << 7) | (off << 23);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            u[i][k] = make_uint4(bf16_to_fp16(u[i][k].x, bias), bf16_to_fp16(u[i][k].y, bias),
+                                 bf16_to_fp16(u[i][k].z, bias), bf16_to_fp16(u[i][k].w, bias));
+          f *= __uint_as_float((off + 15u) << 23);
         }
-        if (pr == 0 && warp < 4 && lane == 0) mask_s[b * 4 + warp] = (uint16_t)live_bits;
-        const uint32_t w4[4] = {now.x, now.y, now.z, now.w};
+        if (lane == 0) cq[(qi % kItems) * kHq + h + i] = f;
+      }
+      const bool got = wait_bar_warp(qempty, (qi & 1) ^ 1, p.status, 71);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint8_t* dst = sq + (lane >> 3) * kQBlockBytes + (h + i) * 128 + (((lane & 7) ^ ((h + i) & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = u[i][0];
+        *reinterpret_cast<uint4*>(dst + 4 * kQBlockBytes) = u[i][1];
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull);
+      return got;
+    };
+    const uint32_t chunks = start[2];
+    bool ok = chunks == 0 || load(0);
+    uint32_t g = 0, item = 0;
+    for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
+      ok = put_q(w.t, item);
+#pragma unroll 1
+      for (int ci = w.c0; ci < w.c1 && ok; ++ci, ++g) {
+        const int b = g & 1;
+        uint32_t v[2][16];  // decoded before the buffer is free
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __half2 s2 = __float2half2_rn(kv4_scale(sc[i]));
+          // word k ^ slot of the group in step k
+          const bool s0 = ss & 1, s1 = ss & 2;
+          const uint32_t a0 = s0 ? d[i].y : d[i].x, a1 = s0 ? d[i].x : d[i].y;
+          const uint32_t a2 = s0 ? d[i].w : d[i].z, a3 = s0 ? d[i].z : d[i].w;
+          const uint32_t w4[4] = {s1 ? a2 : a0, s1 ? a3 : a1, s1 ? a0 : a2, s1 ? a1 : a3};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            kv4_decode8(w4[k], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][4 * k + e] = mul2(h[e], s2);
+          }
+        }
+        if (g + 1 < chunks) ok = load(g + 1);
+        ok = ok && wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 61);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t h[4];
-          kv4_decode8(w4[k], h);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + 2 * pr * kSlotBytes + st_off[k]),
-                       "r"(mul2(h[0], s2)), "r"(mul2(h[1], s2)), "r"(mul2(h[2], s2)), "r"(mul2(h[3], s2))
+          const uint32_t a = st_off[k] + b * kBufBytes, a4 = (st_off[k] ^ 64u) + b * kBufBytes;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0][4 * k]), "r"(v[0][4 * k + 1]),
+                       "r"(v[0][4 * k + 2]), "r"(v[0][4 * k + 3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0 + 512], {%1, %2, %3, %4};" ::"r"(a4), "r"(v[1][4 * k]), "r"(v[1][4 * k + 1]),
+                       "r"(v[1][4 * k + 2]), "r"(v[1][4 * k + 3])
                        : "memory");
         }
         fence_proxy_async();  // decoded rows -> visible to the tensor core
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kvfull[b * kPairs + pr]);
+        if (lane == 0) mbar_arrive(&kvfull[b * kHalves + half]);
       }
-      live = live_next;
     }
-  } else if (warp == kSWarp) {
-    // ------------------------------------------------------------------------ S = Q K^T
-    uint32_t gc = 0, item = 0;
-    bool ok = true;
-    const uint32_t q_addr = smem_u32(sq), kv_addr = smem_u32(skv);
-    for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-      for (int c = w.c0; c < w.c1; ++c, ++gc) {
-        const int b = gc & 1;
-        if (!mbar_wait_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 62)) { ok = false; break; }
-        for (int pr = 0; pr < kPairs; ++pr) {
-          if (c == w.c0 && !mbar_wait_warp(&qfull[pr], item & 1, p.status, 63)) { ok = false; break; }
-          if (!mbar_wait_warp(&kvfull[b * kPairs + pr], (gc >> 1) & 1, p.status, 64)) { ok = false; break; }
-          tc_fence_after();
+  } else if (warp >= kSWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kSWarp) {
+      // ------------------------------------------------------------------------ S = Q K^T
+      uint32_t gc = 0, item = 0;
+      bool ok = true;
+      const uint64_t q_desc = desc_sw128(smem_u32(sq), 16, 1024), kv_desc = desc_sw128(smem_u32(skv), 16, 1024);
+      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
+        for (int c = w.c0; c < w.c1; ++c, ++gc) {
+          const int b = gc & 1;
+          if (!wait_bar_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 62)) { ok = false; break; }
+          if (c == w.c0) {
+            if (lane == 0 && w.left > w.c1 - w.c0) prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kKv4Dim, kHq * kKv4Dim * 2);
+            if (!wait_bar_warp(qfull, item & 1, p.status, 63)) { ok = false; break; }
+          }
+#pragma unroll 1
+          for (int half = 0; half < kHalves; ++half) {
+            if (!wait_bar_warp(&kvfull[b * kHalves + half], (gc >> 1) & 1, p.status, 64)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t a0 = q_desc + half * (4 * kQBlockBytes >> 4);
+            const uint64_t b0 = kv_desc + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            const int kb = 2 * pr + h2;
+            for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = desc_sw128(q_addr + kb * kQBlockBytes + kk * 32, 16, 1024);
-              const uint64_t bd = desc_sw128(kv_addr + b * kBufBytes + kb * kSlotBytes + kk * 32, 16, 1024);
-              tc_mma_f16_elect(tmem + b * kHq, a, bd, kIdescS, (kb | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f16_elect(tmem + b * kHq, a0 + (kb * kQBlockBytes + kk * 32 >> 4), b0 + (kb * kSlotBytes + kk * 32 >> 4),
+                                 kIdescS, half | kb | kk);
+          }
+          if (!ok) break;
+          if (c == w.c1 - 1) tc_commit_elect(qempty);  // the next item's q may replace this one's
+          // the arrival of this warp hands on what it waited for (the chunk's mask, the item's factors)
+          if (lane == 0) mbar_arrive(&sfull[b]);
+          tc_commit_elect(&sfull[b]);
+        }
+      }
+    } else if (warp == kSlotWarp) {
+      // --------------------------------------------------------- slots of the rows, a few chunks ahead
+      uint32_t gc = 0;
+      bool ok = true;
+      for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
+        const int t = w.t, n = rows_s[t], b = request_of(p, t);
+        const int held = n > 0 && p.indices ? __ldg(p.rows + b) : 0x7fffffff;
+        const int32_t* list = p.indices ? p.indices + (int64_t)t * p.k_top : nullptr;
+        const int32_t* table = p.tables + (int64_t)(n > 0 ? b : 0) * p.max_pages;
+        for (int c = w.c0; c < w.c1; ++c, ++gc) {
+          int slot[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = c * kRows + lane + 32 * i;
+            const int row = j >= 0 && j < n ? (list ? __ldg(list + j) : j) : -1;
+            const int pg = row >> p.log_page;
+            slot[i] = -1;
+            if (row >= 0 && row < held && pg < p.max_pages) {
+              const int page = __ldg(table + pg);
+              const int64_t at = ((int64_t)page << p.log_page) + (row & ((1 << p.log_page) - 1));
+              if (page >= 0 && at < p.n_slots) slot[i] = (int)at;
             }
           }
-          if (c == w.c1 - 1) tc_commit_elect(&qempty[pr]);  // the next item's q may replace this quarter
+          const uint32_t m0 = __ballot_sync(0xffffffffu, slot[0] >= 0), m1 = __ballot_sync(0xffffffffu, slot[1] >= 0);
+          ok = wait_bar_warp(&slempty[gc % kRing], ((gc / kRing) & 1) ^ 1, p.status, 59);
+          if (!ok) break;
+          slot_s[(gc % kRing) * kRows + lane] = slot[0];
+          slot_s[(gc % kRing) * kRows + lane + 32] = slot[1];
+          // a mask is overwritten eight chunks later: its slots were read then four chunks ago, by warps that
+          // are at most two chunks ahead of the softmax
+          if (lane == 0) *reinterpret_cast<uint2*>(mask_s + (gc % kMaskRing) * 2) = make_uint2(m0, m1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&slfull[gc % kRing]);
         }
-        if (!ok) break;
-        // the arrival of this warp hands on what it waited for (the chunk's mask, the item's factors)
-        if (lane == 0) mbar_arrive(&sfull[b]);
-        tc_commit_elect(&sfull[b]);
       }
-    }
-  } else if (warp == kOWarp) {
-    // --------------------------------------------------------------------- O^T += V^T P^T
-    uint32_t gc = 0, item = 0;
-    uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
-    bool ok = true;
-    const uint32_t kv_addr = smem_u32(skv), p_addr = smem_u32(sp);
-    for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-      for (int c = w.c0; c < w.c1; ++c, ++gc) {
-        const int b = gc & 1;
-        if (!mbar_wait_warp(&pfull[b], (gc >> 1) & 1, p.status, 65)) { ok = false; break; }
-        tc_fence_after();
+    } else if (warp == kOWarp) {
+      // --------------------------------------------------------------------- O^T += V^T P^T
+      uint32_t gc = 0, item = 0;
+      uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
+      bool ok = true;
+      const uint64_t v_desc = desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_desc = desc_sw128(smem_u32(sp), 16, 1024);
+      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
+        for (int c = w.c0; c < w.c1; ++c, ++gc) {
+          const int b = gc & 1;
+          if (!wait_bar_warp(&pfull[b], (gc >> 1) & 1, p.status, 65)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int db = 0; db < kPairs; ++db) {
+            const int os = oslot(item, db);
+            // an item's first product overwrites its slot: the output that last read it is done
+            if (c == w.c0) {
+              if (!wait_bar_warp(&oempty[os], ((o_ph >> os) & 1u) ^ 1u, p.status, 66)) { ok = false; break; }
+              o_ph ^= 1u << os;
+              tc_fence_after();
+            }
+            const uint64_t a0 = v_desc + (b * kBufBytes + 2 * db * kSlotBytes >> 4), b0 = p_desc + (b * kPBytes >> 4);
 #pragma unroll
-        for (int db = 0; db < kPairs; ++db) {
-          const int os = oslot(item, db);
-          // an item's first product overwrites its slot: the output that last read it is done
-          if (c == w.c0) {
-            if (!mbar_wait_warp(&oempty[os], ((o_ph >> os) & 1u) ^ 1u, p.status, 66)) { ok = false; break; }
-            o_ph ^= 1u << os;
-            tc_fence_after();
+            for (int ks = 0; ks < kRows / 16; ++ks)
+              tc_mma_f16_elect(tmem + kColO + os * kHq, a0 + (ks * 2048 >> 4), b0 + (ks * 32 >> 4), kIdescO, c > w.c0 || ks > 0);
+            if (db & 1) tc_commit_elect(&kvempty[b * kHalves + (db >> 1)]);  // this half of the chunk is free
+            if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
           }
-#pragma unroll
-          for (int ks = 0; ks < kRows / 16; ++ks) {
-            const uint64_t a = desc_sw128(kv_addr + b * kBufBytes + (2 * db) * kSlotBytes + ks * 2048, kSlotBytes, 1024);
-            const uint64_t bd = desc_sw128(p_addr + b * kPBytes + ks * 32, 16, 1024);
-            tc_mma_f16_elect(tmem + kColO + os * kHq, a, bd, kIdescO, (c > w.c0 || ks > 0));
-          }
-          tc_commit_elect(&kvempty[b * kPairs + db]);  // this quarter of the chunk is free
-          if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
+          if (!ok) break;
+          tc_commit_elect(&pempty[b]);
         }
-        if (!ok) break;
-        tc_commit_elect(&pempty[b]);
       }
     }
   } else if (warp < kOutWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------------------- softmax
     // S holds head 16 quad + i on TMEM lane 32 quad + i (i < 16).  The 16x256b load gives thread
     // (g = lane / 4, e = lane % 4) the heads hA = 16 quad + g and hB = hA + 8 and, of each, the
@@ -430,33 +547,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     const int hA = 16 * quad + g, hB = hA + 8;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t gc = 0, item = 0;
-    bool ok = true;
-    for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
+    // a wait that gave up is acted on where the four warps meet, so that they leave together
+    bool ok = true, leave = false;
+    for (Walk w(rows_s, start); w.left > 0 && !leave; w.next(), ++item) {
       float mA = -INFINITY, mB = -INFINITY;          // running maximum (log2 units)
       float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of the weights, and of the rounded ones
       for (int ci = w.c0; ci < w.c1; ++ci, ++gc) {
         const int b = gc & 1;
-        ok = named_and(kSoftBar, kGroupThreads, mbar_wait(&sfull[b], (gc >> 1) & 1, p.status, 67));
-        if (!ok) break;
+        ok = ok && wait_bar_warp(&sfull[b], (gc >> 1) & 1, p.status, 67);
         tc_fence_after();
         float x[32];
         tmem_ld_16x256b_x8(tmem + t_lane + b * kHq, x);
-        const uint2 live = *reinterpret_cast<const uint2*>(mask_s + b * 4);
-        const float cA = cq[(item & 1) * 2 * kHq + hA], cB = cq[(item & 1) * 2 * kHq + hB];
+        const uint2 live = *reinterpret_cast<const uint2*>(mask_s + (gc % kMaskRing) * 2);
+        const float cA = cq[(item % kItems) * kHq + hA], cB = cq[(item % kItems) * kHq + hB];
         tc_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[b]);
-        const uint32_t v0 = live.x >> (2 * e), v1 = live.y >> (2 * e);
+        // scaled before the maximum is taken from them: a fused multiply-add would not cancel exactly
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          x[4 * r] *= cA;
+          x[4 * r + 1] *= cA;
+          x[4 * r + 2] *= cB;
+          x[4 * r + 3] *= cB;
+        }
+        if ((live.x & live.y) != 0xffffffffu) {
+          const uint32_t v0 = live.x >> (2 * e), v1 = live.y >> (2 * e);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const uint32_t bits = (r < 4 ? v0 : v1) >> (8 * (r & 3));
+            if (!(bits & 1u)) x[4 * r] = x[4 * r + 2] = -INFINITY;
+            if (!(bits & 2u)) x[4 * r + 1] = x[4 * r + 3] = -INFINITY;
+          }
+        }
         float mxA = -INFINITY, mxB = -INFINITY;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const uint32_t bits = (r < 4 ? v0 : v1) >> (8 * (r & 3));
-          const bool ok0 = (bits & 1u) != 0, ok1 = (bits & 2u) != 0;
-          x[4 * r] = ok0 ? x[4 * r] * cA : -INFINITY;
-          x[4 * r + 2] = ok0 ? x[4 * r + 2] * cB : -INFINITY;
-          x[4 * r + 1] = ok1 ? x[4 * r + 1] * cA : -INFINITY;
-          x[4 * r + 3] = ok1 ? x[4 * r + 3] * cB : -INFINITY;
           mxA = fmaxf(mxA, fmaxf(x[4 * r], x[4 * r + 1]));
           mxB = fmaxf(mxB, fmaxf(x[4 * r + 2], x[4 * r + 3]));
         }
@@ -476,7 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           aB = needB ? ex2_approx(mB - mxB) : 0.f;
           mB = mxB;
         }
-        if (named_or(kSoftBar, kGroupThreads, needA || needB)) {
+        if (named_or(kSoftBar, kGroupThreads, needA || needB || !ok)) {
+          leave = named_or(kSoftBar, kGroupThreads, !ok);
+          if (leave) break;
           if (e == 0) {
             alpha_s[hA] = needA ? aA : 1.f;
             alpha_s[hB] = needB ? aB : 1.f;
@@ -484,8 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           named_sync(kSoftBar, kGroupThreads);
           // O^T must hold all of the previous chunk before its columns are rescaled
           const uint32_t prev = gc - 1;
-          ok = named_and(kSoftBar, kGroupThreads, mbar_wait(&pempty[prev & 1], (prev >> 1) & 1, p.status, 68));
-          if (!ok) break;
+          ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 68);
           tc_fence_after();
 #pragma unroll 1
           for (int q2 = 0; q2 < 2 * kPairs; ++q2) {  // 4 quarters x 2 halves of 32 heads
@@ -504,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         rA *= aA;
         lB *= aB;
         rB *= aB;
-        // weights 2^(x - m + 7), rounded to fp16 for the product
+        // weights 2^(x - m + 4), rounded to fp16 for the product
         const float nA = kWeightLog2 - (mA == -INFINITY ? 0.f : mA);
         const float nB = kWeightLog2 - (mB == -INFINITY ? 0.f : mB);
         uint32_t pkA[8], pkB[8];
@@ -515,14 +643,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           const __half2 hp = __floats2half2_rn(a0, a1), hq = __floats2half2_rn(b0, b1);
           lA += a0 + a1;
           lB += b0 + b1;
-          const float2 fp = __half22float2(hp), fq = __half22float2(hq);
-          rA += fp.x + fp.y;
-          rB += fq.x + fq.y;
+          add_halves(rA, hp);
+          add_halves(rB, hq);
           pkA[r] = *reinterpret_cast<const uint32_t*>(&hp);
           pkB[r] = *reinterpret_cast<const uint32_t*>(&hq);
         }
-        ok = named_and(kSoftBar, kGroupThreads, mbar_wait(&pempty[b], ((gc >> 1) & 1) ^ 1, p.status, 69));
-        if (!ok) break;
+        ok = ok && wait_bar_warp(&pempty[b], ((gc >> 1) & 1) ^ 1, p.status, 69);
         {
           // P[h][j], K-major with the 128-byte swizzle: 16-byte chunk r of line h at (r ^ (h & 7))
           uint8_t* lineA = sp + b * kPBytes + hA * 128 + 4 * e;
@@ -538,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[b]);
       }
-      if (!ok) break;
+      if (leave) break;
 #pragma unroll
       for (int d = 1; d <= 2; d <<= 1) {
         lA += __shfl_xor_sync(0xffffffffu, lA, d);
@@ -547,8 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         rB += __shfl_xor_sync(0xffffffffu, rB, d);
       }
       // the slot of this item's parity was last read by the output of item - 2
-      ok = named_and(kSoftBar, kGroupThreads, mbar_wait(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 70));
-      if (!ok) break;
+      ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 70);
       if (e == 0) {
         float* row = lm + (item & 1) * 4 * kHq;
         row[hA] = rA;
@@ -564,151 +689,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       if (lane == 0) mbar_arrive(&lready[item & 1]);
     }
   } else {
-    // ------------------------------------------------------------- q in, output out
-    const int quad = warp - kOutWarp, tid4 = tid - kOutWarp * 32;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    // --------------------------------------------------------------------------- output
+    const int quad = warp - kOutWarp;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
     const bool odd = lane & 1;
-    // a head's factors: q is multiplied by +-2^s, s from its largest magnitude (compared as bits); a
-    // logit in log2 units is then |scale| log2(e) 2^-s times the product
-    auto head_factors = [&](int t, uint32_t item) {
-      float* f = cq + (item & 1) * 2 * kHq;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)t * kHq + quad * 16) * kKv4Dim) + lane * 2;
-#pragma unroll
-      for (int h0 = 0; h0 < 16; h0 += 4) {
-        uint4 u[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i][0] = __ldg(src + (h0 + i) * (kKv4Dim / 8));
-          u[i][1] = __ldg(src + (h0 + i) * (kKv4Dim / 8) + 1);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            top = __vmaxu2(top, u[i][k].x & 0x7fff7fffu);
-            top = __vmaxu2(top, u[i][k].y & 0x7fff7fffu);
-            top = __vmaxu2(top, u[i][k].z & 0x7fff7fffu);
-            top = __vmaxu2(top, u[i][k].w & 0x7fff7fffu);
-          }
-#pragma unroll
-          for (int d = 16; d >= 1; d >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
-          top = max(top & 0xffffu, top >> 16);
-          if (lane == 0) {
-            const float a = kBf16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((uint16_t)top));
-            int s = 0;
-            if (a > 0.f && a < INFINITY) s = min(14 + 127 - (int)(__float_as_uint(a) >> 23), 126);
-            const int h = quad * 16 + h0 + i;
-            f[h] = fabsf(p.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - s) << 23);
-            const float up = __uint_as_float((uint32_t)(127 + s) << 23);
-            f[kHq + h] = p.scale < 0.f ? -up : up;
-          }
-        }
-      }
-    };
-    // q of token t as fp16 into the operand's layout, quarter by quarter as the quarters become free
-    auto convert_q = [&](int t, uint32_t item) {
-      const float* f = cq + (item & 1) * 2 * kHq + kHq;
-      const int h0 = tid4 >> 4, ch = tid4 & 15;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)t * kHq + h0) * kKv4Dim) + ch;
-      bool got = true;
-      for (int pr = 0; pr < kPairs; ++pr) {
-        uint4 u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = __ldg(src + 8 * i * (kKv4Dim / 8) + pr * 16);
-        got = got && mbar_wait_warp(&qempty[pr], (item & 1) ^ 1, p.status, 71);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int h = h0 + 8 * i;
-          const float m = f[h];
-          uint4 o;
-          o.x = scaled2<kBf16>(u[i].x, m);
-          o.y = scaled2<kBf16>(u[i].y, m);
-          o.z = scaled2<kBf16>(u[i].z, m);
-          o.w = scaled2<kBf16>(u[i].w, m);
-          *reinterpret_cast<uint4*>(sq + (2 * pr + (ch >> 3)) * kQBlockBytes + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) = o;
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[pr]);
-      }
-      return got;
-    };
     uint32_t item = 0;
     uint32_t f_ph = 0;  // bit s: phase of O^T slot s's full barrier
     bool ok = true;
-    Walk w(rows_s, start);
-    if (w.left > 0) {
-      head_factors(w.t, 0);
-      named_sync(kEpiBar, kGroupThreads);
-      ok = named_and(kEpiBar, kGroupThreads, convert_q(w.t, 0));
-    }
-    // a wait that gave up is acted on where the four warps meet, so that they leave together
-    for (; w.left > 0; w.next(), ++item) {
-      if (w.left > w.c1 - w.c0) {  // the next item's q, while this item is worked on
-        head_factors(w.t + 1, item + 1);
-        named_sync(kEpiBar, kGroupThreads);
-        const bool got = convert_q(w.t + 1, item + 1);
-        ok = named_and(kEpiBar, kGroupThreads, ok && got);
-        if (!ok) break;
-      }
+    for (Walk w(rows_s, start); w.left > 0; w.next(), ++item) {
       const int par = item & 1;
-      ok = named_and(kEpiBar, kGroupThreads, ok && mbar_wait(&lready[par], (item >> 1) & 1, p.status, 72));
+      ok = wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
       if (!ok) break;
       const float* lrow = lm + par * 4 * kHq;
       // chunks before the block, or behind it: the sums go to the block's first or second part
       const bool whole = w.c0 == 0 && w.c1 == chunks_of(rows_s[w.t]);
       const int64_t part = 2 * (int64_t)blockIdx.x + (w.c0 == 0);
-      if (quad == 0) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int hh = lane + 32 * k;
-          const float l = lrow[kHq + hh], m = lrow[2 * kHq + hh];
-          if (!whole) {
-            float* st = p.stat + part * kStatFloats;
-            st[hh] = lrow[hh];
-            st[kHq + hh] = l;
-            st[2 * kHq + hh] = m;
-          } else if (p.lse) {
-            p.lse[(int64_t)w.t * kHq + hh] = l == 0.f ? -INFINITY : (m + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
-          }
+      if (lane < 16) {
+        const int hh = quad * 16 + lane;
+        const float l = lrow[kHq + hh], m = lrow[2 * kHq + hh];
+        if (!whole) {
+          float* st = p.stat + part * kStatFloats;
+          st[hh] = lrow[hh];
+          st[kHq + hh] = l;
+          st[2 * kHq + hh] = m;
+        } else if (p.lse) {
+          p.lse[(int64_t)w.t * kHq + hh] = l == 0.f ? -INFINITY : (m + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
         }
       }
 #pragma unroll 1
-      for (int db = 0; db < kPairs; ++db) {
+      for (int half = 0; half < 2 * kPairs; ++half) {  // quarters of the dims by halves of the heads
+        const int db = half >> 1, hb = (half & 1) * 32;
         const int os = oslot(item, db);
-        ok = ok && mbar_wait_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 73);
-        f_ph ^= 1u << os;
-        tc_fence_after();
-        float va[32], vb[32];
-        tmem_ld32(tmem + t_lane + kColO + os * kHq, va);
-        tmem_ld32(tmem + t_lane + kColO + os * kHq + 32, vb);
+        if (hb == 0) {
+          ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 73);
+          if (!ok) break;
+          f_ph ^= 1u << os;
+          tc_fence_after();
+        }
+        float v[32];
+        tmem_ld32(tmem + t_lane + kColO + os * kHq + hb, v);
         tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&oempty[os]);
+        if (hb) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&oempty[os]);
+        }
+        const int d = db * 128 + quad * 32 + lane;
         if (whole) {
-          uint32_t* orow = reinterpret_cast<uint32_t*>(p.out + (int64_t)w.t * kHq * kKv4Dim);
-          const int d_even = db * 128 + quad * 32 + (lane & ~1);
+          // neighbouring lanes exchange, so that each writes two dims of one head
+          uint32_t* orow = reinterpret_cast<uint32_t*>(p.out + ((int64_t)w.t * kHq + hb + (odd ? 1 : 0)) * kKv4Dim) + (d >> 1);
+          const float4* inv = reinterpret_cast<const float4*>(lrow + 3 * kHq + hb);
+          const uint32_t sel = odd ? 0x3276u : 0x5410u;  // even: both first heads; odd: both second ones
 #pragma unroll
-          for (int h0 = 0; h0 < kHq; h0 += 2) {
-            const float a0 = (h0 < 32 ? va[h0 & 31] : vb[h0 & 31]) * lrow[3 * kHq + h0];
-            const float a1 = (h0 < 32 ? va[(h0 + 1) & 31] : vb[(h0 + 1) & 31]) * lrow[3 * kHq + h0 + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-            const int hw = h0 + (odd ? 1 : 0);
-            orow[((int64_t)hw * kKv4Dim + d_even) >> 1] =
-                odd ? (uint32_t)to16<kBf16>(got) | ((uint32_t)to16<kBf16>(a1) << 16)
-                    : (uint32_t)to16<kBf16>(a0) | ((uint32_t)to16<kBf16>(got) << 16);
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f = inv[i / 4];
+            const uint32_t w0 = pack16<kBf16>(v[i] * f.x, v[i + 1] * f.y), w1 = pack16<kBf16>(v[i + 2] * f.z, v[i + 3] * f.w);
+            orow[i * (kKv4Dim / 2)] = __byte_perm(w0, __shfl_xor_sync(0xffffffffu, w0, 1), sel);
+            orow[(i + 2) * (kKv4Dim / 2)] = __byte_perm(w1, __shfl_xor_sync(0xffffffffu, w1, 1), sel);
           }
         } else {
-          float* dst = p.part + part * kPartFloats + db * 128 + quad * 32 + lane;
+          float* dst = p.part + part * kPartFloats + hb * kKv4Dim + d;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) {
-            dst[h * kKv4Dim] = va[h];
-            dst[(h + 32) * kKv4Dim] = vb[h];
-          }
+          for (int i = 0; i < 32; ++i) dst[i * kKv4Dim] = v[i];
         }
       }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&lfree[par]);
     }
@@ -758,8 +804,7 @@ __global__ void __launch_bounds__(kKv4Dim / 4) kv4_combine_kernel(const int4* __
     acc.w += f * o.w;
   }
   const float inv = r == 0.f ? 0.f : 1.f / r;
-  const uint32_t lo = (uint32_t)to16<kBf16>(acc.x * inv) | ((uint32_t)to16<kBf16>(acc.y * inv) << 16);
-  const uint32_t hi = (uint32_t)to16<kBf16>(acc.z * inv) | ((uint32_t)to16<kBf16>(acc.w * inv) << 16);
+  const uint32_t lo = pack16<kBf16>(acc.x * inv, acc.y * inv), hi = pack16<kBf16>(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h) * kKv4Dim + 4 * threadIdx.x) = make_uint2(lo, hi);
   if (threadIdx.x == 0 && lse)
     lse[(int64_t)at.x * kHq + h] =
