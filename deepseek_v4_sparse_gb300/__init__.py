@@ -14,6 +14,7 @@ Entry points (same names as the C ABI, without the ``ds4x_`` prefix):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -550,62 +551,68 @@ def decode_local(q, w, q_attn, k, kv, S0: int, pos0: int, ratio: int, kv_raw, kv
 
 
 # ----------------------------------------------------------------------- paged 4-bit cache
-class _On:
-    """Makes `device` current, and `stream` when one is given, so that what a call allocates belongs to
-    the stream that its kernels run on.  Gives that stream's address."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self._ctx = ()
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                               device=device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-        if stream is not None:
-            self._ctx = (torch.cuda.device(device), torch.cuda.stream(stream))
-        elif torch.cuda.current_device() != device.index:
-            self._ctx = (torch.cuda.device(device),)
-        self._stream, self._device = stream, device
-
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        s = _torch().cuda.current_stream(self._device) if self._stream is None else self._stream
-        return s.cuda_stream
-
-    def __exit__(self, *e):
-        for c in reversed(self._ctx):
-            c.__exit__(*e)
-
-
-def _tensor(name, t, dtype, device=None, numel=None, shape=None):
-    """The address of a CUDA tensor after checking its dtype, device, layout and size (numel: at least)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device, got {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be of shape {shape}, got {tuple(t.shape)}")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
+# A decode step calls these with a few microseconds of GPU work each, so the checks are written to cost
+# little: a tensor that passes is looked at once, and the current stream is asked for by its address.
+def _addr(name, t, dtype, dev):
+    """The address of a contiguous tensor of `dtype` on CUDA device number `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, dev)
     return t.data_ptr()
 
 
-def _kv4_pool(codes, scales, device):
-    """Addresses of a pool's codes [..., 256] and scales [..., 16], and its number of slots."""
+def _refuse(name, t, dtype, dev):
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _addr_n(name, t, dtype, dev, n):
+    """_addr of a tensor of at least n elements."""
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
+    return _addr(name, t, dtype, dev)
+
+
+def _elsewhere(dev, stream):
+    """None when a call may run as it is: `dev` is current and no stream was given.  Otherwise the contexts
+    to run it in, so that what it allocates belongs to the device and stream that its kernels run on."""
     torch = _torch()
-    pc = _tensor("codes", codes, torch.uint8, device)
-    psc = _tensor("scales", scales, torch.uint8, device)
-    if codes.shape[-1] != KV4_CODE_BYTES or scales.shape[-1] != KV4_SCALE_BYTES:
+    if dev < 0:
+        raise ValueError("tensors passed to libds4x must live on a CUDA device")
+    if stream is None:
+        return None if torch._C._cuda_getDevice() == dev else (torch.cuda.device(dev),)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           device=torch.device("cuda", dev))
+    if stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    return torch.cuda.device(dev), torch.cuda.stream(stream)
+
+
+def _within(contexts, call, *args, **kw):
+    with contextlib.ExitStack() as stack:
+        for c in contexts:
+            stack.enter_context(c)
+        return call(*args, **kw)
+
+
+def _raw_stream(dev):
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _kv4_pool(codes, scales, dev):
+    """Addresses of a pool's codes [..., 256] and scales [..., 16], and its number of slots."""
+    uint8 = _torch().uint8
+    pc, psc = _addr("codes", codes, uint8, dev), _addr("scales", scales, uint8, dev)
+    n = codes.numel() // KV4_CODE_BYTES
+    if codes.size(-1) != KV4_CODE_BYTES or scales.size(-1) != KV4_SCALE_BYTES:
         raise ValueError(f"codes must end in {KV4_CODE_BYTES} bytes and scales in {KV4_SCALE_BYTES}, got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
-    n = codes.numel() // KV4_CODE_BYTES
-    if scales.numel() // KV4_SCALE_BYTES != n:
+    if scales.numel() != n * KV4_SCALE_BYTES:
         raise ValueError(f"codes hold {n} slots, scales {scales.numel() // KV4_SCALE_BYTES}")
     return pc, psc, n
 
@@ -618,62 +625,79 @@ def page_plan(seen, n_new, rows, tables, free_pages, n_free, ratio: int, page_ro
     [n_req, max_pages] int32, the new pages' entries are written in place; pages are taken from the end of
     free_pages[:n_free] (n_free [1] int32).  Returns (positions [T_cap], req [T_cap], slots [R_cap], seen_out,
     rows_out, n_free_out, totals [4] = tokens, completed rows, rows with a slot, pages taken); the packed
-    outputs end in -1.  An output may be passed in; seen_out, rows_out and n_free_out may be their inputs."""
+    outputs end in -1.  Outputs may be passed in (when none is, they share one allocation); seen_out, rows_out
+    and n_free_out may be their inputs."""
     torch = _torch()
-    i32, dev = torch.int32, seen.device
+    i32, dev = torch.int32, seen.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, page_plan, seen, n_new, rows, tables, free_pages, n_free, ratio, page_rows, T_cap,
+                       R_cap, positions, req, slots, seen_out, rows_out, n_free_out, totals)
     B = seen.numel()
-    if tables.dim() != 2 or tables.shape[0] != B:
+    if tables.dim() != 2 or tables.size(0) != B:
         raise ValueError(f"tables must be [{B}, max_pages], got {tuple(tables.shape)}")
-    max_pages = tables.shape[1]
-    a = [_tensor("seen", seen, i32), _tensor("n_new", n_new, i32, dev, B), _tensor("rows", rows, i32, dev, B),
-         _tensor("tables", tables, i32, dev), _tensor("free_pages", free_pages, i32, dev)]
-    pf = _tensor("n_free", n_free, i32, dev, 1)
-    with _On(dev, stream) as st:
-        def out(name, t, n):
-            if t is None:
-                t = torch.empty((n,), dtype=i32, device=dev)
-            return t, _tensor(name, t, i32, dev, n)
-        positions, p0 = out("positions", positions, T_cap)
-        req, p1 = out("req", req, T_cap)
-        slots, p2 = out("slots", slots, R_cap)
-        seen_out, p3 = out("seen_out", seen_out, B)
-        rows_out, p4 = out("rows_out", rows_out, B)
-        n_free_out, p5 = out("n_free_out", n_free_out, 1)
-        totals, p6 = out("totals", totals, 4)
-        rc = load().ds4x_page_plan(*a, free_pages.numel(), pf, B, max_pages, page_rows, ratio, T_cap, R_cap,
-                                   p0, p1, p2, p3, p4, p5, p6, st)
-    _check("ds4x_page_plan", rc)
-    return positions, req, slots, seen_out, rows_out, n_free_out, totals
+    if T_cap < 0 or R_cap < 0:
+        raise ValueError(f"T_cap and R_cap must not be negative, got {T_cap} and {R_cap}")
+    max_pages = tables.size(1)
+    a = (_addr("seen", seen, i32, dev), _addr_n("n_new", n_new, i32, dev, B), _addr_n("rows", rows, i32, dev, B),
+         _addr("tables", tables, i32, dev), _addr("free_pages", free_pages, i32, dev))
+    pf = _addr_n("n_free", n_free, i32, dev, 1)
+    outs = (positions, req, slots, seen_out, rows_out, n_free_out, totals)
+    sizes = (T_cap, T_cap, R_cap, B, B, 1, 4)
+    if positions is req is slots is seen_out is rows_out is n_free_out is totals is None:
+        # the positions come first: 16-byte aligned, as the scorer and the top-k take them
+        fresh = torch.empty((2 * T_cap + R_cap + 2 * B + 5,), dtype=i32, device=dev)
+        at = fresh.data_ptr()
+        b = [at, at + 4 * T_cap, at + 8 * T_cap]
+        b += [b[2] + 4 * R_cap, b[2] + 4 * (R_cap + B), b[2] + 4 * (R_cap + 2 * B), b[2] + 4 * (R_cap + 2 * B + 1)]
+        outs = fresh.split_with_sizes(sizes)
+    else:
+        outs = tuple([torch.empty((n,), dtype=i32, device=dev) if t is None else t for n, t in zip(sizes, outs)])
+        b = [_addr_n(name, t, i32, dev, n) for name, t, n in zip(
+            ("positions", "req", "slots", "seen_out", "rows_out", "n_free_out", "totals"), outs, sizes)]
+    rc = (_lib or load()).ds4x_page_plan(*a, free_pages.numel(), pf, B, max_pages, page_rows, ratio, T_cap, R_cap, *b,
+                                         _raw_stream(dev))
+    if rc:
+        _check("ds4x_page_plan", rc)
+    return outs
 
 
 def kv4_append(rows, slots, codes, scales, stream=None):
     """Quantises rows [n, 512] (fp16 or bf16) and writes row i to slot slots[i] of the pool codes [..., 256],
     scales [..., 16]; a slot outside the pool (the -1 of page_plan) skips its row.  Slots must be distinct."""
     torch = _torch()
-    dt, dev = _kv_dtype(rows), rows.device
+    dt, dev = _kv_dtype(rows), rows.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, kv4_append, rows, slots, codes, scales)
     n, Dkv = rows.shape
-    pr = _tensor("rows", rows, rows.dtype)
-    ps = _tensor("slots", slots, torch.int32, dev, n)
+    pr = _addr("rows", rows, rows.dtype, dev)
+    ps = _addr_n("slots", slots, torch.int32, dev, n)
     pc, psc, n_slots = _kv4_pool(codes, scales, dev)
-    with _On(dev, stream) as st:
-        rc = load().ds4x_kv4_append(pr, dt, ps, n, Dkv, pc, psc, n_slots, st)
-    _check("ds4x_kv4_append", rc)
+    rc = (_lib or load()).ds4x_kv4_append(pr, dt, ps, n, Dkv, pc, psc, n_slots, _raw_stream(dev))
+    if rc:
+        _check("ds4x_kv4_append", rc)
 
 
 def kv4_read(codes, scales, slots, dtype, out=None, stream=None):
     """The rows at slots [n] int32 of the pool as [n, 512] of `dtype` (float16 or bfloat16); zeros for a slot
     outside the pool."""
     torch = _torch()
-    dev = codes.device
+    dev = codes.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, kv4_read, codes, scales, slots, dtype, out)
     pc, psc, n_slots = _kv4_pool(codes, scales, dev)
     n, Dkv = slots.numel(), 2 * KV4_CODE_BYTES
-    ps = _tensor("slots", slots, torch.int32, dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((n, Dkv), dtype=dtype, device=dev)
-        po = _tensor("out", out, dtype, dev, shape=(n, Dkv))
-        rc = load().ds4x_kv4_read(pc, psc, n_slots, ps, n, Dkv, po, _kv_dtype(out), st)
-    _check("ds4x_kv4_read", rc)
+    ps = _addr("slots", slots, torch.int32, dev)
+    if out is None:
+        out = torch.empty((n, Dkv), dtype=dtype, device=dev)
+    elif out.shape != (n, Dkv):
+        raise ValueError(f"out must be of shape {(n, Dkv)}, got {tuple(out.shape)}")
+    po = _addr("out", out, dtype, dev)
+    rc = (_lib or load()).ds4x_kv4_read(pc, psc, n_slots, ps, n, Dkv, po, _kv_dtype(out), _raw_stream(dev))
+    if rc:
+        _check("ds4x_kv4_read", rc)
     return out
 
 
@@ -690,47 +714,57 @@ def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, posi
     [T, k_top] it attends to those rows (the first counts[t] entries; -1 and rows not held are skipped),
     without to every row visible at positions[t] (None: all held).  Returns (out, lse)."""
     torch = _torch()
-    i32, dev = torch.int32, q_attn.device
+    i32, dev = torch.int32, q_attn.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, kv4_attn, q_attn, codes, scales, tables, rows, page_rows, req, positions, ratio,
+                       indices, counts, scale, out, lse, workspace, want_lse)
     dt = _kv_dtype(q_attn)
-    T, Hq, Dkv = q_attn.shape
-    pq = _tensor("q_attn", q_attn, q_attn.dtype)
+    dtype = q_attn.dtype
+    T, Hq, Dkv = shape = q_attn.shape
+    pq = _addr("q_attn", q_attn, dtype, dev)
     pc, psc, n_slots = _kv4_pool(codes, scales, dev)
     n_req = rows.numel()
-    prow = _tensor("rows", rows, i32, dev)
-    if tables.dim() != 2 or tables.shape[0] != n_req:
+    prow = _addr("rows", rows, i32, dev)
+    if tables.dim() != 2 or tables.size(0) != n_req:
         raise ValueError(f"tables must be [{n_req}, max_pages], got {tuple(tables.shape)}")
-    max_pages = tables.shape[1]
-    ptab = _tensor("tables", tables, i32, dev)
-    preq = None if req is None else _tensor("req", req, i32, dev, T)
-    ppos = None if positions is None else _tensor("positions", positions, i32, dev, T)
+    max_pages = tables.size(1)
+    ptab = _addr("tables", tables, i32, dev)
+    preq = None if req is None else _addr_n("req", req, i32, dev, T)
+    ppos = None if positions is None else _addr_n("positions", positions, i32, dev, T)
     k_top, pidx, pcnt, max_rows = 0, None, None, max_pages * page_rows
     if indices is not None:
-        if indices.dim() != 2 or indices.shape[0] != T:
+        if indices.dim() != 2 or indices.size(0) != T:
             raise ValueError(f"indices must be [{T}, k_top], got {tuple(indices.shape)}")
-        k_top = max_rows = indices.shape[1]
-        pidx = _tensor("indices", indices, i32, dev)
-        pcnt = None if counts is None else _tensor("counts", counts, i32, dev, T)
+        k_top = max_rows = indices.size(1)
+        pidx = _addr("indices", indices, i32, dev)
+        pcnt = None if counts is None else _addr_n("counts", counts, i32, dev, T)
     elif counts is not None:
         raise ValueError("counts belong to indices")
-    scale = 1.0 / math.sqrt(Dkv) if scale is None else scale
-    lib = load()
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(q_attn)
-        if lse is None and want_lse:
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif out.shape != shape:
+        raise ValueError(f"out must be of shape {tuple(shape)}, got {tuple(out.shape)}")
+    if lse is None:
+        if want_lse:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        po = _tensor("out", out, q_attn.dtype, dev, shape=(T, Hq, Dkv))
-        pl = None if lse is None else _tensor("lse", lse, torch.float32, dev, shape=(T, Hq))
-        if workspace is None:
-            need = lib.ds4x_kv4_attn_workspace_bytes(T, max_rows)
-            if need > 0:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        pw, wbytes = None, 0
-        if workspace is not None:
-            pw, wbytes = _tensor("workspace", workspace, workspace.dtype, dev), workspace.nbytes
-        rc = lib.ds4x_kv4_attn(pq, dt, pc, psc, n_slots, ptab, prow, n_req, max_pages, page_rows, preq, ppos, ratio,
-                               pidx, pcnt, T, Hq, Dkv, k_top, scale, po, pl, pw, wbytes, st)
-    _check("ds4x_kv4_attn", rc)
+    elif lse.shape != (T, Hq):
+        raise ValueError(f"lse must be of shape {(T, Hq)}, got {tuple(lse.shape)}")
+    lib = _lib or load()
+    if workspace is None and 0 <= max_rows < 2**31:
+        need = lib.ds4x_kv4_attn_workspace_bytes(T, max_rows)
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    pw, wbytes = None, 0
+    if workspace is not None:
+        pw, wbytes = _addr("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size()
+    rc = lib.ds4x_kv4_attn(pq, dt, pc, psc, n_slots, ptab, prow, n_req, max_pages, page_rows, preq, ppos, ratio, pidx,
+                           pcnt, T, Hq, Dkv, k_top, 1.0 / math.sqrt(Dkv) if scale is None else scale,
+                           _addr("out", out, dtype, dev),
+                           None if lse is None else _addr("lse", lse, torch.float32, dev), pw, wbytes,
+                           _raw_stream(dev))
+    if rc:
+        _check("ds4x_kv4_attn", rc)
     return out, lse
 
 

@@ -9,8 +9,10 @@
 // The step plan is bound by latency at a decode step's sizes (a few hundred bytes) and by its writes at
 // a large step's (8 bytes a token).  Every block computes the prefix sums over all requests for itself
 // (at most 4096 of them: cheaper than handing them over through memory) and then fills its share of the
-// outputs, finding the request of an element by binary search in shared memory.  The blocks are one
-// cluster, whose barrier separates the reads of the request state from its (in place) update.
+// outputs: a warp takes a run of neighbouring elements, finds the request of the first by a search in which
+// each lane looks at one place (three steps for 4096), and from there on the requests of 128 elements at a
+// time, between which a lane searches.  The blocks are one cluster, whose barrier separates the reads of
+// the request state from its (in place) update.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -147,14 +149,54 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// First request whose inclusive sum is above x; n if there is none.
-__device__ __forceinline__ int find_above(const uint32_t* ends, int n, uint32_t x) {
-  int lo = 0, hi = n;
+// First request in [lo, hi) whose inclusive sum is above x; hi if there is none.
+__device__ __forceinline__ int find_above(const uint32_t* ends, int lo, int hi, uint32_t x) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (ends[mid] > x) hi = mid; else lo = mid + 1;
   }
   return lo;
+}
+// The same by a whole warp: each lane looks at the last place of its part.
+__device__ __forceinline__ int warp_find_above(const uint32_t* ends, int lo, int hi, uint32_t x) {
+  const int lane = threadIdx.x & 31;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5;
+    const int at = lo + (lane + 1) * step - 1;
+    const uint32_t above = __ballot_sync(0xffffffffu, at >= hi || ends[at] > x);
+    if (above == 0) return hi;  // 32 whole parts, and none of them ends above x
+    const int f = __ffs(above) - 1;
+    if (step == 1) return min(lo + f, hi);
+    hi = min(hi, lo + (f + 1) * step - 1);  // that place is above x already
+    lo += f * step;
+  }
+  return lo;
+}
+// f(element, request) for elements [0, n) of lists packed by request, `ends` their inclusive sums; request
+// n_req for what lies behind the last list.  Each warp takes a run of whole 32s; `shift` moves the runs on
+// by as many warps, so that short lists are filled by warps of their own.  Returns the shift for the next.
+template <typename F>
+__device__ __forceinline__ uint32_t for_packed(const uint32_t* ends, int n_req, uint32_t n, uint32_t shift, F f) {
+  const uint32_t warps = gridDim.x * (kPlanThreads / 32), lane = threadIdx.x & 31;
+  const uint32_t run = ((n + 31) / 32 + warps - 1) / warps * 32, runs = run ? (n + run - 1) / run : 0;
+  const uint32_t mine = (blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5) + warps - shift % warps) % warps;
+  if (mine < runs) {
+    const uint32_t begin = mine * run, end = min(begin + run, n);
+    int b0 = warp_find_above(ends, 0, n_req, begin);
+    for (uint32_t x0 = begin; x0 < end; x0 += 128) {
+      const uint32_t x1 = min(x0 + 127, end - 1);
+      const int at = b0 + (int)lane;
+      const uint32_t above = __ballot_sync(0xffffffffu, at >= n_req || ends[at] > x1);
+      const int b1 = above ? min(b0 + __ffs(above) - 1, n_req) : warp_find_above(ends, b0 + 32, n_req, x1);
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t x = x0 + 32 * i + lane;
+        if (x < end) f(x, find_above(ends, b0, b1, x));
+      }
+      b0 = b1;
+    }
+  }
+  return shift + runs;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p) {
@@ -168,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   uint32_t* new_s = sm + 5 * B;        // tokens and completed rows of each request (a saturated sum
   uint32_t* done_s = sm + 6 * B;       // does not give them back)
   __shared__ uint32_t part[96];        // [3][32] the warps' sums
-  __shared__ unsigned long long placed_s;  // placed rows, summed by block 0
+  __shared__ unsigned long long placed_s[32];  // placed rows, by warp of block 0
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ps = 1 << p.log_page;
   const int cap = p.max_pages << p.log_page;
@@ -219,7 +261,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     part[32 + warp] = ic;
     part[64 + warp] = ig;
   }
-  if (tid == 0) placed_s = 0;
   __syncthreads();
   if (warp == 0) {
     uint32_t a = part[lane], b = part[32 + lane], e = part[64 + lane];
@@ -263,7 +304,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   // the request state has been read by every block before any block writes it
   if (gridDim.x > 1) cluster_sync(); else __syncthreads();
 
-  const uint32_t gtid = blockIdx.x * kPlanThreads + tid, gthreads = gridDim.x * kPlanThreads;
   auto pages_got = [&](int b, int& first) {
     first = (int)min(b > 0 ? page_end[b - 1] : 0u, (uint32_t)F);
     return (int)min(page_end[b], (uint32_t)F) - first;
@@ -274,13 +314,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   };
   auto held_pages = [&](int b) { return (rows_s[b] >> p.log_page) + ((rows_s[b] & (ps - 1)) != 0); };
 
-  for (uint32_t t = gtid; t < (uint32_t)p.T_cap; t += gthreads) {
-    const int b = find_above(tok_end, B, t);
+  uint32_t shift = for_packed(tok_end, B, (uint32_t)p.T_cap, 0, [&](uint32_t t, int b) {
     p.req[t] = b < B ? b : -1;
     p.positions[t] = b < B ? seen_s[b] + (int)(t - (b > 0 ? tok_end[b - 1] : 0u)) : -1;
-  }
-  for (uint32_t j = gtid; j < (uint32_t)p.R_cap; j += gthreads) {
-    const int b = find_above(row_end, B, j);
+  });
+  shift = for_packed(row_end, B, (uint32_t)p.R_cap, shift, [&](uint32_t j, int b) {
     int slot = -1;
     if (b < B) {
       const int i = (int)(j - (b > 0 ? row_end[b - 1] : 0u));
@@ -296,13 +334,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
       }
     }
     p.slots[j] = slot;
-  }
+  });
   const int taken = (int)min(page_end[B - 1], (uint32_t)F);
-  for (uint32_t k = gtid; k < (uint32_t)taken; k += gthreads) {
-    const int b = find_above(page_end, B, k);
+  for_packed(page_end, B, (uint32_t)taken, shift, [&](uint32_t k, int b) {
     const int first = (int)(b > 0 ? page_end[b - 1] : 0u);
     p.tables[(int64_t)b * p.max_pages + held_pages(b) + ((int)k - first)] = p.free_pages[F - 1 - (int)k];
-  }
+  });
   if (blockIdx.x == 0) {
     unsigned long long mine = 0;
     for (int b = tid; b < B; b += kPlanThreads) {
@@ -313,14 +350,17 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
       if (p.rows_out) p.rows_out[b] = rows_s[b] + pl;
       if (p.seen_out) p.seen_out[b] = seen_s[b] + (int)new_s[b];
     }
-    if (mine) atomicAdd(&placed_s, mine);  // integers: the order does not matter
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if (lane == 0) placed_s[warp] = mine;
     __syncthreads();
     if (tid == 0) {
+      for (int i = 1; i < 32; ++i) mine += placed_s[i];
       if (p.n_free_out) *p.n_free_out = F - taken;
       if (p.totals) {
         p.totals[0] = (int)tok_end[B - 1];
         p.totals[1] = (int)row_end[B - 1];
-        p.totals[2] = (int)min(placed_s, (unsigned long long)kSat);
+        p.totals[2] = (int)min(mine, (unsigned long long)kSat);
         p.totals[3] = taken;
       }
     }
