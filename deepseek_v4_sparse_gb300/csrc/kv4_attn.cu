@@ -232,29 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto oslot = [](uint32_t item, int db) { return (int)((4u * (item % 3u) + (uint32_t)db) % kOSlots); };
 
-  if (tid == 0) {
-    mbar_init(qfull, kDecWarps);
-    mbar_init(qempty, 1);
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&slfull[i], 1);
-      mbar_init(&slempty[i], kDecWarps);
-    }
-    for (int i = 0; i < 2 * kHalves; ++i) {
-      mbar_init(&kvfull[i], kDecWarps / 2);
-      mbar_init(&kvempty[i], 1);
-    }
-    for (int i = 0; i < kOSlots; ++i) {
-      mbar_init(&ofull[i], 1);
-      mbar_init(&oempty[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 2);  // the products' completion and the issuing warp itself
-      mbar_init(&sempty[i], 4);
-      mbar_init(&pfull[i], 4);
-      mbar_init(&pempty[i], 1);
-      mbar_init(&lready[i], 4);
-      mbar_init(&lfree[i], 4);
-    }
+  if (tid < kNumBars) {  // one barrier a thread
+    uint64_t* bar = qfull + tid;
+    const bool four = (bar >= sempty && bar < pempty) || bar >= oempty;  // by the softmax or the output warps
+    mbar_init(bar, bar == qfull ? kDecWarps
+                   : bar >= slempty && bar < kvfull ? kDecWarps
+                   : bar >= kvfull && bar < kvempty ? kDecWarps / kHalves
+                   : bar >= sfull && bar < sempty ? 2  // the products' completion and the issuing warp itself
+                   : four ? 4 : 1);
     fence_mbarrier_init();
   }
   if (warp == kSWarp) tmem_alloc(tmem_slot, kTmemCols);
@@ -281,14 +266,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     if (lane == 31) scan[warp] = incl;
     if (tid == 0) start[2] = 0;
     __syncthreads();
-    long long before = incl - sum, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-      const long long v = scan[w];
-      if (w < warp) before += v;
-      total += v;
+    long long before = lane < kWarps ? scan[lane] : 0;  // every warp scans the warps' sums
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
     }
-    const long long quota = (total + gridDim.x - 1) / gridDim.x;
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before = __shfl_sync(0xffffffffu, before, (warp + 31) & 31);
+    before = (warp > 0 ? before : 0) + incl - sum;
+    const long long quota = total >> 31 ? (total + gridDim.x - 1) / gridDim.x
+                                        : (long long)(((uint32_t)total + gridDim.x - 1u) / gridDim.x);
     const long long g0 = quota * blockIdx.x, g1 = min(total, g0 + quota);
     if (g0 < total) {
       long long at = before;
@@ -348,15 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       return got;
     };
     // q of token t as fp16 into the operand's layout; each warp 4 heads, 16-byte units lane and lane + 32
-    auto put_q = [&](int qt, uint32_t qi) {
-      const int h = warp * 4;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qt * kHq + h) * kKv4Dim) + lane;
-      uint4 u[4][2];
+    auto load_q = [&](int qt, uint4 (&u)[4][2]) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qt * kHq + warp * 4) * kKv4Dim) + lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         u[i][0] = __ldg(src + i * (kKv4Dim / 8));
         u[i][1] = __ldg(src + i * (kKv4Dim / 8) + 32);
       }
+    };
+    auto put_q = [&](uint4 (&u)[4][2], uint32_t qi) {
+      const int h = warp * 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float f = p.scale * 1.4426950408889634f;
@@ -393,10 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       return got;
     };
     const uint32_t chunks = start[2];
-    bool ok = chunks == 0 || load(0);
+    bool ok = true;
     uint32_t g = 0, item = 0;
     for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-      ok = put_q(w.t, item);
+      uint4 u[4][2];
+      load_q(w.t, u);
+      if (item == 0) ok = load(0);
+      ok = put_q(u, item) && ok;
 #pragma unroll 1
       for (int ci = w.c0; ci < w.c1 && ok; ++ci, ++g) {
         const int b = g & 1;
@@ -441,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       uint32_t gc = 0, item = 0;
       bool ok = true;
       const uint64_t q_desc = desc_sw128(smem_u32(sq), 16, 1024), kv_desc = desc_sw128(smem_u32(skv), 16, 1024);
-      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-        for (int c = w.c0; c < w.c1; ++c, ++gc) {
+      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+        for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
           if (!wait_bar_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 62)) { ok = false; break; }
           if (c == w.c0) {
@@ -474,22 +466,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       uint32_t gc = 0;
       bool ok = true;
       for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
-        const int t = w.t, n = rows_s[t], b = request_of(p, t);
-        const int held = n > 0 && p.indices ? __ldg(p.rows + b) : 0x7fffffff;
+        const int t = w.t, n = rows_s[t];
         const int32_t* list = p.indices ? p.indices + (int64_t)t * p.k_top : nullptr;
+        auto row_of = [&](int c, int i) {
+          const int j = c * kRows + lane + 32 * i;
+          return j >= 0 && j < n ? (list ? __ldg(list + j) : j) : -1;
+        };
+        int next[2] = {row_of(w.c0, 0), row_of(w.c0, 1)};  // on their way while the request is looked up
+        const int b = request_of(p, t);
+        const int held = n > 0 && list ? __ldg(p.rows + b) : 0x7fffffff;
         const int32_t* table = p.tables + (int64_t)(n > 0 ? b : 0) * p.max_pages;
         for (int c = w.c0; c < w.c1; ++c, ++gc) {
           int slot[2];
+          const int now[2] = {next[0], next[1]};
+          if (c + 1 < w.c1) {
+            next[0] = row_of(c + 1, 0);
+            next[1] = row_of(c + 1, 1);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int j = c * kRows + lane + 32 * i;
-            const int row = j >= 0 && j < n ? (list ? __ldg(list + j) : j) : -1;
+            const int row = now[i];
             const int pg = row >> p.log_page;
             slot[i] = -1;
-            if (row >= 0 && row < held && pg < p.max_pages) {
+            if (row >= 0 && pg < p.max_pages) {  // the table is read while the rows held are on their way
               const int page = __ldg(table + pg);
               const int64_t at = ((int64_t)page << p.log_page) + (row & ((1 << p.log_page) - 1));
-              if (page >= 0 && at < p.n_slots) slot[i] = (int)at;
+              if (page >= 0 && at < p.n_slots && row < held) slot[i] = (int)at;
             }
           }
           const uint32_t m0 = __ballot_sync(0xffffffffu, slot[0] >= 0), m1 = __ballot_sync(0xffffffffu, slot[1] >= 0);
@@ -510,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
       bool ok = true;
       const uint64_t v_desc = desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_desc = desc_sw128(smem_u32(sp), 16, 1024);
-      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-        for (int c = w.c0; c < w.c1; ++c, ++gc) {
+      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+        for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
           if (!wait_bar_warp(&pfull[b], (gc >> 1) & 1, p.status, 65)) { ok = false; break; }
           tc_fence_after();
@@ -769,56 +771,94 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
 }
 
 // Joins the parts of a token that several blocks worked on (one block per boundary between two of them
-// and head, 4 dims a thread): part i holds O_i = sum_j 2^(x_j - m_i) kv_j and the sums r_i of its rounded
-// weights and l_i of the exact ones, so with M = max_i m_i
+// and head): part i holds O_i = sum_j 2^(x_j - m_i) kv_j and the sums r_i of its rounded weights and l_i of
+// the exact ones, so with M = max_i m_i
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) r_i,   lse = ln 2 (M + log2 sum_i 2^(m_i - M) l_i).
-// The parts are added in the order of the blocks: the same bits on every run.
-template <bool kBf16>
-__global__ void __launch_bounds__(kKv4Dim / 4) kv4_combine_kernel(const int4* __restrict__ parts_of,
-                                                                  const float* __restrict__ part,
-                                                                  const float* __restrict__ stat, uint16_t* out,
-                                                                  float* lse) {
+// 128 threads hold 4 dims each; kGroups such groups take the parts in turn and are added up at the end, in
+// an order that depends on the parts' number alone: the same bits on every run.  One group where a token has
+// two parts or three (67 tokens: 29 us in all, 34 us with four), four where it may have many (one token with
+// 126 parts: 36 us in all, 61 us with one).
+constexpr int kMaxParts = 256;
+template <bool kBf16, int kGroups>
+__global__ void __launch_bounds__(kGroups * kKv4Dim / 4)
+    kv4_combine_kernel(const int4* __restrict__ parts_of, const float* __restrict__ part, const float* __restrict__ stat,
+                       uint16_t* out, float* lse) {
+  constexpr int kLane4 = kKv4Dim / 4;
+  __shared__ float weight[kMaxParts], sums[2];
+  __shared__ float4 acc_s[kGroups > 1 ? kGroups - 1 : 1][kLane4];
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x + 1, h = blockIdx.y;
+  const int i = blockIdx.x + 1, h = blockIdx.y, tid = threadIdx.x;
   const int4 at = parts_of[i];  // token, its chunks before block i, its chunks, a block's chunks
   // the boundary before block i joins a token only if it is the first that the token crosses
   if (at.x < 0 || at.y == 0 || at.y > at.w) return;
   const int n = 1 + (at.z - at.y + at.w - 1) / at.w;  // parts: block i - 1's second, then the first ones
   auto part_no = [&](int k) { return k == 0 ? 2 * (int64_t)(i - 1) + 1 : 2 * (int64_t)(i - 1 + k); };
   float mx = -INFINITY;
-  for (int k = 0; k < n; ++k) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
-  float r = 0.f, l = 0.f;
+  if (tid < 32) {
+    for (int k = tid; k < n; k += 32) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float r = 0.f, l = 0.f;
+    for (int k = tid; k < n; k += 32) {
+      const float* st = stat + part_no(k) * kStatFloats;
+      const float m = st[2 * kHq + h];
+      const float f = mx == -INFINITY ? 1.f : exp2f(m - mx);  // without a maximum all is 0 (or NaN)
+      weight[k] = f;
+      r += f * st[h];
+      l += f * st[kHq + h];
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      r += __shfl_xor_sync(0xffffffffu, r, d);
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+    }
+    if (tid == 0) {
+      sums[0] = r == 0.f ? 0.f : 1.f / r;
+      if (lse)
+        lse[(int64_t)at.x * kHq + h] =
+            l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx) + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
+    }
+  }
+  __syncthreads();
+  const int group = tid / kLane4, x = tid % kLane4;
+  const float4* src = reinterpret_cast<const float4*>(part + h * kKv4Dim) + x;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* st = stat + part_no(k) * kStatFloats;
-    const float4 o = *reinterpret_cast<const float4*>(part + part_no(k) * kPartFloats + h * kKv4Dim + 4 * threadIdx.x);
-    const float m = st[2 * kHq + h];
-    const float f = mx == -INFINITY ? 1.f : exp2f(m - mx);  // without a maximum all is 0 (or NaN)
-    r += f * st[h];
-    l += f * st[kHq + h];
+#pragma unroll 8
+  for (int k = group; k < n; k += kGroups) {
+    const float4 o = src[part_no(k) * (kPartFloats / 4)];
+    const float f = weight[k];
     acc.x += f * o.x;
     acc.y += f * o.y;
     acc.z += f * o.z;
     acc.w += f * o.w;
   }
-  const float inv = r == 0.f ? 0.f : 1.f / r;
+  if constexpr (kGroups > 1) {
+    if (group > 0) acc_s[group - 1][x] = acc;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float4 o = acc_s[k][x];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+  }
+  const float inv = sums[0];
   const uint32_t lo = pack16<kBf16>(acc.x * inv, acc.y * inv), hi = pack16<kBf16>(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h) * kKv4Dim + 4 * threadIdx.x) = make_uint2(lo, hi);
-  if (threadIdx.x == 0 && lse)
-    lse[(int64_t)at.x * kHq + h] =
-        l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx) + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
+  *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h) * kKv4Dim + 4 * x) = make_uint2(lo, hi);
 }
 
 // Blocks for T tokens of up to max_rows rows: one an SM, at most one a chunk.
 int grid_of(int T, int max_rows) {
   const int64_t chunks = (int64_t)T * (max_rows > kRows ? (max_rows - 1) / kRows + 1 : 1);
   const int sms = device_sm_count();
-  return (int)(chunks < sms ? chunks : sms);
+  const int64_t most = sms < kMaxParts ? sms : kMaxParts;  // a token has at most a part of every block
+  return (int)(chunks < most ? chunks : most);
 }
-constexpr size_t kHeadBytes = 4096;  // the int4 of every block
-static_assert(kHeadBytes / 16 >= 256, "blocks a launch may have");
+constexpr size_t kHeadBytes = 16 * kMaxParts;  // the int4 of every block
 
 }  // namespace
 
@@ -862,8 +902,11 @@ static int launch_typed(const Kv4AttnArgs& a, int max_rows, cudaStream_t stream)
       return DS4X_ERR_CUDA;
     count_launch();
     if (grid > 1 && max_rows > kRows) {  // a token of one chunk is never split
-      if (launch_pdl(kv4_combine_kernel<kBf16>, dim3(grid - 1, kHq), dim3(kKv4Dim / 4), 0, stream,
-                     (const int4*)p.parts_of, (const float*)p.part, (const float*)p.stat, p.out, p.lse) != cudaSuccess)
+      // blocks a token on average; with four or more, some tokens have many parts
+      const bool few = 4 * p.T < grid;
+      if (launch_pdl(few ? kv4_combine_kernel<kBf16, 4> : kv4_combine_kernel<kBf16, 1>, dim3(grid - 1, kHq),
+                     dim3((few ? 4 : 1) * kKv4Dim / 4), 0, stream, (const int4*)p.parts_of, (const float*)p.part,
+                     (const float*)p.stat, p.out, p.lse) != cudaSuccess)
         return DS4X_ERR_CUDA;
       count_launch();
     }
