@@ -449,7 +449,8 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   const int64_t fill = (int64_t)T_cap + R_cap;
   const int blocks = fill <= 4 * kPlanThreads ? 1 : kPlanCluster;
   const size_t smem = (size_t)7 * n_req * sizeof(uint32_t);
-  if (ensure_dynamic_smem(page_plan_kernel, 7 * DS4X_MAX_REQ * 4) != cudaSuccess) return DS4X_ERR_CUDA;
+  if (smem > 48 * 1024 && ensure_dynamic_smem(page_plan_kernel, 7 * DS4X_MAX_REQ * 4) != cudaSuccess)
+    return DS4X_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kPlanThreads);
@@ -463,7 +464,7 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, page_plan_kernel, p) != cudaSuccess) return DS4X_ERR_CUDA;
   count_launch();
   return call_end(DS4X_OK);
