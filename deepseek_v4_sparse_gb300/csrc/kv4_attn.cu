@@ -133,6 +133,31 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// D (+)= A B^T by an elected lane of a converged warp; descriptors by their low words (the addresses): the
+// high words are the same for all operands here.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool kAdd>
+__device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (kAdd)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
+        : "memory");
+}
+
 __device__ __forceinline__ int request_of(const Params& p, int t) { return p.req ? __ldg(p.req + t) : p.t0 + t; }
 
 // Rows in the list of token t (selected: list entries; else visible rows).
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       // ------------------------------------------------------------------------ S = Q K^T
       uint32_t gc = 0, item = 0;
       bool ok = true;
-      const uint64_t q_desc = desc_sw128(smem_u32(sq), 16, 1024), kv_desc = desc_sw128(smem_u32(skv), 16, 1024);
+      const uint32_t q_lo = (uint32_t)desc_sw128(smem_u32(sq), 16, 1024), kv_lo = (uint32_t)desc_sw128(smem_u32(skv), 16, 1024);
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
@@ -445,14 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           for (int half = 0; half < kHalves; ++half) {
             if (!wait_bar_warp(&kvfull[b * kHalves + half], (gc >> 1) & 1, p.status, 64)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t a0 = q_desc + half * (4 * kQBlockBytes >> 4);
-            const uint64_t b0 = kv_desc + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
+            const uint32_t a = q_lo + half * (4 * kQBlockBytes >> 4), k = kv_lo + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
+            mma_elect<false>(tmem + b * kHq, a, k, kIdescS, half);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_f16_elect(tmem + b * kHq, a0 + (kb * kQBlockBytes + kk * 32 >> 4), b0 + (kb * kSlotBytes + kk * 32 >> 4),
-                                 kIdescS, half | kb | kk);
+            for (int i = 1; i < 16; ++i)
+              mma_elect<true>(tmem + b * kHq, a + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
+                              k + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), kIdescS, 1);
           }
           if (!ok) break;
           if (c == w.c1 - 1) tc_commit_elect(qempty);  // the next item's q may replace this one's
@@ -511,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       uint32_t gc = 0, item = 0;
       uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
       bool ok = true;
-      const uint64_t v_desc = desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_desc = desc_sw128(smem_u32(sp), 16, 1024);
+      const uint32_t v_lo = (uint32_t)desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_lo = (uint32_t)desc_sw128(smem_u32(sp), 16, 1024);
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
@@ -526,10 +549,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
               o_ph ^= 1u << os;
               tc_fence_after();
             }
-            const uint64_t a0 = v_desc + (b * kBufBytes + 2 * db * kSlotBytes >> 4), b0 = p_desc + (b * kPBytes >> 4);
+            const uint32_t a = v_lo + (b * kBufBytes + 2 * db * kSlotBytes >> 4), k = p_lo + (b * kPBytes >> 4);
+            mma_elect<false>(tmem + kColO + os * kHq, a, k, kIdescO, c > w.c0);
 #pragma unroll
-            for (int ks = 0; ks < kRows / 16; ++ks)
-              tc_mma_f16_elect(tmem + kColO + os * kHq, a0 + (ks * 2048 >> 4), b0 + (ks * 32 >> 4), kIdescO, c > w.c0 || ks > 0);
+            for (int ks = 1; ks < kRows / 16; ++ks)
+              mma_elect<true>(tmem + kColO + os * kHq, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             if (db & 1) tc_commit_elect(&kvempty[b * kHalves + (db >> 1)]);  // this half of the chunk is free
             if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
           }
