@@ -794,43 +794,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
   }
 }
 
-// Joins the parts of a token that several blocks worked on (one block per boundary between two of them
-// and head): part i holds O_i = sum_j 2^(x_j - m_i) kv_j and the sums r_i of its rounded weights and l_i of
-// the exact ones, so with M = max_i m_i
-//   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) r_i,   lse = ln 2 (M + log2 sum_i 2^(m_i - M) l_i).
-// 128 threads hold 4 dims each; kGroups such groups take the parts in turn and are added up at the end, in
-// an order that depends on the parts' number alone: the same bits on every run.  One group where a token has
-// two parts or three (67 tokens: 29 us in all, 34 us with four), four where it may have many (one token with
-// 126 parts: 36 us in all, 61 us with one).
+// Joins the parts of a token that several blocks worked on: part k holds O_k = sum_j 2^(x_j - m_k) kv_j and
+// the sums r_k of its rounded weights and l_k of the exact ones, so with M = max_k m_k
+//   out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) r_k,   lse = ln 2 (M + log2 sum_k 2^(m_k - M) l_k).
+// A thread holds 4 dims; kGroups groups of threads take the parts in turn and are added up at the end, in
+// an order that depends on the parts' number alone: the same bits on every run.
+//   Many tokens (two or three parts each): a block per boundary between two blocks and four heads, one group
+//   of 128 threads a head.
+//   Few tokens (one may have a part of every block): a block per token, head and kDimBlocks-th of the dims,
+//   eight groups.  A block that finds nothing to join costs its launch: 9664 of them about as much as the
+//   joining.
 constexpr int kMaxParts = 256;
-template <bool kBf16, int kGroups>
-__global__ void __launch_bounds__(kGroups * kKv4Dim / 4)
-    kv4_combine_kernel(const int4* __restrict__ parts_of, const float* __restrict__ part, const float* __restrict__ stat,
-                       uint16_t* out, float* lse) {
-  constexpr int kLane4 = kKv4Dim / 4;
-  __shared__ float weight[kMaxParts], sums[2];
+template <bool kBf16, bool kByToken, int kGroups, int kHeads, int kDimBlocks>
+__global__ void __launch_bounds__(kGroups * kHeads * kKv4Dim / 4 / kDimBlocks)
+    kv4_combine_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
+                       const float* __restrict__ stat, uint16_t* out, float* lse) {
+  constexpr int kLane4 = kKv4Dim / 4 / kDimBlocks, kTeam = kGroups * kLane4;
+  static_assert(kTeam >= 32 && (kHeads == 1 || kGroups == 1), "a team's first warp takes its statistics");
+  __shared__ float weight[kHeads][kMaxParts], inv_s[kHeads];
   __shared__ float4 acc_s[kGroups > 1 ? kGroups - 1 : 1][kLane4];
+  __shared__ int found;
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x + 1, h = blockIdx.y, tid = threadIdx.x;
-  const int4 at = parts_of[i];  // token, its chunks before block i, its chunks, a block's chunks
-  // the boundary before block i joins a token only if it is the first that the token crosses
-  if (at.x < 0 || at.y == 0 || at.y > at.w) return;
+  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, h = blockIdx.y * kHeads + team;
+  // block i's entry: the token it starts in, its chunks before the block, its chunks, a block's chunks.  The
+  // first block that a token reaches into tells all about it.
+  int i = blockIdx.x + 1;
+  auto joins_at = [](int4 at) { return at.x >= 0 && at.y > 0 && at.y <= at.w; };
+  if constexpr (kByToken) {
+    if (threadIdx.x == 0) found = 0;
+    __syncthreads();
+    for (int k = 1 + threadIdx.x; k < blocks; k += blockDim.x) {
+      const int4 at = parts_of[k];
+      if (at.x == (int)blockIdx.x && joins_at(at)) found = k;  // there is one at most
+    }
+    __syncthreads();
+    i = found;
+    if (i == 0) return;
+  }
+  const int4 at = parts_of[i];
+  if (!joins_at(at)) return;
   const int n = 1 + (at.z - at.y + at.w - 1) / at.w;  // parts: block i - 1's second, then the first ones
   auto part_no = [&](int k) { return k == 0 ? 2 * (int64_t)(i - 1) + 1 : 2 * (int64_t)(i - 1 + k); };
-  float mx = -INFINITY;
   if (tid < 32) {
+    float mx = -INFINITY, r = 0.f, l = 0.f;
     for (int k = tid; k < n; k += 32) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    float r = 0.f, l = 0.f;
     for (int k = tid; k < n; k += 32) {
-      const float* st = stat + part_no(k) * kStatFloats;
-      const float m = st[2 * kHq + h];
+      const float* st = stat + part_no(k) * kStatFloats + h;
+      const float m = st[2 * kHq];
       const float f = mx == -INFINITY ? 1.f : exp2f(m - mx);  // without a maximum all is 0 (or NaN)
-      weight[k] = f;
-      r += f * st[h];
-      l += f * st[kHq + h];
+      weight[team][k] = f;
+      r += f * st[0];
+      l += f * st[kHq];
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
@@ -838,39 +855,39 @@ __global__ void __launch_bounds__(kGroups * kKv4Dim / 4)
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
     if (tid == 0) {
-      sums[0] = r == 0.f ? 0.f : 1.f / r;
-      if (lse)
+      inv_s[team] = r == 0.f ? 0.f : 1.f / r;
+      if (lse && blockIdx.z == 0)
         lse[(int64_t)at.x * kHq + h] =
             l == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx) + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
-  const int group = tid / kLane4, x = tid % kLane4;
+  const int group = tid / kLane4, lane4 = tid % kLane4, x = blockIdx.z * kLane4 + lane4;
   const float4* src = reinterpret_cast<const float4*>(part + h * kKv4Dim) + x;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int k = group; k < n; k += kGroups) {
     const float4 o = src[part_no(k) * (kPartFloats / 4)];
-    const float f = weight[k];
+    const float f = weight[team][k];
     acc.x += f * o.x;
     acc.y += f * o.y;
     acc.z += f * o.z;
     acc.w += f * o.w;
   }
   if constexpr (kGroups > 1) {
-    if (group > 0) acc_s[group - 1][x] = acc;
+    if (group > 0) acc_s[group - 1][lane4] = acc;
     __syncthreads();
     if (group > 0) return;
 #pragma unroll
     for (int k = 0; k < kGroups - 1; ++k) {
-      const float4 o = acc_s[k][x];
+      const float4 o = acc_s[k][lane4];
       acc.x += o.x;
       acc.y += o.y;
       acc.z += o.z;
       acc.w += o.w;
     }
   }
-  const float inv = sums[0];
+  const float inv = inv_s[team];
   const uint32_t lo = pack16<kBf16>(acc.x * inv, acc.y * inv), hi = pack16<kBf16>(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h) * kKv4Dim + 4 * x) = make_uint2(lo, hi);
 }
@@ -926,12 +943,19 @@ static int launch_typed(const Kv4AttnArgs& a, int max_rows, cudaStream_t stream)
       return DS4X_ERR_CUDA;
     count_launch();
     if (grid > 1 && max_rows > kRows) {  // a token of one chunk is never split
-      // blocks a token on average; with four or more, some tokens have many parts
-      const bool few = 4 * p.T < grid;
-      if (launch_pdl(few ? kv4_combine_kernel<kBf16, 4> : kv4_combine_kernel<kBf16, 1>, dim3(grid - 1, kHq),
-                     dim3((few ? 4 : 1) * kKv4Dim / 4), 0, stream, (const int4*)p.parts_of, (const float*)p.part,
-                     (const float*)p.stat, p.out, p.lse) != cudaSuccess)
-        return DS4X_ERR_CUDA;
+      const int4* po = p.parts_of;
+      const float *pp = p.part, *ps = p.stat;
+      cudaError_t e;
+      if (4 * p.T < grid && p.T < 8)  // few tokens: four blocks a head fill more of the GPU
+        e = launch_pdl(kv4_combine_kernel<kBf16, true, 8, 1, 4>, dim3(p.T, kHq, 4), dim3(256), 0, stream, po, grid, pp,
+                       ps, p.out, p.lse);
+      else if (4 * p.T < grid)
+        e = launch_pdl(kv4_combine_kernel<kBf16, true, 4, 1, 1>, dim3(p.T, kHq), dim3(512), 0, stream, po, grid, pp, ps,
+                       p.out, p.lse);
+      else
+        e = launch_pdl(kv4_combine_kernel<kBf16, false, 1, 4, 1>, dim3(grid - 1, kHq / 4), dim3(512), 0, stream, po,
+                       grid, pp, ps, p.out, p.lse);
+      if (e != cudaSuccess) return DS4X_ERR_CUDA;
       count_launch();
     }
   }
