@@ -26,12 +26,14 @@
 // decoded: the fetching warps wait for a buffer then, and have it converted when the products of the token
 // before are done with theirs.  It is brought to L2 an item ahead.
 //
-// What bounds it: the data path of L1 and shared memory, one 128-byte access a clock for the products and
-// the warps together.  A chunk of a 2048-token prefill takes 1790 accesses of the products (128 KB of S
-// operands, 96 KB of O^T operands) and 1890 of the warps (512 of them the decoded stores), 92 % of its
-// time: 224 us for 2048 tokens of 512 rows (613 TFLOP/s, 32 % of the measured peak; a gather that reads a
-// row's codes in 16 lines instead of whole 128-byte lines, and looks the slots up in every warp: 247 us).
-// Three buffers of 48 rows, a shorter chain a chunk but a third more S time a row, took 272 us.
+// What bounds it: a chunk's way through the roles (fetch, S, softmax, O^T, release), two chunks at a time,
+// and the data path of L1 and shared memory, one 128-byte access a clock for the products and the warps
+// together: a chunk takes 1790 accesses of the products (128 KB of S operands, 96 KB of O^T operands) and
+// 1880 of the warps (512 of them the decoded stores) in about 3950 clocks.  219 us for 2048 tokens of 512
+// rows: 627 TFLOP/s, 33 % of the measured peak.  With three quarters of the products left out it took 189 us,
+// without fetches and stores 200 us, with neither and without 2^x 168 us: most is the hand-overs.  Slower:
+// three buffers of 48 rows (272 us: S products cost nearly the same at 48 rows as at 64), rows in 16 lines a
+// load and slots looked up in every warp (247 us), rows by bulk copies into a stage of their own (345 us).
 //
 // The running maximum of a head moves only when a logit exceeds it by more than 2^11 (O^T's column and
 // the sums are rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them
@@ -79,9 +81,10 @@ constexpr int kOffCq = kOffLM + 2 * 4 * kHq * 4; // float[kItems][64]: logit fac
 constexpr int kOffRows = kOffCq + kItems * kHq * 4;  // int[kTokens]: rows of each token's list
 constexpr int kOffMask = kOffRows + kTokens * 4; // uint32[kMaskRing][2]: rows of the chunk that count
 constexpr int kOffSlots = kOffMask + kMaskRing * 8;  // int[kRing][64]: slot of each row of the chunk, -1 for none
-constexpr int kOffScan = kOffSlots + kRing * kRows * 4;         // int64[kWarps] warp sums, then int[4]: the block's part
+constexpr int kOffScan = kOffSlots + kRing * kRows * 4;         // int64[kWarps] warp sums, then int[4]: the block's part, and
+                                                 // the last chunk (+ 1) in which a maximum moved
 constexpr int kOffBars = kOffScan + kWarps * 8 + 16;
-constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 4 * 2 + 2 * kOSlots + 2 * 2;
+constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 5 * 2 + 2 * kOSlots + 2 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -248,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
   uint64_t* sempty = sfull + 2;
   uint64_t* pfull = sempty + 2;
   uint64_t* pempty = pfull + 2;
-  uint64_t* ofull = pempty + 2;             // [O^T slot]
+  uint64_t* looked = pempty + 2;            // every softmax warp has seen whether its maxima move
+  uint64_t* ofull = looked + 2;             // [O^T slot]
   uint64_t* oempty = ofull + kOSlots;       // [O^T slot]
   uint64_t* lready = oempty + kOSlots;      // [item parity] statistics written
   uint64_t* lfree = lready + 2;             // [item parity] ... and read
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
 
   if (tid < kNumBars) {  // one barrier a thread
     uint64_t* bar = qfull + tid;
-    const bool four = (bar >= sempty && bar < pempty) || bar >= oempty;  // by the softmax or the output warps
+    const bool four = (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || bar >= oempty;  // by the softmax or the output warps
     mbar_init(bar, bar == qfull ? kDecWarps
                    : bar >= slempty && bar < kvfull ? kDecWarps
                    : bar >= kvfull && bar < kvempty ? kDecWarps / kHalves
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       if (lane >= d) incl += o;
     }
     if (lane == 31) scan[warp] = incl;
-    if (tid == 0) start[2] = 0;
+    if (tid == 0) start[2] = start[3] = 0;
     __syncthreads();
     long long before = lane < kWarps ? scan[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
@@ -629,7 +633,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           aB = needB ? ex2_approx(mB - mxB) : 0.f;
           mB = mxB;
         }
-        if (named_or(kSoftBar, kGroupThreads, needA || needB || !ok)) {
+        // whether any head's maximum moves is said now and asked for when the weights are ready (the same
+        // answer in all four warps: a later chunk's word is written after all have read this one's)
+        const bool moved = __any_sync(0xffffffffu, needA || needB || !ok);
+        if (lane == 0) {
+          if (moved) *const_cast<volatile int*>(start + 3) = (int)(gc + 1);
+          mbar_arrive(&looked[b]);
+        }
+        lA *= aA;
+        rA *= aA;
+        lB *= aB;
+        rB *= aB;
+        // weights 2^(x - m + 4), rounded to fp16 for the product
+        const float nA = kWeightLog2 - (mA == -INFINITY ? 0.f : mA);
+        const float nB = kWeightLog2 - (mB == -INFINITY ? 0.f : mB);
+        uint32_t pkA[8], pkB[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float a0 = ex2_approx(x[4 * r] + nA), a1 = ex2_approx(x[4 * r + 1] + nA);
+          const float b0 = ex2_approx(x[4 * r + 2] + nB), b1 = ex2_approx(x[4 * r + 3] + nB);
+          const __half2 hp = __floats2half2_rn(a0, a1), hq = __floats2half2_rn(b0, b1);
+          lA += a0 + a1;
+          lB += b0 + b1;
+          add_halves(rA, hp);
+          add_halves(rB, hq);
+          pkA[r] = *reinterpret_cast<const uint32_t*>(&hp);
+          pkB[r] = *reinterpret_cast<const uint32_t*>(&hq);
+        }
+        ok = ok && wait_bar_warp(&looked[b], (gc >> 1) & 1, p.status, 75);
+        if (*const_cast<volatile int*>(start + 3) == (int)(gc + 1)) {
           leave = named_or(kSoftBar, kGroupThreads, !ok);
           if (leave) break;
           if (e == 0) {
@@ -653,26 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           }
           tc_wait_st();
           named_sync(kSoftBar, kGroupThreads);
-        }
-        lA *= aA;
-        rA *= aA;
-        lB *= aB;
-        rB *= aB;
-        // weights 2^(x - m + 4), rounded to fp16 for the product
-        const float nA = kWeightLog2 - (mA == -INFINITY ? 0.f : mA);
-        const float nB = kWeightLog2 - (mB == -INFINITY ? 0.f : mB);
-        uint32_t pkA[8], pkB[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float a0 = ex2_approx(x[4 * r] + nA), a1 = ex2_approx(x[4 * r + 1] + nA);
-          const float b0 = ex2_approx(x[4 * r + 2] + nB), b1 = ex2_approx(x[4 * r + 3] + nB);
-          const __half2 hp = __floats2half2_rn(a0, a1), hq = __floats2half2_rn(b0, b1);
-          lA += a0 + a1;
-          lB += b0 + b1;
-          add_halves(rA, hp);
-          add_halves(rB, hq);
-          pkA[r] = *reinterpret_cast<const uint32_t*>(&hp);
-          pkB[r] = *reinterpret_cast<const uint32_t*>(&hq);
         }
         ok = ok && wait_bar_warp(&pempty[b], ((gc >> 1) & 1) ^ 1, p.status, 69);
         {
