@@ -11,8 +11,9 @@
 // (at most 4096 of them: cheaper than handing them over through memory) and then fills its share of the
 // outputs: a warp takes a run of neighbouring elements, finds the request of the first by a search in which
 // each lane looks at one place (three steps for 4096), and from there on the requests of 128 elements at a
-// time, between which a lane searches.  The blocks are one cluster, whose barrier separates the reads of
-// the request state from its (in place) update.
+// time, between which a lane searches.  Where the state is updated in place the blocks are one cluster,
+// whose barrier separates its reads from the update (17 us for 1500 requests with 96000 tokens on eight
+// blocks); otherwise there are as many as have something to fill (7 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -132,13 +133,14 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
 // ------------------------------------------------------------------------------------ step plan
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = DS4X_MAX_REQ / kPlanThreads;  // requests a thread sums up
-constexpr int kPlanCluster = 8;
+constexpr int kPlanCluster = 8, kPlanBlocks = 64;
 constexpr uint32_t kSat = 0x7fffffffu;
 
 struct PlanParams {
   const int32_t *seen, *n_new, *rows, *free_pages, *n_free;
   int32_t *tables, *positions, *req, *slots, *seen_out, *rows_out, *n_free_out, *totals;
   int n_req, ratio, log_page, max_pages, free_cap, T_cap, R_cap;
+  int in_place;  // an output is its input: with more than one block they are a cluster
 };
 
 // Sums of counts stay at kSat once they reach it (associative, so a scan may use it).
@@ -301,8 +303,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
       }
     }
   }
-  // the request state has been read by every block before any block writes it
-  if (gridDim.x > 1) cluster_sync(); else __syncthreads();
+  // updated in place, the request state has been read by every block before any block writes it
+  if (p.in_place && gridDim.x > 1) cluster_sync(); else __syncthreads();
 
   auto pages_got = [&](int b, int& first) {
     first = (int)min(b > 0 ? page_end[b - 1] : 0u, (uint32_t)F);
@@ -444,10 +446,11 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   while ((1 << log_page) < page_rows) ++log_page;
   const PlanParams p{seen,     n_new,    rows,       free_pages, n_free,  tables, positions, req,       slots,
                      seen_out, rows_out, n_free_out, totals,     n_req,   ratio,  log_page,  max_pages, free_capacity,
-                     T_cap,    R_cap};
-  // one block while it has at most four elements a thread to fill, else a cluster of eight
-  const int64_t fill = (int64_t)T_cap + R_cap;
-  const int blocks = fill <= 4 * kPlanThreads ? 1 : kPlanCluster;
+                     T_cap,    R_cap,    seen == seen_out || rows == rows_out || n_free == n_free_out};
+  // four elements a thread to fill, if the blocks need not wait for one another
+  const int64_t want = ((int64_t)T_cap + R_cap + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const int most = p.in_place ? kPlanCluster : kPlanBlocks;
+  const int blocks = want <= 1 ? 1 : p.in_place || want > most ? most : (int)want;
   const size_t smem = (size_t)7 * n_req * sizeof(uint32_t);
   if (smem > 48 * 1024 && ensure_dynamic_smem(page_plan_kernel, 7 * DS4X_MAX_REQ * 4) != cudaSuccess)
     return DS4X_ERR_CUDA;
@@ -464,7 +467,7 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  cfg.numAttrs = p.in_place && blocks > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, page_plan_kernel, p) != cudaSuccess) return DS4X_ERR_CUDA;
   count_launch();
   return call_end(DS4X_OK);

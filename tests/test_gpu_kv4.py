@@ -143,6 +143,21 @@ def test_page_plan(B, max_pages, ps, ratio, hi_new, spare):
     check_plan(run_plan(c), kv4.page_plan(*c))
 
 
+@pytest.mark.parametrize("B,max_pages,ps,ratio,hi_new,spare", [
+    (1000, 6, 4, 7, 60, 4000), (33, 7, 16, 128, 3000, 0), (5, 40, 64, 4, 5000, 200),
+])
+def test_page_plan_in_place_over_several_blocks(B, max_pages, ps, ratio, hi_new, spare):
+    """The state's outputs are its inputs, with more to fill than one block takes."""
+    rng = np.random.default_rng(B + 1)
+    c = plan_case(rng, B, max_pages, ps, ratio, hi_new, spare)
+    seen, new, rows, tables, free, n_free, ratio, ps, T_cap, R_cap = c
+    d = [i32(x) for x in (seen, new, rows, tables, free, [n_free])]
+    out = ds4x.page_plan(*d, ratio, ps, T_cap, R_cap, seen_out=d[0], rows_out=d[2], n_free_out=d[5])
+    p, r, s, _, _, _, to = (x.cpu().numpy() for x in out)
+    got = (p, r, s, d[3].cpu().numpy(), d[0].cpu().numpy(), d[2].cpu().numpy(), d[5].cpu().numpy()[0], to)
+    check_plan(got, kv4.page_plan(*c))
+
+
 def test_page_plan_short_outputs_and_odd_state():
     rng = np.random.default_rng(3)
     c = plan_case(rng, 40, 3, 8, 4, 50, 20, T_cap=100, R_cap=13)          # packed outputs cut off
