@@ -443,6 +443,8 @@ int ds4x_kv4_read(const uint8_t* codes, const uint8_t* scales, int32_t n_slots, 
  *   workspace: at least ds4x_kv4_attn_workspace_bytes(T, max_rows) bytes, max_rows = k_top, or
  *   max_pages * page_rows without indices (may be NULL when that is 0).  Nothing is kept in it
  *   between calls; calls that may overlap on the GPU need one each.
+ *   The same arguments give the same bits on every run.  A call may be captured into a CUDA graph
+ *   after a first call on the device.
  * ------------------------------------------------------------------------- */
 int ds4x_kv4_attn(const void* q_attn, ds4x_dtype dtype, const uint8_t* codes, const uint8_t* scales,
                   int32_t n_slots, const int32_t* tables, const int32_t* rows, int32_t n_req,
