@@ -742,7 +742,7 @@ def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, posi
     elif counts is not None:
         raise ValueError("counts belong to indices")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(q_attn)
     elif out.shape != shape:
         raise ValueError(f"out must be of shape {tuple(shape)}, got {tuple(out.shape)}")
     if lse is None:

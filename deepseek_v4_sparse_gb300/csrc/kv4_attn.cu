@@ -101,7 +101,8 @@ struct Params {
   uint16_t* out;
   float* lse;
   int* status;
-  int4* parts_of;  // [grid]: the token a block starts in, chunks of it before the block, chunks it has, quota
+  int4* parts_of;  // [grid]: the token a block starts in, chunks of it before the block, chunks it has, quota;
+                   // NULL without a workspace, when there can be no rows at all
   float* part;     // [2 grid][kPartFloats]
   float* stat;     // [2 grid][kStatFloats]
   int n_slots, n_req, max_pages, log_page, ratio, t0, T, k_top;
@@ -316,11 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           start[0] = t;
           start[1] = (int)(g0 - at);
           start[2] = (int)(g1 - g0);
-          p.parts_of[blockIdx.x] = make_int4(t, (int)(g0 - at), nch, (int)quota);
+          if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(t, (int)(g0 - at), nch, (int)quota);
         }
         at += nch;
       }
-    } else if (tid == 0) {
+    } else if (tid == 0 && p.parts_of) {
       p.parts_of[blockIdx.x] = make_int4(-1, 0, 0, (int)quota);
     }
   }
@@ -1024,7 +1025,7 @@ int ds4x_kv4_attn(const void* q_attn, ds4x_dtype dtype, const uint8_t* codes, co
   const Kv4AttnArgs a{q_attn, dtype == DS4X_BF16 ? 1 : 0, codes,     scales,    n_slots, tables,
                       rows,   n_req,                      max_pages, log_page,  req,     positions,
                       ratio,  indices,                    counts,    T,         k_top,   scale,
-                      out,    lse,                        workspace};
+                      out,    lse,                        need > 0 ? workspace : nullptr};
   return call_end(launch_kv4_attn(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -440,6 +440,7 @@ int ds4x_kv4_read(const uint8_t* codes, const uint8_t* scales, int32_t n_slots, 
  *
  *   q_attn, out [T, Hq, Dkv] of `dtype`; lse [T, Hq] fp32 or NULL; indices [T, k_top], counts [T],
  *   req [T], positions [T], rows [n_req] int32.  Hq = 64, Dkv = 512, 1 <= k_top <= DS4X_MAX_KTOP.
+ *   out and lse overlap no input.
  *   workspace: at least ds4x_kv4_attn_workspace_bytes(T, max_rows) bytes, max_rows = k_top, or
  *   max_pages * page_rows without indices (may be NULL when that is 0).  Nothing is kept in it
  *   between calls; calls that may overlap on the GPU need one each.
@@ -462,7 +463,8 @@ const char* ds4x_status_string(int status);
 int ds4x_last_launch_count(void);
 
 /* ---------------------------------------------------------------------------
- * Device status.  Every wait inside the kernels is bounded (about one second); a wait that
+ * Device status.  Every wait inside the kernels is bounded (about one second; a tenth of a second to a
+ * few seconds in ds4x_kv4_attn); a wait that
  * gives up records DS4X_ERR_TIMEOUT in a status word of the current device and the kernel
  * returns without finishing its work.  ds4x_device_status synchronizes `stream`, returns
  * DS4X_OK or DS4X_ERR_TIMEOUT, and clears the word when `clear` != 0.

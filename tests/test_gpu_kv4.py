@@ -491,6 +491,101 @@ def test_attn_many_tokens():
     check_attn(q[some], pool, out[some], lse[some], SCALE, "bf16", dict(req=req[some]))
 
 
+def test_attn_without_any_rows():
+    """Tables without pages, a pool without slots, no requests at all: zeros and -inf, nothing is read."""
+    q = queries(np.random.default_rng(1), 3, "f16")
+    none = torch.zeros((0, 256), dtype=torch.uint8, device="cuda"), torch.zeros((0, 16), dtype=torch.uint8, device="cuda")
+    pool = torch.zeros((64, 256), dtype=torch.uint8, device="cuda"), torch.full((64, 16), 255, dtype=torch.uint8, device="cuda")
+    idx = i32(np.arange(200)[None].repeat(3, 0))
+    cases = [
+        (pool, i32(np.zeros((3, 0))), i32([5, 9, 64]), dict()),                      # no page fits a table
+        (pool, i32(np.zeros((3, 0))), i32([5, 9, 64]), dict(indices=idx)),
+        (none, i32([[0], [0], [0]]), i32([5, 9, 64]), dict()),                       # no slot in the pool
+        (none, i32([[0], [0], [0]]), i32([5, 9, 64]), dict(indices=idx)),
+        (pool, i32(np.zeros((0, 2))), i32([]), dict(req=i32([0, 1, -1]))),           # no requests
+        (pool, i32(np.zeros((0, 2))), i32([]), dict(req=i32([0, 1, -1]), indices=idx)),
+        (pool, i32([[0], [0], [0]]), i32([0, -4, 0]), dict(indices=idx)),            # nothing held
+    ]
+    for (codes, scales), tables, rows, lists in cases:
+        out, lse = ds4x.kv4_attn(q, codes, scales, tables, rows, 64, out=torch.full_like(q, 7.0), **lists)
+        assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    empty, _ = ds4x.kv4_attn(q[:0], *pool, i32([[0]]), i32([1]), 64)
+    assert empty.shape == (0, 64, 512)
+
+
+@pytest.mark.parametrize("T", [2049, 4100])
+def test_attn_a_few_tokens_behind_a_full_launch(T):
+    """The last launch has few tokens, with long lists split over every block."""
+    rng = np.random.default_rng(T)
+    pool = Pool(rng, [9, 3000], 64)
+    req = np.zeros(T, dtype=np.int32)
+    req[2048:2049] = req[T - 1:] = 1
+    q = queries(rng, 16, "f16").repeat((T + 15) // 16, 1, 1)[:T].contiguous()
+    out, lse = run_attn(q, pool, req=req)
+    some = np.array([0, 2047, 2048, T - 1])
+    check_attn(q[some], pool, out[some], lse[some], SCALE, "f16", dict(req=req[some]))
+
+
+def test_attn_two_calls_at_once():
+    """On two streams, each with its own workspace, many times over."""
+    rng = np.random.default_rng(50)
+    pool = Pool(rng, [2500, 700, 60], 32)
+    req = [np.array([0, 1, 2, 0], dtype=np.int32), rng.integers(0, 3, 300).astype(np.int32)]
+    qs = [queries(rng, len(r), "bf16") for r in req]
+    want = [run_attn(q, pool, req=r) for q, r in zip(qs, req)]
+    dr = [i32(r) for r in req]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k in (0, 1):
+            got[k].append(ds4x.kv4_attn(qs[k], *pool.dev, 32, req=dr[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for out, lse in got[k]:
+            assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+
+
+def test_binding_refuses_on_the_device():
+    rng = np.random.default_rng(2)
+    pool = Pool(rng, [20, 30], 16)
+    q = queries(rng, 2, "f16")
+    codes, scales, tables, rows = pool.dev
+
+    def bad(match, *a, **kw):
+        with pytest.raises(ValueError, match=match):
+            ds4x.kv4_attn(*a, **kw)
+    bad("contiguous", q.transpose(0, 1).contiguous().transpose(0, 1), *pool.dev, 16)
+    bad("contiguous", q, codes, scales, tables.t().contiguous().t(), rows, 16) if tables.shape[1] > 1 else None
+    bad("slots", q, codes, scales[:-1], tables, rows, 16)
+    bad("256", q, codes[:, :128].contiguous(), scales, tables, rows, 16)
+    bad("int32", q, codes, scales, tables.long(), rows, 16)
+    bad("max_pages", q, codes, scales, tables[:1], rows, 16)
+    bad("CUDA", q, codes, scales, tables, rows.cpu(), 16)
+    bad("counts belong", q, *pool.dev, 16, counts=rows)
+    bad("indices must be", q, *pool.dev, 16, indices=i32(np.zeros((3, 8))))
+    bad("holds 1", q, *pool.dev, 16, req=i32([0]))
+    bad("shape", q, *pool.dev, 16, out=torch.empty_like(q[:1]))
+    bad("shape", q, *pool.dev, 16, lse=torch.empty((2, 32), device="cuda"))
+    bad("float16 or bfloat16", q.float(), *pool.dev, 16)
+    for kw, status in ((dict(page_rows=24), ds4x.ERR_UNSUPPORTED), (dict(page_rows=0), ds4x.ERR_INVALID)):
+        with pytest.raises(ds4x.Ds4xError) as e:
+            ds4x.kv4_attn(q, *pool.dev, **kw)
+        assert e.value.status == status
+    with pytest.raises(ds4x.Ds4xError) as e:                       # three tokens, two requests
+        ds4x.kv4_attn(queries(rng, 3, "f16"), *pool.dev, 16)
+    assert e.value.status == ds4x.ERR_INVALID
+    with pytest.raises(ds4x.Ds4xError) as e:
+        ds4x.kv4_attn(q, *pool.dev, 16, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == ds4x.ERR_WORKSPACE
+    with pytest.raises(ValueError, match="must not be negative"):
+        ds4x.page_plan(rows, rows, rows, tables, rows, rows[:1], 4, 16, -1, 5)
+    with pytest.raises(ValueError, match="holds 1"):
+        ds4x.kv4_append(torch.zeros((2, 512), dtype=torch.float16, device="cuda"), i32([0]), codes, scales)
+    with pytest.raises(ds4x.Ds4xError):                            # rows of another width
+        ds4x.kv4_append(torch.zeros((2, 128), dtype=torch.float16, device="cuda"), i32([0, 1]), codes, scales)
+
+
 # ------------------------------------------------------------------------------ a run of them all
 def test_serving_steps_end_to_end():
     """Steps of a batch as a server runs them: plan, compress, append, score and top-k, attention; the
