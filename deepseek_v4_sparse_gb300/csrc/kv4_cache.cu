@@ -452,7 +452,8 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   const int most = p.in_place ? kPlanCluster : kPlanBlocks;
   const int blocks = want <= 1 ? 1 : p.in_place || want > most ? most : (int)want;
   const size_t smem = (size_t)7 * n_req * sizeof(uint32_t);
-  if (smem > 48 * 1024 && ensure_dynamic_smem(page_plan_kernel, 7 * DS4X_MAX_REQ * 4) != cudaSuccess)
+  // a launch has 48 KB without asking, the kernel's static arrays among them
+  if (smem > 40 * 1024 && ensure_dynamic_smem(page_plan_kernel, 7 * DS4X_MAX_REQ * 4) != cudaSuccess)
     return DS4X_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);

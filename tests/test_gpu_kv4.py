@@ -1,4 +1,8 @@
 """The paged 4-bit cache on the GPU against its plain implementation in 64 bits (oracle/kv4.py)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -156,6 +160,21 @@ def test_page_plan_in_place_over_several_blocks(B, max_pages, ps, ratio, hi_new,
     p, r, s, _, _, _, to = (x.cpu().numpy() for x in out)
     got = (p, r, s, d[3].cpu().numpy(), d[0].cpu().numpy(), d[2].cpu().numpy(), d[5].cpu().numpy()[0], to)
     check_plan(got, kv4.page_plan(*c))
+
+
+def plan_in_a_fresh_process(B):
+    """A plan as a process's first call, whose shared memory no earlier call has asked for."""
+    c = plan_case(np.random.default_rng(B), B, 2, 8, 4, 9, B)
+    check_plan(run_plan(c), kv4.page_plan(*c))
+
+
+@pytest.mark.parametrize("B", [1732, 1733, 1755, 1756])
+def test_page_plan_as_the_first_call(B):
+    """28 bytes of shared memory a request, around the 48 KB that a launch has without asking."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"from tests.test_gpu_kv4 import plan_in_a_fresh_process as f; f({B})"
+    got = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0, got.stderr[-2000:]
 
 
 def test_page_plan_short_outputs_and_odd_state():
