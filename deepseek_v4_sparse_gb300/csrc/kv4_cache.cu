@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     p.slots[j] = slot;
   });
-  const int taken = (int)min(page_end[B - 1], (uint32_t)F);
+  const int taken = B > 0 ? (int)min(page_end[B - 1], (uint32_t)F) : 0;
   for_packed(page_end, B, (uint32_t)taken, shift, [&](uint32_t k, int b) {
     const int first = (int)(b > 0 ? page_end[b - 1] : 0u);
     p.tables[(int64_t)b * p.max_pages + held_pages(b) + ((int)k - first)] = p.free_pages[F - 1 - (int)k];
@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
       for (int i = 1; i < 32; ++i) mine += placed_s[i];
       if (p.n_free_out) *p.n_free_out = F - taken;
       if (p.totals) {
-        p.totals[0] = (int)tok_end[B - 1];
-        p.totals[1] = (int)row_end[B - 1];
+        p.totals[0] = B > 0 ? (int)tok_end[B - 1] : 0;
+        p.totals[1] = B > 0 ? (int)row_end[B - 1] : 0;
         p.totals[2] = (int)min(mine, (unsigned long long)kSat);
         p.totals[3] = taken;
       }
@@ -433,10 +433,10 @@ int ds4x_page_plan(const int32_t* seen, const int32_t* n_new, const int32_t* row
   if ((page_rows & (page_rows - 1)) != 0 || page_rows > DS4X_MAX_PAGE_ROWS || n_req > DS4X_MAX_REQ)
     return DS4X_ERR_UNSUPPORTED;
   if ((int64_t)max_pages * page_rows > INT32_MAX) return DS4X_ERR_UNSUPPORTED;
-  if (n_req == 0 && T_cap == 0 && R_cap == 0) return call_end(DS4X_OK);
-  if (n_req == 0) return DS4X_ERR_INVALID;  // outputs to fill, but no requests to fill them from
-  if (!seen || !n_new || !rows || !n_free || (max_pages > 0 && !tables) || (free_capacity > 0 && !free_pages) ||
-      (T_cap > 0 && (!positions || !req)) || (R_cap > 0 && !slots))
+  if (n_req == 0 && (T_cap > 0 || R_cap > 0)) return DS4X_ERR_INVALID;  // nothing to fill the outputs from
+  if (n_req == 0 && !n_free_out && !totals) return call_end(DS4X_OK);
+  if ((n_req > 0 && (!seen || !n_new || !rows || (max_pages > 0 && !tables))) || !n_free ||
+      (free_capacity > 0 && !free_pages) || (T_cap > 0 && (!positions || !req)) || (R_cap > 0 && !slots))
     return DS4X_ERR_INVALID;
   const void* all[] = {seen, n_new, rows, tables, free_pages, n_free, positions, req, slots,
                        seen_out, rows_out, n_free_out, totals};

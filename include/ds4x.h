@@ -359,7 +359,8 @@ size_t ds4x_decode_local_workspace_bytes(int32_t capacity, int32_t k_top, int32_
  *   A code is e2m1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  *   negatives); the element is code * 2^(b - 127).  b = 255 marks a group that held a NaN: all of
  *   its elements read as NaN.  The library writes 104 <= b <= 140 otherwise, where every element is
- *   exact in fp16 and in bf16.  A 16-bit row needs 1024 bytes, this one 272.
+ *   exact in fp16 and in bf16; rows that ds4x_kv4_attn reads hold no other bytes.  A 16-bit row needs
+ *   1024 bytes, this one 272.
  *
  *   Pages hold page_rows consecutive slots (a power of two, at most DS4X_MAX_PAGE_ROWS): page g is
  *   slots g*page_rows .. g*page_rows + page_rows - 1.  Row r of request b is at slot
@@ -394,6 +395,7 @@ size_t ds4x_decode_local_workspace_bytes(int32_t capacity, int32_t k_top, int32_
  *   totals [4] (or NULL): tokens, completed rows, rows with a slot, pages taken (each at most
  *       INT32_MAX).  Tokens or rows beyond T_cap / R_cap are left out of the packed outputs only.
  *   free_pages [free_capacity], n_free [1] on the device (*n_free is clipped to the capacity).
+ *   Without requests (n_req = 0) T_cap and R_cap must be 0; *n_free_out and totals are written.
  *   n_req <= DS4X_MAX_REQ and max_pages * page_rows <= INT32_MAX, else DS4X_ERR_UNSUPPORTED.
  *   Apart from the three state pairs the outputs overlap nothing.  To retire a request, put the first
  *   ceil(rows / page_rows) entries of its table row back on the list and set its seen and rows to 0.

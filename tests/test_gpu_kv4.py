@@ -189,6 +189,18 @@ def test_page_plan_short_outputs_and_odd_state():
     check_plan(run_plan(c), kv4.page_plan(*c))
 
 
+@pytest.mark.parametrize("spare", [0, 5])
+def test_page_plan_without_requests(spare):
+    """No tokens, no rows, no pages taken; the free list is as long as before."""
+    c = [np.zeros(0, np.int32)] * 3 + [np.zeros((0, 4), np.int32), np.arange(7, dtype=np.int32), np.int32(spare), 4, 8,
+                                       0, 0]
+    check_plan(run_plan(c, n_free_out=i32([-9]), totals=i32([-9] * 4)), kv4.page_plan(*c))
+    check_plan(run_plan(c), kv4.page_plan(*c))
+    c[8] = 3
+    with pytest.raises(ds4x.Ds4xError):
+        run_plan(c)
+
+
 def test_page_plan_counts_that_pass_32_bits():
     big = 2 ** 31 - 1
     B = 5
