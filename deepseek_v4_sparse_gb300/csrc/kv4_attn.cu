@@ -736,9 +736,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     uint32_t item = 0;
     uint32_t f_ph = 0;  // bit s: phase of O^T slot s's full barrier
     bool ok = true;
+    auto quiet = [&] { return p.status && *const_cast<volatile int*>(p.status) == 0; };
     for (Walk w(rows_s, start); w.left > 0; w.next(), ++item) {
       const int par = item & 1;
-      ok = wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
+      // the one wait that lasts as long as an item: a limit more for every 8192 chunks (which take about a
+      // tenth of the shortest), as long as no other wait has given up
+      ok = false;
+      for (int k = (w.c1 - w.c0) >> 13; k > 0 && !ok && __all_sync(0xffffffffu, quiet()); --k)
+        ok = wait_bar_warp(&lready[par], (item >> 1) & 1, nullptr, 72);
+      ok = ok || wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
       if (!ok) break;
       const float* lrow = lm + par * 4 * kHq;
       // chunks before the block, or behind it: the sums go to the block's first or second part

@@ -557,6 +557,37 @@ def test_attn_a_few_tokens_behind_a_full_launch(T):
     check_attn(q[some], pool, out[some], lse[some], SCALE, "f16", dict(req=req[some]))
 
 
+@pytest.mark.parametrize("rows", [65536, 4194304])
+def test_attn_long_lists_in_one_block(rows):
+    """A token for every SM, each over the same page again and again: every block has one long item.
+
+    Attention over n copies of 64 rows is attention over the 64 rows, and ln(n) more in lse.  The products add
+    16 rows to fp32 sums at a time, each step off by at most 2^-23 of the sum of magnitudes (a truncating adder):
+    rows / 16 * 2^-23 of sum_j w_j |kv_j|, beside what tolerance() counts for the 64 rows.  The sums of the
+    weights round each of their (rows / 8 a thread) steps by 2^-24."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(5)
+    codes = rng.integers(0, 256, (64, 256), dtype=np.uint8)
+    scales = rng.integers(124, 127, (64, 16)).astype(np.uint8)
+    q = queries(rng, sms, "f16")
+    out, lse = ds4x.kv4_attn(q, gpu(codes), gpu(scales), torch.zeros((1, rows // 64), dtype=I32, device="cuda"),
+                             i32([rows]), 64, req=torch.zeros(sms, dtype=I32, device="cuda"))
+    assert ds4x.device_status() == ds4x.OK
+    vals, scale = kv4.values(codes, scales), 1 / np.sqrt(512)
+    once = dict(tables=np.zeros((1, 1), np.int32), rows=[64], page_rows=64, req=np.zeros(1, np.int32))
+    for t in (0, sms - 1):
+        qd = q[t:t + 1].double().cpu().numpy()
+        ref, rlse = kv4.attn(qd, vals, scale, **once)
+        tol, ltol = tolerance(qd[0], vals, ref[0], scale, "f16")
+        x = (qd[0] @ vals.T) * scale
+        w = np.exp(x - rlse[0][:, None])
+        steps = rows / 16 * 2.0 ** -23
+        grow = steps * (w @ np.abs(vals)) + rows / 8 * 2.0 ** -24 * np.abs(ref[0])
+        assert np.all(np.abs(out[t].double().cpu().numpy() - ref[0]) <= tol + grow)
+        assert np.all(np.abs(lse[t].double().cpu().numpy() - rlse[0] - np.log(rows / 64)) <=
+                      ltol + rows / 8 * 2.0 ** -24 + 2.0 ** -20)
+
+
 def test_attn_two_calls_at_once():
     """On two streams, each with its own workspace, many times over."""
     rng = np.random.default_rng(50)
