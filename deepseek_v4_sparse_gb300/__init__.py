@@ -711,8 +711,8 @@ def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, posi
              want_lse: bool = True, stream=None):
     """64-head MQA of q_attn [T, 64, 512] over rows of the paged 4-bit cache.  Token t belongs to request
     req[t] (None: request t), which holds rows[b] rows through tables[b] [max_pages].  With indices
-    [T, k_top] it attends to those rows (the first counts[t] entries; -1 and rows not held are skipped),
-    without to every row visible at positions[t] (None: all held).  Returns (out, lse)."""
+    [T, k_top] it attends to those rows (the first counts[t] entries; -1 and rows not held are skipped; with
+    k_top = 0 to none), without to every row visible at positions[t] (None: all held).  Returns (out, lse)."""
     torch = _torch()
     i32, dev = torch.int32, q_attn.get_device()
     contexts = _elsewhere(dev, stream)
@@ -739,6 +739,8 @@ def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, posi
         k_top = max_rows = indices.size(1)
         pidx = _addr("indices", indices, i32, dev)
         pcnt = None if counts is None else _addr_n("counts", counts, i32, dev, T)
+        if k_top == 0:  # an empty tensor's address is 0, which asks for every row: no page is offered instead
+            max_pages, pidx, pcnt = 0, None, None
     elif counts is not None:
         raise ValueError("counts belong to indices")
     if out is None:

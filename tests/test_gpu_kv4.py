@@ -723,3 +723,24 @@ def test_serving_steps_end_to_end():
                 assert torch.equal(fin, torch.isfinite(lse[sl]))
                 assert (lse[sl][fin] - rlse[fin]).abs().max() <= 2.0 ** -7 if fin.any() else True
                 t0 += new[b]
+
+
+@pytest.mark.parametrize("given", ["nothing", "workspace", "counts", "many tokens"])
+def test_attn_lists_of_width_zero(given):
+    """An index list without entries names no row, whatever the requests hold."""
+    rng = np.random.default_rng(60)
+    pool = Pool(rng, [300, 0, 65], 16)
+    T = 2051 if given == "many tokens" else 3
+    req = rng.integers(0, 3, T).astype(np.int32)
+    q = queries(rng, 3, "bf16").repeat((T + 2) // 3, 1, 1)[:T].contiguous()
+    kw = dict(req=i32(req), positions=i32(np.full(T, 10 ** 6)))
+    if given == "workspace":
+        kw["workspace"] = torch.empty(ds4x.kv4_attn_workspace_bytes(T, pool.max_pages * 16), dtype=torch.uint8, device="cuda")
+    if given == "counts":
+        kw["counts"] = i32([5, 0, -1])
+    wide = i32(np.zeros((T, 8)))
+    for idx in (torch.empty((T, 0), dtype=I32, device="cuda"), wide[:, :0].contiguous(), wide[:, :0]):
+        out, lse = ds4x.kv4_attn(q, *pool.dev, 16, indices=idx, out=torch.full_like(q, 7.0), **kw)
+        assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    with pytest.raises(ValueError, match="indices must be"):
+        ds4x.kv4_attn(q, *pool.dev, 16, indices=torch.empty((T + 1, 0), dtype=I32, device="cuda"), **kw)
