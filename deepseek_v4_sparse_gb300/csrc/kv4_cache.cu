@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   uint32_t* page_end = sm + 2 * B;     // pages wanted
   int32_t* seen_s = reinterpret_cast<int32_t*>(sm + 3 * B);
   int32_t* rows_s = reinterpret_cast<int32_t*>(sm + 4 * B);
-  uint32_t* new_s = sm + 5 * B;        // tokens and completed rows of each request (a saturated sum
-  uint32_t* done_s = sm + 6 * B;       // does not give them back)
+  uint32_t* new_s = sm + 5 * B;        // tokens of each request (a saturated sum does not give them back)
+  int32_t* fits_s = reinterpret_cast<int32_t*>(sm + 6 * B);  // completed rows that its table has room for
   __shared__ uint32_t part[96];        // [3][32] the warps' sums
   __shared__ unsigned long long placed_s[32];  // placed rows, by warp of block 0
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -232,14 +232,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
       const int r0 = min(max(p.rows[b], 0), cap);
       n[i] = after - s;
       c[i] = after / p.ratio - s / p.ratio;
-      const int fits = min((int)c[i], cap - r0);
+      // row r of a request is its r-th pooled row: one that ran short earlier takes no more rows
+      const int fits = r0 < s / p.ratio ? 0 : min((int)c[i], cap - r0);
       const int held = (r0 >> p.log_page) + ((r0 & (ps - 1)) != 0);
       const int end = r0 + fits;
       g[i] = (end >> p.log_page) + ((end & (ps - 1)) != 0) - held;
       seen_s[b] = s;
       rows_s[b] = r0;
       new_s[b] = n[i];
-      done_s[b] = c[i];
+      fits_s[b] = fits;
     }
     sn = sat_add(sn, n[i]);
     sc = sat_add(sc, c[i]);
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   };
   auto rows_placed = [&](int b, int held, int got) {
     const int64_t room = ((int64_t)(held + got) << p.log_page) - rows_s[b];
-    return (int)min((int64_t)min((int)done_s[b], cap - rows_s[b]), room);
+    return (int)min((int64_t)fits_s[b], room);
   };
   auto held_pages = [&](int b) { return (rows_s[b] >> p.log_page) + ((rows_s[b] & (ps - 1)) != 0); };
 

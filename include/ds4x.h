@@ -382,7 +382,11 @@ size_t ds4x_decode_local_workspace_bytes(int32_t capacity, int32_t k_top, int32_
  *   It completes  done_b = (seen+new)/ratio - seen/ratio  rows, the rows that ds4x_compress emits.
  *   Pages for them are taken from the END of free_pages[0 .. *n_free - 1], in request order; a page
  *   that is partly filled is filled up first.  When the list runs out, or a request's table row is
- *   full, the request's remaining rows get no slot.
+ *   full, the request's remaining rows get no slot: it has run short, and rows_out[b] is below
+ *   seen_out[b]/ratio from then on.  Row r of a request is always its r-th pooled row (what positions and
+ *   indices count), so a request whose rows[b] is below seen[b]/ratio takes no more rows and no pages:
+ *   what it holds stays right, what came later is missing.  Retire it, or set its seen back to
+ *   rows[b]*ratio and bring the positions from there on again.
  *
  *   positions, req [T_cap]: the step's tokens packed in request order: position and request id of
  *       each; -1 behind the last one.
@@ -391,8 +395,9 @@ size_t ds4x_decode_local_workspace_bytes(int32_t capacity, int32_t k_top, int32_
  *   tables [n_req, max_pages], updated in place: the entries of the pages taken are written.
  *   seen_out, rows_out [n_req], n_free_out [1]: the state after the step (NULL: not wanted; each may
  *       be its input itself: then the call advances the state, and a captured call can be replayed).
- *       rows_out counts the rows that have a slot.
- *   totals [4] (or NULL): tokens, completed rows, rows with a slot, pages taken (each at most
+ *       rows_out counts the rows that have a place in a page taken (a page number of the caller's that
+ *       is negative, or too large for an int32 slot, counts too: its rows get slot -1).
+ *   totals [4] (or NULL): tokens, completed rows, rows that rows_out gained, pages taken (each at most
  *       INT32_MAX).  Tokens or rows beyond T_cap / R_cap are left out of the packed outputs only.
  *   free_pages [free_capacity], n_free [1] on the device (*n_free is clipped to the capacity).
  *   Without requests (n_req = 0) T_cap and R_cap must be 0; *n_free_out and totals are written.

@@ -68,6 +68,8 @@ def page_plan(seen, n_new, rows, tables, free_pages, n_free, ratio, page_rows, T
         done = after // ratio - s // ratio
         done_all += done
         end = min(r + done, max_pages * page_rows)
+        if r < s // ratio:                                           # it ran short earlier: row r is pooled row r
+            end = r
         for pg in range(-(-r // page_rows), -(-end // page_rows)):   # new pages
             if not free:
                 end = min(end, pg * page_rows)

@@ -744,3 +744,70 @@ def test_attn_lists_of_width_zero(given):
         assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
     with pytest.raises(ValueError, match="indices must be"):
         ds4x.kv4_attn(q, *pool.dev, 16, indices=torch.empty((T + 1, 0), dtype=I32, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("ratio", [1, 4])
+def test_a_request_that_ran_short_keeps_its_rows_in_order(ratio, in_place):
+    """Steps of which one finds too few pages: row r of a request is its r-th pooled row in every step, so a
+    token attends to pooled rows before it only; what has no place is missing, and rows_out says so."""
+    rng = np.random.default_rng(61)
+    B, ps, max_pages, pages = 3, 4, 12, 20
+    start, free_after = [40, 9, 0], [3, 12, 0]                # pages that come back before each later step
+    steps = [np.array(n) * ratio for n in ([10, 6, 5], [7, 7, 3], [5, 1, 9])]
+    truth = rng.standard_normal((B, 100, 512))                # pooled row r of request b
+    truth[:, :, 0] = np.arange(100)[None] / 4                 # tells the rows apart
+    truth = torch.from_numpy(truth).half()
+    seen, rows = np.array(start) // 4 * ratio, np.array(start) // 4
+    held = -(-rows // ps)
+    tables = np.full((B, max_pages), -1)
+    order = rng.permutation(pages)
+    for b in range(B):
+        tables[b, :held[b]] = order[sum(held[:b]):sum(held[:b + 1])]
+    free = list(order[sum(held):])
+    pool = torch.zeros((pages, ps, 256), dtype=torch.uint8, device="cuda"), torch.zeros((pages, ps, 16), dtype=torch.uint8, device="cuda")
+    for b in range(B):
+        r = np.arange(rows[b])
+        if len(r):
+            ds4x.kv4_append(truth[b, :rows[b]].cuda(), i32(tables[b][r // ps] * ps + r % ps), *pool)
+    values = [kv4.values(*kv4.quantise(truth[b].double().numpy())) for b in range(B)]
+    dseen, drows, dtables = i32(seen), i32(rows), i32(tables)
+    n_free = 4                                                # of the list's pages, at the first step
+    short = np.zeros(B, dtype=bool)
+    for new, back in zip(steps, free_after):
+        T, R = int(new.sum()), int(new.sum()) // ratio + B
+        kw = {}
+        dfree, dn = i32(free if free else [0]), i32([min(n_free, len(free))])
+        if in_place:
+            kw = dict(seen_out=dseen, rows_out=drows, n_free_out=dn)
+        positions, req, slots, dseen, drows, dn, totals = ds4x.page_plan(
+            dseen, i32(new), drows, dtables, dfree, dn, ratio, ps, T, R, **kw)
+        first = seen // ratio
+        seen = seen + new
+        done = seen // ratio - first
+        x = torch.cat([truth[b, first[b]:first[b] + done[b]] for b in range(B)]).cuda()
+        ds4x.kv4_append(x, slots, *pool)                      # the rows that the step completed, in its order
+        assert np.array_equal(dseen.cpu().numpy(), seen)
+        now = drows.cpu().numpy()
+        assert np.all(now[short] == rows[short])              # nothing is added behind a gap
+        rows, short = now, now < seen // ratio
+        left = int(dn.cpu()[0])
+        assert totals.cpu().tolist()[3] == min(n_free, len(free)) - left
+        free = free[:left] + free[min(n_free, len(free)):]
+        n_free = left + back
+        q = queries(rng, T, "f16")
+        out, lse = ds4x.kv4_attn(q, *pool, dtables, drows, ps, req=req, positions=positions, ratio=ratio)
+        for t in range(T):
+            b, pos = int(req[t]), int(positions[t])
+            n = min(int(rows[b]), (pos + 1) // ratio)
+            if n == 0:
+                assert torch.all(out[t] == 0)
+                continue
+            kv = values[b][:n]
+            qd = q[t].double().cpu().numpy()
+            x = (qd @ kv.T) * SCALE
+            w = np.exp(x - x.max(axis=1, keepdims=True))
+            ref = w @ kv / w.sum(axis=1, keepdims=True)
+            tol, _ = tolerance(qd, kv, ref, SCALE, "f16")
+            assert np.all(np.abs(out[t].double().cpu().numpy() - ref) <= tol), (b, pos)
+    assert short.any()

@@ -151,3 +151,20 @@ def test_binding_refuses_host_tensors():
         ds4x.kv4_attn(torch.zeros((1, 64, 512), dtype=torch.float16), *pool, z.reshape(4, 1), z, 16)
     with pytest.raises(ValueError, match="float16 or bfloat16"):
         ds4x.kv4_append(torch.zeros((4, 512)), z, *pool)
+
+
+def test_page_plan_by_hand_after_a_shortage():
+    """Ratio 4, ten rows held; no page for the rows behind the second page's end, pages again in the next step."""
+    tables = np.array([[0, 1, 2, -1, -1, -1, -1, -1]], dtype=np.int32)
+    out = kv4.page_plan([40], [40], [10], tables, [9, 8], 0, 4, 4, 40, 12)
+    slots, tab, seen, rows, left, totals = out[2:]
+    assert slots.tolist() == [10, 11] + [-1] * 10 and seen.tolist() == [80] and rows.tolist() == [12]
+    assert totals.tolist() == [40, 10, 2, 0]
+    # pooled rows 20..29 may not become rows 12..21: none gets a slot, no page is taken, what is held stays
+    out = kv4.page_plan(seen, [40], rows, tab, [9, 8, 7], 3, 4, 4, 40, 12)
+    slots, tab2, seen, rows, left, totals = out[2:]
+    assert slots.tolist() == [-1] * 12 and seen.tolist() == [120] and rows.tolist() == [12] and left == 3
+    assert np.array_equal(tab, tab2) and totals.tolist() == [40, 10, 0, 0]
+    # taken back to its last row, it goes on
+    out = kv4.page_plan([48], [8], rows, tab2, [9, 8, 7], 3, 4, 4, 8, 4)
+    assert out[2].tolist() == [28, 29, -1, -1] and out[5].tolist() == [14] and out[6] == 2
