@@ -12,7 +12,8 @@
 // One block an SM.  The tokens' rows are cut into chunks of 64; all chunks of all tokens form one
 // sequence, and each block takes an equal, contiguous part of it.  A token whose chunks lie in several
 // blocks leaves its unnormalised sums there in fp32 and kv4_combine_kernel joins them, so a long row list
-// of one token, a ragged batch and a full prefill chunk are all spread evenly.  Per chunk:
+// of one token, a ragged batch and a full prefill chunk are all spread evenly.  A token's chunks in a block
+// are an item (several, if they are many: kItemChunks).  Per chunk:
 //   S   [64 heads x 64 rows] = Q . K^T       tcgen05, M = 64 (heads on TMEM lanes), K-major
 //   O^T [512 x 64 heads]    += V^T . P^T     tcgen05, M = 128 (dims), A MN-major, B K-major
 // with K = V = the chunk, decoded once into 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
@@ -72,6 +73,10 @@ constexpr int kLaunchRegs = 72, kDecRegs = 72, kMmaRegs = 40, kSoftRegs = 88, kO
 static_assert(kThreads * kLaunchRegs <= 65536 && 4 * kDecRegs + kMmaRegs + kSoftRegs + kOutRegs <= 7 * kLaunchRegs, "registers");
 constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 constexpr int kItems = 4;                        // items whose logit factors are kept
+// Chunks of a token that are added up in one go.  The matrix unit truncates its fp32 sums: over one token's
+// 262144 rows of one sign they came out 0.14 % low, over 4194304 rows 2.6 %; items of 16384 rows, joined with
+// rounded sums, show nothing of it.  An item's end costs the output warps a read and a write of 128 KB.
+constexpr int kItemChunks = 256;
 constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
 constexpr int kOffP = kOffKV + 2 * kBufBytes;
@@ -79,7 +84,9 @@ constexpr int kOffAlpha = kOffP + 2 * kPBytes;   // float[64]: rescale factors o
 constexpr int kOffLM = kOffAlpha + kHq * 4;      // float[2 items][4][64]: sum of rounded weights, sum, m, 1 / first
 constexpr int kOffCq = kOffLM + 2 * 4 * kHq * 4; // float[kItems][64]: logit factor of a head
 constexpr int kOffRows = kOffCq + kItems * kHq * 4;  // int[kTokens]: rows of each token's list
-constexpr int kOffMask = kOffRows + kTokens * 4; // uint32[kMaskRing][2]: rows of the chunk that count
+constexpr int kOffJoin = kOffRows + kTokens * 4; // float[4][5][64], a copy for each output warp: a token's m, sum of rounded
+                                                 // weights and sum so far; factors of the sums so far and of the item's
+constexpr int kOffMask = kOffJoin + 4 * 5 * kHq * 4; // uint32[kMaskRing][2]: rows of the chunk that count
 constexpr int kOffSlots = kOffMask + kMaskRing * 8;  // int[kRing][64]: slot of each row of the chunk, -1 for none
 constexpr int kOffScan = kOffSlots + kRing * kRows * 4;         // int64[kWarps] warp sums, then int[4]: the block's part, and
                                                  // the last chunk (+ 1) in which a maximum moved
@@ -176,22 +183,28 @@ __device__ __forceinline__ int token_rows(const Params& p, int t) {
 }
 __device__ __forceinline__ int chunks_of(int rows) { return rows > kRows ? (rows - 1) / kRows + 1 : 1; }
 
-// A block's part of the chunk sequence, walked token by token: chunks [c0, c1) of token t.  What is read
-// from shared memory goes through a warp reduction, whose result is a uniform register: the loops over it
-// are then known to be the same in every lane, and the issuing warps' operands stay in such registers.
+// A block's part of the chunk sequence, walked item by item: chunks [c0, c1) of token t, of which the block
+// has the chunks up to `end`.  What is read from shared memory goes through a warp reduction, whose result is a
+// uniform register: the loops over it are then known to be the same in every lane, and the issuing warps'
+// operands stay in such registers.
 struct Walk {
-  int t, c0, c1, left;
+  int t, c0, c1, end, left;
   const int* rows;
   __device__ __forceinline__ static int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
   __device__ __forceinline__ Walk(const int* rows_s, const int* start)
       : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), rows(rows_s) {
-    c1 = left > 0 ? min(chunks_of(uniform(rows[t])), c0 + left) : c0;
+    cut();
+  }
+  __device__ __forceinline__ void cut() {
+    end = left > 0 ? min(chunks_of(uniform(rows[t])), c0 + left) : c0;
+    c1 = min(end, c0 + kItemChunks);
   }
   __device__ __forceinline__ void next() {
+    const int over = c1 == end;
     left -= c1 - c0;
-    ++t;
-    c0 = 0;
-    c1 = left > 0 ? min(chunks_of(uniform(rows[t])), left) : 0;
+    t += over;
+    c0 = over ? 0 : c1;
+    cut();
   }
 };
 
@@ -468,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           const int b = gc & 1;
           if (!wait_bar_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 62)) { ok = false; break; }
           if (c == w.c0) {
-            if (lane == 0 && w.left > w.c1 - w.c0) prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kKv4Dim, kHq * kKv4Dim * 2);
+            if (lane == 0 && w.c1 == w.end && w.left > w.c1 - w.c0)
+              prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kKv4Dim, kHq * kKv4Dim * 2);
             if (!wait_bar_warp(qfull, item & 1, p.status, 63)) { ok = false; break; }
           }
 #pragma unroll 1
@@ -736,20 +750,83 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     uint32_t item = 0;
     uint32_t f_ph = 0;  // bit s: phase of O^T slot s's full barrier
     bool ok = true;
-    auto quiet = [&] { return p.status && *const_cast<volatile int*>(p.status) == 0; };
+    int from = 0;                                // the block's first chunk of the token
     for (Walk w(rows_s, start); w.left > 0; w.next(), ++item) {
       const int par = item & 1;
-      // the one wait that lasts as long as an item: a limit more for every 8192 chunks (which take about a
-      // tenth of the shortest), as long as no other wait has given up
-      ok = false;
-      for (int k = (w.c1 - w.c0) >> 13; k > 0 && !ok && __all_sync(0xffffffffu, quiet()); --k)
-        ok = wait_bar_warp(&lready[par], (item >> 1) & 1, nullptr, 72);
-      ok = ok || wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
+      ok = wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
       if (!ok) break;
       const float* lrow = lm + par * 4 * kHq;
       // chunks before the block, or behind it: the sums go to the block's first or second part
-      const bool whole = w.c0 == 0 && w.c1 == chunks_of(rows_s[w.t]);
-      const int64_t part = 2 * (int64_t)blockIdx.x + (w.c0 == 0);
+      if (w.c0 == 0 || item == 0) from = w.c0;
+      const bool begins = w.c0 == from, ends = w.c1 == w.end;
+      const bool whole = ends && from == 0 && w.c1 == chunks_of(rows_s[w.t]);
+      const int64_t part = 2 * (int64_t)blockIdx.x + (from == 0);
+      if (!(begins && ends)) {
+        // One of several items: its sums are joined to those so far, as kv4_combine_kernel joins parts.  They
+        // lie where the part's go: the second part's own token is the block's last, behind all that lie whole
+        // in the block.  A thread reads back only what it wrote.
+        float* so_far = reinterpret_cast<float*>(smem + kOffJoin) + quad * 5 * kHq;
+#pragma unroll 1
+        for (int hh = lane; hh < kHq; hh += 32) {
+          const float mi = lrow[2 * kHq + hh], m0 = begins ? -INFINITY : so_far[hh];
+          const float m = fmaxf(m0, mi);
+          const float f0 = begins ? 0.f : m == -INFINITY ? 1.f : ex2_approx(m0 - m);
+          const float fi = m == -INFINITY ? 1.f : ex2_approx(mi - m);
+          const float r = lrow[hh] * fi + (begins ? 0.f : so_far[kHq + hh] * f0);
+          const float l = lrow[kHq + hh] * fi + (begins ? 0.f : so_far[2 * kHq + hh] * f0);
+          so_far[hh] = m;
+          so_far[kHq + hh] = r;
+          so_far[2 * kHq + hh] = l;
+          const float inv = !whole ? 1.f : r == 0.f ? 0.f : 1.f / r;
+          so_far[3 * kHq + hh] = f0 * inv;
+          so_far[4 * kHq + hh] = fi * inv;
+          if (quad == 0 && ends && !whole) {
+            float* st = p.stat + part * kStatFloats;
+            st[hh] = r;
+            st[kHq + hh] = l;
+            st[2 * kHq + hh] = m;
+          } else if (quad == 0 && whole && p.lse) {
+            p.lse[(int64_t)w.t * kHq + hh] = l == 0.f ? -INFINITY : (m + (log2f(l) - kWeightLog2)) * 0.69314718055994531f;
+          }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int step = 0; step < 4 * kPairs; ++step) {  // quarters of the dims by quarters of the heads
+          const int db = step >> 2, hb = (step & 3) * 16;
+          const int os = oslot(item, db);
+          if (hb == 0) {
+            ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 73);
+            if (!ok) break;
+            f_ph ^= 1u << os;
+            tc_fence_after();
+          }
+          float v[16];
+          tmem_ld16(tmem + t_lane + kColO + os * kHq + hb, v);
+          tc_wait_ld();
+          if (hb == 48) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&oempty[os]);
+          }
+          const int d = db * 128 + quad * 32 + lane;
+          float* sums = p.part + part * kPartFloats + hb * kKv4Dim + d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] *= so_far[4 * kHq + hb + i];
+            if (!begins) v[i] += so_far[3 * kHq + hb + i] * sums[i * kKv4Dim];
+          }
+          uint16_t* orow = p.out + ((int64_t)w.t * kHq + hb) * kKv4Dim + d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (whole) orow[i * kKv4Dim] = (uint16_t)pack16<kBf16>(v[i], 0.f);
+            else sums[i * kKv4Dim] = v[i];
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lfree[par]);
+        continue;
+      }
       if (lane < 16) {
         const int hh = quad * 16 + lane;
         const float l = lrow[kHq + hh], m = lrow[2 * kHq + hh];

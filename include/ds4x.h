@@ -451,8 +451,7 @@ int ds4x_kv4_read(const uint8_t* codes, const uint8_t* scales, int32_t n_slots, 
  *   workspace: at least ds4x_kv4_attn_workspace_bytes(T, max_rows) bytes, max_rows = k_top, or
  *   max_pages * page_rows without indices (may be NULL when that is 0).  Nothing is kept in it
  *   between calls; calls that may overlap on the GPU need one each.
- *   Sums over a token's rows are fp32 within a block (an SM's share of all the rows) and truncate: 262144
- *   rows of one token in a block come out 0.03 % low, 1048576 rows 0.14 %, 4194304 rows 0.6 %.
+ *   Sums over a token's rows are fp32, added up 16384 rows at a time at most and then joined.
  *   The same arguments give the same bits on every run.  A call may be captured into a CUDA graph
  *   after a first call on the device.
  * ------------------------------------------------------------------------- */

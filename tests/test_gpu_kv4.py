@@ -811,3 +811,83 @@ def test_a_request_that_ran_short_keeps_its_rows_in_order(ratio, in_place):
             tol, _ = tolerance(qd, kv, ref, SCALE, "f16")
             assert np.all(np.abs(out[t].double().cpu().numpy() - ref) <= tol), (b, pos)
     assert short.any()
+
+
+def test_attn_sums_of_very_long_lists_are_not_biased():
+    """4194304 rows of one token in a block.  Dims 32.. are the same in every row, so out is that value: what
+    is left is the error of the sums alone (the weights' rounding stands in numerator and normaliser alike).
+
+    A list is added up 16384 rows at a time.  O^T: 1024 steps of 16 products, each of which the matrix unit may
+    add in four truncating parts, so each is off by less than 2^-21 of the sum so far, half of that over a chain
+    of growing sums: 1024 / 2 * 2^-21 = 2^-12.  The normaliser: 4096 terms a thread, each step rounded by 2^-24
+    of the sum so far, half of that: 2^-13.  The 256 sums are joined by two products and an addition each:
+    256 * 3 / 2 * 2^-24, in numerator and normaliser.  The output is rounded once: 2^-11 relative.  lse: as the
+    normaliser, the factors of 2^x at 2^-22 a join, and the logits' part of tolerance()."""
+    rows = 4194304
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(63)
+    codes = np.tile(rng.integers(1, 8, (1, 256), dtype=np.uint8) * 17, (64, 1))   # both nibbles: positive values
+    codes[:, :16] = rng.integers(0, 256, (64, 16), dtype=np.uint8)                # dims 0..31: the logits
+    scales = np.full((64, 16), 127, dtype=np.uint8)
+    q = queries(rng, sms, "f16")
+    q[:, :, 32:] = 0
+    out, lse = ds4x.kv4_attn(q, gpu(codes), gpu(scales), torch.zeros((1, rows // 64), dtype=I32, device="cuda"),
+                             i32([rows]), 64, req=torch.zeros(sms, dtype=I32, device="cuda"))
+    assert ds4x.device_status() == ds4x.OK
+    vals = kv4.values(codes, scales)
+    norm = 2.0 ** -13 + 256 * 3 / 2 * 2.0 ** -24
+    for t in (0, 1, sms - 1):
+        qd = q[t].double().cpu().numpy()
+        want = vals[0, 32:]
+        got = out[t, :, 32:].double().cpu().numpy()
+        worst = np.abs(got / want - 1).max()
+        assert worst <= 2.0 ** -12 + 256 * 3 / 2 * 2.0 ** -24 + norm + 2.0 ** -11, worst
+        x = (qd @ vals.T) * SCALE
+        m = x.max(axis=1, keepdims=True)
+        rlse = m[:, 0] + np.log(np.exp(x - m).sum(axis=1)) + np.log(rows / 64)
+        ref = np.exp(x - m) @ vals / np.exp(x - m).sum(axis=1, keepdims=True)
+        _, ltol = tolerance(qd, vals, ref, SCALE, "f16")
+        assert np.all(np.abs(lse[t].double().cpu().numpy() - rlse) <= ltol + norm + 256 * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype,size", [("f16", 1.0), ("bf16", 30.0)])
+def test_attn_long_lists_added_up_in_parts(dtype, size):
+    """Tokens of several times 16384 rows a block, whole in a block or over two, among short ones; the largest
+    logits come late."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(64)
+    pool = Pool(rng, [20000, 70000, 3, 0], 64)
+    late = pool.tables[1, -3:, None] * 64 + np.arange(40)
+    pool.scales[late[late < pool.n_slots].ravel()] += 2
+    pool.dev = pool.dev[0], gpu(pool.scales), *pool.dev[2:]
+    req = np.concatenate([[2, 1, 3, 0], rng.choice([0, 1, 1, 1, 2, 3], 3 * sms // 2), [1, 0]]).astype(np.int32)
+    T = len(req)
+    # visible rows: a few short of all, so that tokens start and end at different places of the blocks
+    positions = (pool.rows[req] - 1 - rng.integers(0, 300, T)).astype(np.int32)
+    q = queries(rng, T, dtype, size)
+    out, lse = run_attn(q, pool, req=req, positions=positions, ratio=1)
+    assert torch.isfinite(out).all()
+    o2, l2 = run_attn(q, pool, req=req, positions=positions, ratio=1)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    vals = torch.from_numpy(pool.values()).cuda()
+    for t in np.unique(np.concatenate([np.arange(4), [T - 2, T - 1], rng.integers(0, T, 20)])):
+        at = kv4.attended_slots(t, pool.tables, pool.rows, 64, pool.n_slots, req=req, positions=positions)
+        if not at:
+            assert torch.all(out[t] == 0) and torch.all(torch.isneginf(lse[t]))
+            continue
+        kv, qd = vals[at], q[t].double()
+        x = qd @ kv.T * SCALE
+        rlse = torch.logsumexp(x, 1)
+        w = torch.exp(x - rlse[:, None])
+        ref = w @ kv
+        # tolerance() with the mean of |kv_j - ref| bounded by its root mean square, and 2^-12 of w |kv| for the
+        # sums of 16384 rows (half of 1024 steps of at most 2^-21)
+        ex = 64 * 2.0 ** -23 * SCALE * (qd.abs() @ kv.abs().T).amax(1) + 2.0 ** -20
+        spread = (w @ kv ** 2 - ref ** 2).clamp_min(0).sqrt()
+        eta = 2 * (2.0 ** -11 + 2 * ex)
+        half = torch.finfo(DT[dtype]).eps / 2
+        tol = (eta[:, None] * spread + 2.0 ** -12 * (w @ kv.abs()) + len(at) * 2.0 ** -29 * kv.abs().max() +
+               half * 1.01 * ref.abs() + 2.0 ** -25)
+        worst = ((out[t].double() - ref).abs() / tol).max().item()
+        assert worst <= 1, (t, len(at), worst)
+        assert torch.all((lse[t].double() - rlse).abs() <= 2 * ex + 2.0 ** -13 + 2.0 ** -20 * (1 + x.abs().amax(1)))
