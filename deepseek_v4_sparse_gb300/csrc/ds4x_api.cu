@@ -197,7 +197,7 @@ __global__ void bounded_wait_selftest_kernel(int* status, unsigned long long tim
     fence_mbarrier_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) (void)mbar_wait_ns(&bar, 0, status, 0x7e, timeout_ns);
+  if (threadIdx.x == 0) (void)mbar_wait_ns(&bar, 0, status, 0x7c, timeout_ns);
 }
 }  // namespace
 

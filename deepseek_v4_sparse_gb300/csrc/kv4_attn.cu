@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     uint32_t sc[2];
     // codes and scales of chunk x: a row without a slot reads slot 0 with a scale of 0
     auto load = [&](uint32_t x) {
-      const bool got = wait_bar_warp(&slfull[x % kRing], (x / kRing) & 1, p.status, 60);
+      const bool got = wait_bar_warp(&slfull[x % kRing], (x / kRing) & 1, p.status, 80);
       const int* sl = slot_s + (x % kRing) * kRows + 8 * (warp & 7) + lr;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         }
         if (lane == 0) cq[(qi % kItems) * kHq + h + i] = f;
       }
-      const bool got = wait_bar_warp(qempty, (qi & 1) ^ 1, p.status, 71);
+      const bool got = wait_bar_warp(qempty, (qi & 1) ^ 1, p.status, 91);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint8_t* dst = sq + (lane >> 3) * kQBlockBytes + (h + i) * 128 + (((lane & 7) ^ ((h + i) & 7)) << 4);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           }
         }
         if (g + 1 < chunks) ok = load(g + 1);
-        ok = ok && wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 61);
+        ok = ok && wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 81);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t a = st_off[k] + b * kBufBytes, a4 = (st_off[k] ^ 64u) + b * kBufBytes;
@@ -479,15 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
-          if (!wait_bar_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 62)) { ok = false; break; }
+          if (!wait_bar_warp(&sempty[b], ((gc >> 1) & 1) ^ 1, p.status, 82)) { ok = false; break; }
           if (c == w.c0) {
             if (lane == 0 && w.c1 == w.end && w.left > w.c1 - w.c0)
               prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kKv4Dim, kHq * kKv4Dim * 2);
-            if (!wait_bar_warp(qfull, item & 1, p.status, 63)) { ok = false; break; }
+            if (!wait_bar_warp(qfull, item & 1, p.status, 83)) { ok = false; break; }
           }
 #pragma unroll 1
           for (int half = 0; half < kHalves; ++half) {
-            if (!wait_bar_warp(&kvfull[b * kHalves + half], (gc >> 1) & 1, p.status, 64)) { ok = false; break; }
+            if (!wait_bar_warp(&kvfull[b * kHalves + half], (gc >> 1) & 1, p.status, 84)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a = q_lo + half * (4 * kQBlockBytes >> 4), k = kv_lo + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
             mma_elect<false>(tmem + b * kHq, a, k, kIdescS, half);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
             }
           }
           const uint32_t m0 = __ballot_sync(0xffffffffu, slot[0] >= 0), m1 = __ballot_sync(0xffffffffu, slot[1] >= 0);
-          ok = wait_bar_warp(&slempty[gc % kRing], ((gc / kRing) & 1) ^ 1, p.status, 59);
+          ok = wait_bar_warp(&slempty[gc % kRing], ((gc / kRing) & 1) ^ 1, p.status, 79);
           if (!ok) break;
           slot_s[(gc % kRing) * kRows + lane] = slot[0];
           slot_s[(gc % kRing) * kRows + lane + 32] = slot[1];
@@ -557,14 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++gc) {
           const int b = gc & 1;
-          if (!wait_bar_warp(&pfull[b], (gc >> 1) & 1, p.status, 65)) { ok = false; break; }
+          if (!wait_bar_warp(&pfull[b], (gc >> 1) & 1, p.status, 85)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int db = 0; db < kPairs; ++db) {
             const int os = oslot(item, db);
             // an item's first product overwrites its slot: the output that last read it is done
             if (c == w.c0) {
-              if (!wait_bar_warp(&oempty[os], ((o_ph >> os) & 1u) ^ 1u, p.status, 66)) { ok = false; break; }
+              if (!wait_bar_warp(&oempty[os], ((o_ph >> os) & 1u) ^ 1u, p.status, 86)) { ok = false; break; }
               o_ph ^= 1u << os;
               tc_fence_after();
             }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
       float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of the weights, and of the rounded ones
       for (int ci = w.c0; ci < w.c1; ++ci, ++gc) {
         const int b = gc & 1;
-        ok = ok && wait_bar_warp(&sfull[b], (gc >> 1) & 1, p.status, 67);
+        ok = ok && wait_bar_warp(&sfull[b], (gc >> 1) & 1, p.status, 87);
         tc_fence_after();
         float x[32];
         tmem_ld_16x256b_x8(tmem + t_lane + b * kHq, x);
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           pkA[r] = *reinterpret_cast<const uint32_t*>(&hp);
           pkB[r] = *reinterpret_cast<const uint32_t*>(&hq);
         }
-        ok = ok && wait_bar_warp(&looked[b], (gc >> 1) & 1, p.status, 75);
+        ok = ok && wait_bar_warp(&looked[b], (gc >> 1) & 1, p.status, 95);
         if (*const_cast<volatile int*>(start + 3) == (int)(gc + 1)) {
           leave = named_or(kSoftBar, kGroupThreads, !ok);
           if (leave) break;
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           named_sync(kSoftBar, kGroupThreads);
           // O^T must hold all of the previous chunk before its columns are rescaled
           const uint32_t prev = gc - 1;
-          ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 68);
+          ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 88);
           tc_fence_after();
 #pragma unroll 1
           for (int q2 = 0; q2 < 2 * kPairs; ++q2) {  // 4 quarters x 2 halves of 32 heads
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           tc_wait_st();
           named_sync(kSoftBar, kGroupThreads);
         }
-        ok = ok && wait_bar_warp(&pempty[b], ((gc >> 1) & 1) ^ 1, p.status, 69);
+        ok = ok && wait_bar_warp(&pempty[b], ((gc >> 1) & 1) ^ 1, p.status, 89);
         {
           // P[h][j], K-major with the 128-byte swizzle: 16-byte chunk r of line h at (r ^ (h & 7))
           uint8_t* lineA = sp + b * kPBytes + hA * 128 + 4 * e;
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         rB += __shfl_xor_sync(0xffffffffu, rB, d);
       }
       // the slot of this item's parity was last read by the output of item - 2
-      ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 70);
+      ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 90);
       if (e == 0) {
         float* row = lm + (item & 1) * 4 * kHq;
         row[hA] = rA;
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
     int from = 0;                                // the block's first chunk of the token
     for (Walk w(rows_s, start); w.left > 0; w.next(), ++item) {
       const int par = item & 1;
-      ok = wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 72);
+      ok = wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 92);
       if (!ok) break;
       const float* lrow = lm + par * 4 * kHq;
       // chunks before the block, or behind it: the sums go to the block's first or second part
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
           const int db = step >> 2, hb = (step & 3) * 16;
           const int os = oslot(item, db);
           if (hb == 0) {
-            ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 73);
+            ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 94);
             if (!ok) break;
             f_ph ^= 1u << os;
             tc_fence_after();
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
         const int db = half >> 1, hb = (half & 1) * 32;
         const int os = oslot(item, db);
         if (hb == 0) {
-          ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 73);
+          ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 93);
           if (!ok) break;
           f_ph ^= 1u << os;
           tc_fence_after();

@@ -168,3 +168,18 @@ def test_page_plan_by_hand_after_a_shortage():
     # taken back to its last row, it goes on
     out = kv4.page_plan([48], [8], rows, tab2, [9, 8, 7], 3, 4, 4, 8, 4)
     assert out[2].tolist() == [28, 29, -1, -1] and out[5].tolist() == [14] and out[6] == 2
+
+
+def test_wait_sites_name_one_kernel():
+    """The status word tells which wait gave up: no two source files share a number."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(ds4x_build.__file__), "csrc")
+    of = {}
+    for name in sorted(os.listdir(csrc)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        for site in re.findall(r"status, (0x[0-9a-f]+|\d+)(?:, timeout_ns)?\)", text):
+            of.setdefault(int(site, 0), set()).add(name)
+    assert len(of) > 30
+    shared = {site: files for site, files in of.items() if len(files) > 1}
+    assert not shared, shared
