@@ -999,7 +999,9 @@ constexpr size_t kHeadBytes = 16 * kMaxParts;  // the int4 of every block
 
 }  // namespace
 
+// A token of one chunk is never split: the head alone then, which the launch writes all the same.
 size_t kv4_attn_workspace_bytes(int T, int max_rows) {
+  if (max_rows <= kRows) return kHeadBytes;
   const int grid = grid_of(T < kTokens ? T : kTokens, max_rows);
   return kHeadBytes + (size_t)2 * grid * (kPartFloats + kStatFloats) * sizeof(float);
 }

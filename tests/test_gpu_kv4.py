@@ -891,3 +891,20 @@ def test_attn_long_lists_added_up_in_parts(dtype, size):
         worst = ((out[t].double() - ref).abs() / tol).max().item()
         assert worst <= 1, (t, len(at), worst)
         assert torch.all((lse[t].double() - rlse).abs() <= 2 * ex + 2.0 ** -13 + 2.0 ** -20 * (1 + x.abs().amax(1)))
+
+
+@pytest.mark.parametrize("T,max_rows", [(1, 1), (5, 64), (152, 33), (3000, 64)])
+def test_attn_workspace_of_tokens_that_are_never_split(T, max_rows):
+    """Up to 64 rows a token is one chunk, which no second block works on: no room for parts is asked for."""
+    rng = np.random.default_rng(62)
+    need = ds4x.kv4_attn_workspace_bytes(T, max_rows)
+    assert need <= 65536
+    assert ds4x.kv4_attn_workspace_bytes(T, 65) > need
+    pool = Pool(rng, [max_rows], 1)
+    q = queries(rng, min(T, 8), "f16").repeat((T + 7) // 8, 1, 1)[:T].contiguous()
+    buf = torch.full((need + 4096,), 173, dtype=torch.uint8, device="cuda")
+    lists = dict(req=np.zeros(T, np.int32))
+    out, lse = ds4x.kv4_attn(q, *pool.dev, 1, req=i32(lists["req"]), workspace=buf[:need])
+    assert torch.all(buf[need:] == 173)
+    some = np.unique([0, T // 2, T - 1])
+    check_attn(q[some], pool, out[some], lse[some], SCALE, "f16", dict(req=lists["req"][some]))
