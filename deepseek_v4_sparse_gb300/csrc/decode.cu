@@ -44,8 +44,6 @@ __global__ void append_rows_kernel(uint4* __restrict__ k, const uint4* __restric
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 }  // namespace ds4x
 

@@ -31,8 +31,6 @@ int current_device() {
   return d;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Window arguments: local_pos0 >= 0, L >= 0, 0 <= window <= DS4X_MAX_WINDOW, and a buffer (16-byte
 // aligned when it is device memory) whenever a row of it can be attended.
 int check_window(const void* kv_local, int32_t local_pos0, int32_t L, int32_t window, bool device) {

@@ -11,6 +11,10 @@
 
 namespace ds4x {
 
+// What the entry points ask of pointers: 16 bytes for tensors that kernels read as vectors, else an element.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Launches `kernel` on `st` with programmatic stream serialization (see pdl_wait / pdl_trigger in
 // ds4x_ptx.cuh): the launch overlaps the tail of the previous kernel on the stream.
 template <typename... KArgs, typename... Args>

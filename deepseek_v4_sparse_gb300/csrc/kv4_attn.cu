@@ -140,10 +140,6 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, in
   return __all_sync(0xffffffffu, wait_bar(bar, parity, status, site));
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // D (+)= A B^T by an elected lane of a converged warp; descriptors by their low words (the addresses): the
 // high words are the same for all operands here.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -1068,11 +1064,6 @@ int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
 }  // namespace ds4x
 
 using namespace ds4x;
-
-namespace {
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-}  // namespace
 
 extern "C" {
 

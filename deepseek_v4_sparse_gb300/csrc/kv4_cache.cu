@@ -370,9 +370,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // Blocks of 8 rows: every row its own warp while that fits the GPU eight times over, then strided.
 int row_blocks(int n) {
   const int64_t want = ((int64_t)n + kWarpsPerBlock - 1) / kWarpsPerBlock;
