@@ -908,3 +908,18 @@ def test_attn_workspace_of_tokens_that_are_never_split(T, max_rows):
     assert torch.all(buf[need:] == 173)
     some = np.unique([0, T // 2, T - 1])
     check_attn(q[some], pool, out[some], lse[some], SCALE, "f16", dict(req=lists["req"][some]))
+
+
+@pytest.mark.parametrize("T,dtype", [(7, "bf16"), (9, "f16"), (37, "f16"), (38, "bf16"), (64, "f16")])
+def test_attn_one_long_request_among_short_ones(T, dtype):
+    """Its parts lie in most of the blocks, whichever form of the joining kernel the number of tokens picks."""
+    rng = np.random.default_rng(T)
+    rows = rng.integers(0, 65, T)
+    rows[T // 2] = 9000 + T
+    pool = Pool(rng, rows, 32)
+    q = queries(rng, T, dtype)
+    out, lse = run_attn(q, pool)
+    some = np.array([0, T // 2 - 1, T // 2, T // 2 + 1, T - 1])
+    check_attn(q[some], pool, out[some], lse[some], SCALE, dtype, dict(req=some.astype(np.int32)))
+    o2, l2 = run_attn(q, pool)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
