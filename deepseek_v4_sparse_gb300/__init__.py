@@ -626,8 +626,9 @@ def page_plan(seen, n_new, rows, tables, free_pages, n_free, ratio: int, page_ro
     free_pages[:n_free] (n_free [1] int32).  Returns (positions [T_cap], req [T_cap], slots [R_cap], seen_out,
     rows_out, n_free_out, totals [4] = tokens, completed rows, rows placed, pages taken); the packed
     outputs end in -1.  A request whose rows_out is below seen_out // ratio ran out of pages: it takes no more
-    rows until it is retired or its seen is set back to rows * ratio.  Outputs may be passed in (when none is, they share one allocation); seen_out, rows_out
-    and n_free_out may be their inputs."""
+    rows until it is retired or its seen is set back to rows * ratio.  Outputs may be passed in (when none is,
+    they are views of one allocation, which lives as long as any of them); seen_out, rows_out and n_free_out may
+    be their inputs."""
     torch = _torch()
     i32, dev = torch.int32, seen.get_device()
     contexts = _elsewhere(dev, stream)

@@ -6,8 +6,8 @@
 //
 // The products run on the tensor cores in fp16, whatever the type of q: a row's values (code times a
 // power of two, kv4_common.cuh) are exact in fp16, a bf16 q is made so by a power of two a head (which
-// moves its largest magnitude to [2^14, 2^15); what is under 2^-28 of the largest reads as 0), and the
-// softmax weights keep eleven bits instead of bf16's eight.
+// moves its largest magnitude to [2^14, 2^15); what comes to lie under 2^-14 is off by at most 2^-15, 2^-29 of
+// the head's largest), and the softmax weights keep eleven bits instead of bf16's eight.
 //
 // One block an SM.  The tokens' rows are cut into chunks of 64; all chunks of all tokens form one
 // sequence, and each block takes an equal, contiguous part of it.  A token whose chunks lie in several
@@ -27,14 +27,14 @@
 // decoded: the fetching warps wait for a buffer then, and have it converted when the products of the token
 // before are done with theirs.  It is brought to L2 an item ahead.
 //
-// What bounds it: a chunk's way through the roles (fetch, S, softmax, O^T, release), two chunks at a time,
-// and the data path of L1 and shared memory, one 128-byte access a clock for the products and the warps
-// together: a chunk takes 1790 accesses of the products (128 KB of S operands, 96 KB of O^T operands) and
-// 1880 of the warps (512 of them the decoded stores) in about 3950 clocks.  219 us for 2048 tokens of 512
-// rows: 627 TFLOP/s, 33 % of the measured peak.  With three quarters of the products left out it took 189 us,
-// without fetches and stores 200 us, with neither and without 2^x 168 us: most is the hand-overs.  Slower:
-// three buffers of 48 rows (272 us: S products cost nearly the same at 48 rows as at 64), rows in 16 lines a
-// load and slots looked up in every warp (247 us), rows by bulk copies into a stage of their own (345 us).
+// What bounds it: a chunk's way through the roles (fetch, S, softmax, O^T, release), two chunks at a time, in
+// about 3950 clocks a chunk.  221 us for 2048 tokens of 512 rows: 622 TFLOP/s, 33 % of the measured peak.  With
+// three quarters of the products left out it took 189 us, without fetches and stores 200 us, with neither and
+// without 2^x 168 us: no one resource, most is the hand-overs.  (The data path of L1 and shared memory has
+// something to do in 93 % of its cycles, 1790 accesses a chunk of the products and 1880 of the warps, but 37 %
+// fewer accesses saved 14 % of the time: it is not what bounds.)  Slower: three buffers of 48 rows (272 us: S
+// products cost nearly the same at 48 rows as at 64), rows in 16 lines a load and slots looked up in every
+// warp (247 us), rows by bulk copies into a stage of their own (345 us).
 //
 // The running maximum of a head moves only when a logit exceeds it by more than 2^11 (O^T's column and
 // the sums are rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them
@@ -214,8 +214,9 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// Two bf16 values as fp16, their exponents lowered by the head's offset (twice in `bias`, in place): what
-// falls to fp16's least exponent or below it is at most 2^-28 of the head's largest magnitude.
+// Two bf16 values as fp16, their exponents lowered by the head's offset (twice in `bias`, in place).  Exact from
+// 2^-14 on (and so from 2^-28 of the head's largest magnitude on); what falls one exponent below reads as the
+// subnormal of its mantissa, the rest as 0: off by at most 2^-15.
 __device__ __forceinline__ uint32_t bf16_to_fp16(uint32_t u, uint32_t bias) {
   const uint32_t a = __vmaxu2(u & 0x7fff7fffu, bias);
   return (a * 8u - bias * 8u) | (u & 0x80008000u);
@@ -893,9 +894,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Params p) {
 // an order that depends on the parts' number alone: the same bits on every run.
 //   Many tokens (two or three parts each): a block per boundary between two blocks and four heads, one group
 //   of 128 threads a head.
-//   Few tokens (one may have a part of every block): a block per token, head and kDimBlocks-th of the dims,
-//   eight groups.  A block that finds nothing to join costs its launch: 9664 of them about as much as the
-//   joining.
+//   Few tokens (under a quarter of the blocks; one may have a part of every block): a block per token and head,
+//   four groups.  Under 8 tokens four blocks a head, each a quarter of the dims, eight groups.  A block that
+//   finds nothing to join costs its launch: 9664 of them about as much as the joining.
+//   The rule looks at the number of tokens alone.  One request of 16384 rows among short ones, which has a part
+//   of nearly every block: 26 us for 37 tokens (by token), 36 us for 38 (by boundary: its parts one after another);
+//   64 requests of 320 rows: 23 us (by boundary).
 constexpr int kMaxParts = 256;
 template <bool kBf16, bool kByToken, int kGroups, int kHeads, int kDimBlocks>
 __global__ void __launch_bounds__(kGroups * kHeads * kKv4Dim / 4 / kDimBlocks)

@@ -12,8 +12,8 @@
 // outputs: a warp takes a run of neighbouring elements, finds the request of the first by a search in which
 // each lane looks at one place (three steps for 4096), and from there on the requests of 128 elements at a
 // time, between which a lane searches.  Where the state is updated in place the blocks are one cluster,
-// whose barrier separates its reads from the update (17 us for 1500 requests with 96000 tokens on eight
-// blocks); otherwise there are as many as have something to fill (7 us).
+// whose barrier separates its reads from the update (17.4 us for 1500 requests with 96000 tokens on eight
+// blocks); otherwise there are as many as have something to fill (7.3 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

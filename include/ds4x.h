@@ -451,7 +451,10 @@ int ds4x_kv4_read(const uint8_t* codes, const uint8_t* scales, int32_t n_slots, 
  *   workspace: at least ds4x_kv4_attn_workspace_bytes(T, max_rows) bytes, max_rows = k_top, or
  *   max_pages * page_rows without indices (may be NULL when that is 0).  Nothing is kept in it
  *   between calls; calls that may overlap on the GPU need one each.
- *   Sums over a token's rows are fp32, added up 16384 rows at a time at most and then joined.
+ *   Sums over a token's rows are fp32, added up 16384 rows at a time at most and then joined.  Softmax
+ *   weights are rounded to fp16 for the second product, in numerator and normaliser alike; bf16 queries go
+ *   through fp16 with a power of two a head, elements under 2^-28 of their head's largest magnitude come
+ *   out off by up to 2^-29 of it.
  *   The same arguments give the same bits on every run.  A call may be captured into a CUDA graph
  *   after a first call on the device.
  * ------------------------------------------------------------------------- */
