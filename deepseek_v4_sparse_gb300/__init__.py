@@ -10,7 +10,8 @@ Entry points (same names as the C ABI, without the ``ds4x_`` prefix):
   indexer_score, topk, sparse_attn, index_and_attend, workspace_bytes, decode,
   decode_workspace_bytes, topk_workspace_bytes, topk_static_scratch, device_status,
   selftest_bounded_wait, last_launch_count; the paged 4-bit cache: page_plan, kv4_append,
-  kv4_read, kv4_attn, kv4_attn_workspace_bytes
+  kv4_read, kv4_attn, kv4_attn_workspace_bytes; the paged 16-bit cache: rotate, kv16_append,
+  kv16_attn, kv16_attn_workspace_bytes
 """
 from __future__ import annotations
 
@@ -30,6 +31,7 @@ MAX_WINDOW = 1024
 MAX_RATIO = 65536
 MAX_REQ = 4096
 MAX_PAGE_ROWS = 65536
+MAX_ROT = 4096
 KV4_CODE_BYTES, KV4_SCALE_BYTES = 256, 16  # of one 512-dim row of the 4-bit cache
 EXPORTS = (
     "ds4x_indexer_score", "ds4x_topk", "ds4x_topk_workspace_bytes", "ds4x_sparse_attn",
@@ -41,6 +43,7 @@ EXPORTS = (
     "ds4x_index_and_attend_local_host", "ds4x_index_and_attend_local_host_bytes", "ds4x_compress",
     "ds4x_decode_local", "ds4x_decode_local_workspace_bytes",
     "ds4x_page_plan", "ds4x_kv4_append", "ds4x_kv4_read", "ds4x_kv4_attn", "ds4x_kv4_attn_workspace_bytes",
+    "ds4x_rotate", "ds4x_kv16_append", "ds4x_kv16_attn", "ds4x_kv16_attn_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -108,7 +111,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                       i32, f32, P, P, P, sz, P]
         lib.ds4x_kv4_attn_workspace_bytes.argtypes = [i32, i32]
         lib.ds4x_kv4_attn_workspace_bytes.restype = sz
-        for f in ("ds4x_page_plan", "ds4x_kv4_append", "ds4x_kv4_read", "ds4x_kv4_attn", "ds4x_indexer_score", "ds4x_topk", "ds4x_sparse_attn", "ds4x_index_and_attend", "ds4x_decode",
+        lib.ds4x_rotate.argtypes = [P, ctypes.c_int, P, P, i32, i32, i32, i32, i32, P, P]
+        lib.ds4x_kv16_append.argtypes = [P, ctypes.c_int, P, P, P, i32, i32, i32, P, i32, P]
+        lib.ds4x_kv16_attn.argtypes = [P, ctypes.c_int, P, i32, P, P, i32, i32, i32, P, P, i32, i32, P, P, i32, i32, i32,
+                                       f32, f32, P, P, P, P, P, P, P, sz, P]
+        lib.ds4x_kv16_attn_workspace_bytes.argtypes = [i32, i32]
+        lib.ds4x_kv16_attn_workspace_bytes.restype = sz
+        for f in ("ds4x_rotate", "ds4x_kv16_append", "ds4x_kv16_attn", "ds4x_page_plan", "ds4x_kv4_append", "ds4x_kv4_read", "ds4x_kv4_attn", "ds4x_indexer_score", "ds4x_topk", "ds4x_sparse_attn", "ds4x_index_and_attend", "ds4x_decode",
                   "ds4x_index_and_attend_host", "ds4x_local_pooled_attn", "ds4x_index_and_attend_local",
                   "ds4x_index_and_attend_local_host", "ds4x_compress", "ds4x_decode_local",
                   "ds4x_last_launch_count", "ds4x_device_status", "ds4x_selftest_bounded_wait"):
@@ -769,6 +778,144 @@ def kv4_attn(q_attn, codes, scales, tables, rows, page_rows: int, req=None, posi
                            _raw_stream(dev))
     if rc:
         _check("ds4x_kv4_attn", rc)
+    return out, lse
+
+
+# ---------------------------------------------------------------------- paged 16-bit cache
+def rotate(x, positions, inv_freq, inverse: bool = False, out=None, stream=None):
+    """x [T, H, D] (or [T, D]) fp16 or bf16 with the last 2 * len(inv_freq) elements of each row rotated by its
+    token's position: neighbours (x0, x1), pair i by positions[t] * inv_freq[i] radians (back with `inverse`).
+    positions [T] int32, inv_freq [rot / 2] float64.  out may be x (in place)."""
+    torch = _torch()
+    dt, dev = _kv_dtype(x), x.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, rotate, x, positions, inv_freq, inverse, out)
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [T, H, D] or [T, D], got {tuple(x.shape)}")
+    T, D = x.size(0), x.size(-1)
+    H = x.size(1) if x.dim() == 3 else 1
+    px = _addr("x", x, x.dtype, dev)
+    pp = _addr_n("positions", positions, torch.int32, dev, T)
+    pf = _addr("inv_freq", inv_freq, torch.float64, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape:
+        raise ValueError(f"out must be of shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    rc = (_lib or load()).ds4x_rotate(px, dt, pp, pf, T, H, D, 2 * inv_freq.numel(), 1 if inverse else 0,
+                                      _addr("out", out, x.dtype, dev), _raw_stream(dev))
+    if rc:
+        _check("ds4x_rotate", rc)
+    return out
+
+
+def _kv16_pool(pool, dtype, dev):
+    """Address of a pool [..., 512] and its number of slots."""
+    if pool.size(-1) != 512:
+        raise ValueError(f"pool must end in 512 elements, got {tuple(pool.shape)}")
+    return _addr("pool", pool, dtype, dev), pool.numel() // 512
+
+
+def kv16_append(rows, slots, pool, positions=None, inv_freq=None, stream=None):
+    """Writes row i of rows [n, 512] (fp16 or bf16) to slot slots[i] of the pool [..., 512] of the same type, its
+    last 2 * len(inv_freq) elements rotated by positions[i] as in rotate (inv_freq None: as it is); a slot outside
+    the pool (the -1 of page_plan) skips its row.  Slots must be distinct."""
+    torch = _torch()
+    dt, dev = _kv_dtype(rows), rows.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, kv16_append, rows, slots, pool, positions, inv_freq)
+    n, Dkv = rows.shape
+    pr = _addr("rows", rows, rows.dtype, dev)
+    ps = _addr_n("slots", slots, torch.int32, dev, n)
+    ppool, n_slots = _kv16_pool(pool, rows.dtype, dev)
+    pp = pf = None
+    rot = 0
+    if inv_freq is not None:
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        rot = 2 * inv_freq.numel()
+        pp = _addr_n("positions", positions, torch.int32, dev, n)
+        pf = _addr("inv_freq", inv_freq, torch.float64, dev)
+    rc = (_lib or load()).ds4x_kv16_append(pr, dt, ps, pp, pf, n, Dkv, rot, ppool, n_slots, _raw_stream(dev))
+    if rc:
+        _check("ds4x_kv16_append", rc)
+
+
+def kv16_attn_workspace_bytes(T: int, max_rows: int) -> int:
+    """Workspace of kv16_attn: max_rows = max_pages * page_rows, or min(window, that) with a window and no prefix."""
+    return int(load().ds4x_kv16_attn_workspace_bytes(T, max_rows))
+
+
+def kv16_attn(q_attn, pool, tables, rows, page_rows: int, req=None, positions=None, ratio: int = 1, window: int = 0,
+              first=None, prefix=None, scale: float | None = None, cap: float = 0.0, slopes=None, sinks=None,
+              other=None, out=None, lse=None, workspace=None, want_lse: bool = True, stream=None):
+    """64-head MQA of q_attn [T, 64, 512] over rows of the paged 16-bit cache pool [..., 512] of the same type.
+    Token t belongs to request req[t] (None: request t), which holds rows[b] rows through tables[b] [max_pages], and
+    stands behind row e - 1, e = (positions[t] + 1) // ratio (None: behind all rows held).  It sees the rows below e,
+    of these the last `window` (0: all) from first[t] on (None: 0), and those below prefix[b] even if they are not
+    below e.  cap > 0 caps the logits by cap * tanh(x / cap); slopes [64] subtract slopes[h] * |e - 1 - r|; sinks [64]
+    add exp(sinks[h]) to the normaliser; other = (out, lse) of an attention over other rows (kv4_attn over the pooled
+    ones) joins the same softmax.  Returns (out, lse)."""
+    torch = _torch()
+    i32, dev = torch.int32, q_attn.get_device()
+    contexts = _elsewhere(dev, stream)
+    if contexts is not None:
+        return _within(contexts, kv16_attn, q_attn, pool, tables, rows, page_rows, req, positions, ratio, window,
+                       first, prefix, scale, cap, slopes, sinks, other, out, lse, workspace, want_lse)
+    dt = _kv_dtype(q_attn)
+    dtype = q_attn.dtype
+    T, Hq, Dkv = shape = q_attn.shape
+    pq = _addr("q_attn", q_attn, dtype, dev)
+    ppool, n_slots = _kv16_pool(pool, dtype, dev)
+    n_req = rows.numel()
+    prow = _addr("rows", rows, i32, dev)
+    if tables.dim() != 2 or tables.size(0) != n_req:
+        raise ValueError(f"tables must be [{n_req}, max_pages], got {tuple(tables.shape)}")
+    max_pages = tables.size(1)
+    ptab = _addr("tables", tables, i32, dev)
+    preq = None if req is None else _addr_n("req", req, i32, dev, T)
+    ppos = None if positions is None else _addr_n("positions", positions, i32, dev, T)
+    pfirst = None if first is None else _addr_n("first", first, i32, dev, T)
+    pprefix = None if prefix is None else _addr_n("prefix", prefix, i32, dev, n_req)
+    pslopes = None if slopes is None else _addr_n("slopes", slopes, torch.float32, dev, Hq)
+    psinks = None if sinks is None else _addr_n("sinks", sinks, torch.float32, dev, Hq)
+    poo = pol = None
+    if other is not None:
+        oo, ol = other
+        if oo.shape != shape or ol.shape != (T, Hq):
+            raise ValueError(f"other must be of shapes {tuple(shape)} and {(T, Hq)}, got {tuple(oo.shape)} and "
+                             f"{tuple(ol.shape)}")
+        poo, pol = _addr("other's out", oo, dtype, dev), _addr("other's lse", ol, torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(q_attn)
+    elif out.shape != shape:
+        raise ValueError(f"out must be of shape {tuple(shape)}, got {tuple(out.shape)}")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    elif lse.shape != (T, Hq):
+        raise ValueError(f"lse must be of shape {(T, Hq)}, got {tuple(lse.shape)}")
+    if not (0 <= window < 2**31 and 0 < ratio < 2**31 and 0 < page_rows <= MAX_PAGE_ROWS):
+        raise ValueError(f"window, ratio or page_rows is out of range: {window}, {ratio}, {page_rows}")
+    lib = _lib or load()
+    max_rows = max_pages * page_rows
+    if prefix is None and 0 < window < max_rows:
+        max_rows = window
+    if workspace is None and 0 <= max_rows < 2**31:
+        need = lib.ds4x_kv16_attn_workspace_bytes(T, max_rows)
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    pw, wbytes = None, 0
+    if workspace is not None:
+        pw, wbytes = _addr("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size()
+    rc = lib.ds4x_kv16_attn(pq, dt, ppool, n_slots, ptab, prow, n_req, max_pages, page_rows, preq, ppos, ratio, window,
+                            pfirst, pprefix, T, Hq, Dkv, 1.0 / math.sqrt(Dkv) if scale is None else scale, cap, pslopes,
+                            psinks, poo, pol, _addr("out", out, dtype, dev),
+                            None if lse is None else _addr("lse", lse, torch.float32, dev), pw, wbytes,
+                            _raw_stream(dev))
+    if rc:
+        _check("ds4x_kv16_attn", rc)
     return out, lse
 
 

@@ -168,6 +168,32 @@ struct Kv4AttnArgs {
 size_t kv4_attn_workspace_bytes(int T, int max_rows);
 int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream);
 
+struct Kv16AttnArgs {
+  const void* q_attn;  // [T, 64, 512]
+  int bf16;
+  const void* pool;  // [n_slots, 512]
+  int n_slots;
+  const int32_t* tables;  // [n_req, max_pages]
+  const int32_t* rows;    // [n_req]
+  int n_req, max_pages, log_page;
+  const int32_t* req;        // [T] or NULL (token t = request t)
+  const int32_t* positions;  // [T] or NULL (behind all rows held)
+  int ratio, window;
+  const int32_t* first;   // [T] or NULL
+  const int32_t* prefix;  // [n_req] or NULL
+  int T;
+  float scale, cap;
+  const float *slopes, *sinks;  // [64] or NULL
+  const void* other_out;        // [T, 64, 512] or NULL
+  const float* other_lse;       // [T, 64]
+  void* out;
+  float* lse;
+  void* workspace;  // at least kv16_attn_workspace_bytes(T, max_rows)
+  int max_rows;
+};
+size_t kv16_attn_workspace_bytes(int T, int max_rows);
+int launch_kv16_attn(const Kv16AttnArgs& a, cudaStream_t stream);
+
 // The fused path (score -> top-k -> attention, Hq = 64, Dkv = 512) on validated arguments, and
 // the workspace it needs: [scores T x S fp32 | top-k scratch | split-attention scratch].
 size_t fused_workspace_bytes(int T, int S, int k_top, int window = 0);

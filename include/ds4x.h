@@ -466,6 +466,85 @@ int ds4x_kv4_attn(const void* q_attn, ds4x_dtype dtype, const uint8_t* codes, co
                   size_t workspace_bytes, void* stream);
 size_t ds4x_kv4_attn_workspace_bytes(int32_t T, int32_t max_rows);
 
+/* ---------------------------------------------------------------------------
+ * The paged 16-bit cache: raw rows (or pooled ones, with a ratio) of many requests in one pool of pages.
+ * No counterpart on the pages: the serving form of the raw window that ds4x_decode_local keeps for one
+ * sequence.  pool [n_slots, Dkv] of `dtype`, Dkv = 512; pages, tables and slots as in the 4-bit cache
+ * (ds4x_page_plan with ratio = 1 gives the raw rows' slots: raw row r is the row of position r).
+ *
+ * Rotation by position.  The last `rot` elements of a row (rot even) are pairs (x0, x1) of neighbours; pair i
+ * of a row at position p becomes
+ *     (x0 cos a - x1 sin a,  x1 cos a + x0 sin a),   a = p * inv_freq[i]   (-a for the inverse)
+ * with inv_freq [rot / 2] fp64 (finite), 8-byte aligned.  a is taken modulo a turn in 64-bit fixed point: off
+ * by at most |p| (inv_freq[i] + 1) 2^-51 + 2^-22 (radians).  The pair is turned in fp32 and rounded once.
+ * ------------------------------------------------------------------------- */
+
+#define DS4X_MAX_ROT 4096
+
+/* ---------------------------------------------------------------------------
+ * ds4x_rotate — out = x with the last `rot` elements of each row rotated by its token's position.
+ *
+ *   x, out [T, H, D] of `dtype`, positions [T] int32 (any value); D a multiple of 8, H * D <= INT32_MAX and
+ *   2 <= rot <= min(D, DS4X_MAX_ROT).
+ *   For queries on the way in, and with inverse != 0 for attention outputs (sums of rotated rows) on the
+ *   way back.  out may be x itself: then only the 16-byte pieces that hold rotated elements are
+ *   written; else they do not overlap.
+ * ------------------------------------------------------------------------- */
+int ds4x_rotate(const void* x, ds4x_dtype dtype, const int32_t* positions, const double* inv_freq,
+                int32_t T, int32_t H, int32_t D, int32_t rot, int32_t inverse, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ds4x_kv16_append — rotates n rows by their positions and writes row i to slot slots[i] of the pool.
+ *
+ *   rows [n, Dkv] and pool [n_slots, Dkv] of `dtype`, slots [n], positions [n] int32.  rot = 0: rows are
+ *   written as they are (positions and inv_freq are not read).  A slot outside [0, n_slots) skips its row (the
+ *   -1 of ds4x_page_plan).  The slots in range must be distinct; rows and pool do not overlap.
+ * ------------------------------------------------------------------------- */
+int ds4x_kv16_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, const int32_t* positions,
+                     const double* inv_freq, int32_t n, int32_t Dkv, int32_t rot, void* pool,
+                     int32_t n_slots, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ds4x_kv16_attn — 64-head attention of decode tokens, or of chunks of new tokens, over the paged 16-bit
+ * cache (a row is key and value, as in ds4x_sparse_attn).
+ *
+ *   Token t belongs to request b = req[t] (req = NULL: b = t, which needs T <= n_req; a request outside
+ *   [0, n_req) has no rows).  It stands behind row e - 1, e = floor((positions[t] + 1) / ratio)
+ *   (positions = NULL: e = the rows held; a token at a negative position sees no row), and sees the rows
+ *       max(0, first[t], e - window) <= r < min(held, max(e, prefix[b])),
+ *       held = min(rows[b], max_pages * page_rows)
+ *   (window = 0, first = NULL or prefix = NULL: without that bound): the causal rows, the last `window` of
+ *   them, those of the token's own document, and a prefix that all tokens see.  A row whose table entry is
+ *   negative or whose slot is not below n_slots is skipped (pages behind the window may have been given back).
+ *   Logit of row r, head h:
+ *       x = scale * q[t,h,:] . row_r
+ *       x = cap * tanh(x / cap)               if cap > 0
+ *       x = x - slopes[h] * |e - 1 - r|       if slopes
+ *   With w = sum_r exp(x_r) + exp(sinks[h]) (if sinks) + exp(other_lse[t,h]) (if other):
+ *       out[t,h,:] = (sum_r exp(x_r) row_r + exp(other_lse[t,h]) other_out[t,h,:]) / w,   lse[t,h] = log w
+ *   so `other`, the out and lse of an attention over other rows (ds4x_kv4_attn over the pooled ones), is joined
+ *   into one softmax.  Where w is an empty sum: out = 0 and lse = -INFINITY.  Where other_lse is -INFINITY
+ *   other_out is not read.
+ *
+ *   q_attn, out, other_out [T, Hq, Dkv] of `dtype`; lse (or NULL), other_lse [T, Hq] fp32; slopes, sinks [Hq]
+ *   fp32 or NULL; req, positions, first [T], rows, prefix [n_req] int32, tables [n_req, max_pages].
+ *   Hq = 64, Dkv = 512, cap >= 0 and finite.  out and lse overlap no input.
+ *   workspace: at least ds4x_kv16_attn_workspace_bytes(T, max_rows) bytes, max_rows the most rows that a token
+ *   can see: max_pages * page_rows, or min(window, that) with a window and no prefix (may be NULL when that is
+ *   0).  Nothing is kept in it between calls; calls that may overlap on the GPU need one each.
+ *   Sums are fp32.  Softmax weights are rounded to `dtype` for the second product, in numerator and normaliser
+ *   alike.  The same arguments give the same bits on every run.  A call may be captured into a CUDA graph after
+ *   a first call on the device.
+ * ------------------------------------------------------------------------- */
+int ds4x_kv16_attn(const void* q_attn, ds4x_dtype dtype, const void* pool, int32_t n_slots,
+                   const int32_t* tables, const int32_t* rows, int32_t n_req, int32_t max_pages,
+                   int32_t page_rows, const int32_t* req, const int32_t* positions, int32_t ratio,
+                   int32_t window, const int32_t* first, const int32_t* prefix, int32_t T, int32_t Hq,
+                   int32_t Dkv, float scale, float cap, const float* slopes, const float* sinks,
+                   const void* other_out, const float* other_lse, void* out, float* lse, void* workspace,
+                   size_t workspace_bytes, void* stream);
+size_t ds4x_kv16_attn_workspace_bytes(int32_t T, int32_t max_rows);
+
 /* Human-readable name of a ds4x_status value (static storage, never NULL). */
 const char* ds4x_status_string(int status);
 

@@ -1,0 +1,644 @@
+"""The paged 16-bit cache on the GPU against its plain implementation in 64 bits (oracle/kv16.py)."""
+import numpy as np
+import pytest
+import torch
+
+import deepseek_v4_sparse_gb300 as ds4x
+from oracle import kv4, kv16
+
+pytestmark = pytest.mark.gpu
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+I32 = torch.int32
+SCALE = 512 ** -0.5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from deepseek_v4_sparse_gb300 import build
+    build.build()
+    ds4x.load()
+    yield
+    torch.cuda.synchronize()
+    assert ds4x.device_status() == ds4x.OK
+
+
+def gpu(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def i32(a):
+    return gpu(np.asarray(a, dtype=np.int32))
+
+
+def frequencies(rot, base=10000.0):
+    return base ** (-np.arange(0, rot, 2) / rot)
+
+
+# -------------------------------------------------------------------------------------- rotation
+def turn_tolerance(y, x, positions, f, dtype):
+    """Half a step of the type for the one rounding (fp16 below its normal range: 2^-25), and the pair's length
+    times what the angle may be off: |p| (f + 1) 2^-51 + 2^-22 of the call, |p| f 2^-53 of the 64-bit angle here,
+    and 2^-22 for cos, sin and the two products in fp32."""
+    half = torch.finfo(DT[dtype]).eps / 2
+    tol = half * 1.001 * np.abs(y) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    start = y.shape[-1] - 2 * len(f)
+    length = np.hypot(x[..., start::2], x[..., start + 1::2])
+    p = np.abs(np.asarray(positions, dtype=np.float64)).reshape((-1,) + (1,) * (y.ndim - 1))
+    off = length * (p * (f + 1) * 2.0 ** -50.5 + 2.0 ** -21)
+    tol[..., start:] += np.repeat(off, 2, axis=-1)
+    return tol
+
+
+POSITIONS = [0, 1, -1, 77, 1 << 20, 999999, 2 ** 31 - 1, -2 ** 31, 12345678]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,H,D,rot", [(1, 64, 512, 64), (9, 64, 512, 64), (5, 3, 128, 128), (9, 1, 512, 512),
+                                       (4, 64, 72, 10), (2, 1, 8, 2), (3, 5, 64, 6), (7, 33, 4096, 4096)])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotate(T, H, D, rot, dtype, inverse):
+    rng = np.random.default_rng(T * 7 + rot)
+    x = torch.from_numpy(rng.standard_normal((T, H, D)) * 3).to(DT[dtype])
+    pos, f = np.array(POSITIONS[:T]), frequencies(rot)
+    args = i32(pos), gpu(f)
+    ref = kv16.rotate(x.double().numpy(), pos, f, inverse)
+    tol = turn_tolerance(ref, x.double().numpy(), pos, f, dtype)
+    dx = x.cuda()
+    y = ds4x.rotate(dx, *args, inverse=inverse)
+    assert torch.equal(dx.cpu(), x)
+    got = y.double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
+    assert torch.equal(y[..., :D - rot].cpu(), x[..., :D - rot])
+    assert ds4x.rotate(dx, *args, inverse=inverse, out=dx) is dx and torch.equal(dx, y)   # in place
+    if H == 1:
+        assert torch.equal(ds4x.rotate(x[:, 0].contiguous().cuda(), *args, inverse=inverse), y[:, 0])
+
+
+def test_rotate_back_and_odd_values():
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((6, 64, 512))).bfloat16()
+    x[0, 0, 0], x[1, 1, 447], x[2, 2, 100] = float("nan"), float("inf"), float("-inf")   # not rotated
+    x[3, 3, 448], x[4, 4, 511] = float("nan"), float("inf")
+    pos, f = i32([5, 1 << 20, 77, 3, 0, -9]), gpu(frequencies(64))
+    y = ds4x.rotate(x.cuda(), pos, f)
+    z = ds4x.rotate(y, pos, f, inverse=True).cpu()
+    assert torch.equal(z[..., :448].view(torch.int16), x[..., :448].view(torch.int16))
+    odd = ~torch.isfinite(x[..., 448:])
+    odd |= odd.reshape(6, 64, 32, 2).flip(-1).reshape(6, 64, 64)                         # and their partners
+    got, want = z[..., 448:].double()[~odd], x[..., 448:].double()[~odd]
+    # two roundings of numbers no longer than their pair, and the pair's length 2^-20 for two inexact angles
+    length = x[..., 448:].double().reshape(6, 64, 32, 2).norm(dim=-1, keepdim=True).expand(6, 64, 32, 2)
+    tol = 2.0 * 2.0 ** -8 * length.reshape(6, 64, 64)[~odd] * 1.01
+    assert torch.all((got - want).abs() <= tol)
+    assert not torch.isfinite(y.cpu()[..., 448:][odd]).any()
+
+
+def test_rotate_more_tokens_than_a_grid_axis():
+    T = 70001
+    x = torch.randn((T, 8), device="cuda").half()
+    pos = torch.arange(T, dtype=I32, device="cuda")
+    f = gpu([0.7, 1e-4])
+    y = ds4x.rotate(x, pos, f)
+    pick = torch.tensor([0, 1, 65534, 65535, 65536, 70000])
+    ref = kv16.rotate(x[pick].double().cpu().numpy(), pick.numpy(), f.cpu().numpy())
+    tol = turn_tolerance(ref, x[pick].double().cpu().numpy(), pick.numpy(), f.cpu().numpy(), "f16")
+    assert np.all(np.abs(y[pick].double().cpu().numpy() - ref) <= tol)
+    assert ds4x.rotate(x[:0], pos[:0], f).shape == (0, 8)
+
+
+# ---------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n,rot", [(0, 64), (1, 64), (7, 64), (61, 64), (300, 0), (300, 512), (1301, 2), (5000, 10),
+                                   (20011, 64)])
+def test_append(n, rot, dtype):
+    rng = np.random.default_rng(n + rot)
+    x = torch.from_numpy(rng.standard_normal((n, 512)) * 2).to(DT[dtype])
+    n_slots = n + 11
+    slots = rng.permutation(n_slots)[:n].astype(np.int32)
+    if n >= 7:
+        slots[::5] = -1
+        slots[1], slots[3] = n_slots, 2 ** 31 - 1
+        x[2, 17] = float("nan")
+    pos = rng.integers(0, 1 << 20, n).astype(np.int32)
+    before = torch.from_numpy(rng.standard_normal((n_slots, 512))).to(DT[dtype])
+    pool, f = before.cuda(), frequencies(rot) if rot else None
+    ds4x.kv16_append(x.cuda(), i32(slots), pool, **(dict(positions=i32(pos), inv_freq=gpu(f)) if rot else {}))
+    got = pool.cpu()
+    ok = (slots >= 0) & (slots < n_slots)
+    kept = np.setdiff1d(np.arange(n_slots), slots)
+    assert torch.equal(got[kept], before[kept])
+    at, xs = slots[ok], x[torch.from_numpy(ok)]
+    assert torch.equal(got[at][:, :512 - rot].view(torch.int16), xs[:, :512 - rot].view(torch.int16))
+    if rot and ok.any():
+        xn = torch.nan_to_num(xs).double().numpy()
+        ref = kv16.rotate(xn, pos[ok], f)
+        tol = turn_tolerance(ref, xn, pos[ok], f, dtype)[:, 512 - rot:]
+        g, w = got[at].double().numpy()[:, 512 - rot:], ref[:, 512 - rot:]
+        sure = torch.isfinite(xs).numpy()[:, 512 - rot:].reshape(len(at), -1, 2).all(-1).repeat(2, axis=-1)
+        assert np.all((np.abs(g - w) <= tol) | ~sure)
+
+
+# ------------------------------------------------------------------------------------- attention
+class Pool:
+    """A pool of random rows; whatever no request holds is NaN, and so is every page of a request before `gone`
+    rows of it, which the table no longer names."""
+
+    def __init__(self, rng, rows, ps, dtype, gone=None, size=1.0):
+        self.rows, self.ps = np.asarray(rows, dtype=np.int32), ps
+        B = len(self.rows)
+        held = -(-self.rows // ps)
+        skip = [0] * B if gone is None else [g // ps for g in gone]
+        self.max_pages = max(1, int(held.max(initial=0)))
+        n_pages = int(held.sum()) + 3
+        self.n_slots = n_pages * ps
+        pages = rng.permutation(n_pages)
+        self.tables = np.full((B, self.max_pages), -1, dtype=np.int32)
+        pool = torch.full((self.n_slots, 512), float("nan"), dtype=DT[dtype])
+        k = 0
+        for b in range(B):
+            for pg in range(skip[b], held[b]):
+                self.tables[b, pg] = pages[k]
+                k += 1
+                n = min(ps, self.rows[b] - pg * ps)
+                x = rng.standard_normal((n, 512)) * size * np.exp2(rng.integers(-3, 2, (n, 1)).astype(float))
+                at = self.tables[b, pg] * ps
+                pool[at:at + n] = torch.from_numpy(x).to(DT[dtype])
+        self.dev = pool.cuda(), i32(self.tables), i32(self.rows)
+
+    def values(self):
+        return self.dev[0].double().cpu().numpy()
+
+
+def tolerance(x, kv, w, out, dtype, cap):
+    """How far out [H, 512] and lse [H] of one token may be: logits x [H, n] of the rows kv [n, 512] (the other
+    attention's output and the sink among them, if any) with normalised weights w [H, n]; `x` comes with ex [H],
+    the bound on what a logit may be off.
+
+    A weight moves by 2 ex + 2^-20 (2^x and its argument, whose size counts: 2^-23 |x|) relative, and is rounded
+    to `dtype` once, half a step u, in numerator and normaliser alike: a normalised weight moves by at most
+    eta = 2 (u + 2 ex'), and |out - ref| <= eta sum_j w_j |kv_j - ref|.  The largest weight of a head is at least
+    one before the sum, so those below fp16's normal range are off by 2^-25 each at most against it.
+    The output is rounded once: half a step, 2^-25 below fp16's normal range."""
+    logit, ex = x
+    u = torch.finfo(DT[dtype]).eps / 2
+    size = np.where(np.isfinite(logit), np.abs(logit), 0).max(axis=1, initial=0.0)
+    ex = ex + 2.0 ** -20 + 2.0 ** -22 * size + cap * 2.0 ** -20
+    eta = 2 * (u + 2 * ex)
+    spread = np.stack([w[h] @ np.abs(kv[h] - out[h][None, :]) for h in range(w.shape[0])])
+    tiny = kv.shape[1] * 2.0 ** -25 * np.abs(kv).max(initial=0.0) * (dtype == "f16")
+    return (eta[:, None] * spread + tiny + u * 1.01 * np.abs(out) + 2.0 ** -25, 2 * ex)
+
+
+def check_attn(q, pool, got, lse, dtype, scale, opts, lists, tokens=None):
+    vals = pool.values()
+    T = q.shape[0]
+    qd, g, gl = q.double().cpu().numpy(), got.double().cpu().numpy(), lse.double().cpu().numpy()
+    host = {k: v for k, v in opts.items()}
+    if "other" in host:
+        host["other"] = tuple(t.double().cpu().numpy() for t in host["other"])
+    for t in range(T) if tokens is None else tokens:
+        one = {k: (v[t:t + 1] if k in ("req", "positions", "first") and v is not None else v) for k, v in lists.items()}
+        if one.get("req") is None:
+            one["req"] = [t]
+        if "other" in host:
+            one_host = dict(host, other=(host["other"][0][t:t + 1], host["other"][1][t:t + 1]))
+        else:
+            one_host = host
+        tabs = dict(tables=pool.tables, rows=pool.rows, page_rows=pool.ps)
+        ref, rlse = kv16.attn(qd[t:t + 1], vals, scale, **one_host, **tabs, **one)
+        ref, rlse = ref[0], rlse[0]
+        e, see, at = kv16.seen_rows(0, n_slots=pool.n_slots, **tabs, **one)
+        none = np.isneginf(rlse)
+        assert np.all(np.isneginf(gl[t][none])) and np.all(g[t][none] == 0), t
+        if none.all():
+            continue
+        kv = vals[at] if at else np.zeros((0, 512))
+        x = kv16.logits(qd[t], kv, see, e, scale, opts.get("cap", 0.0), opts.get("slopes")) if at else np.zeros((64, 0))
+        # 512 exact products summed in fp32 by a truncating adder, 64 steps of at most 2^-23 of the magnitudes
+        ex = 64 * 2.0 ** -23 * scale * (np.abs(qd[t]) @ np.abs(kv).T).max(axis=1, initial=0.0)
+        kvh = np.broadcast_to(kv, (64,) + kv.shape)
+        if "sinks" in opts:
+            x = np.concatenate([x, np.asarray(opts["sinks"])[:, None]], 1)
+            kvh = np.concatenate([kvh, np.zeros((64, 1, 512))], 1)
+        if "other" in opts:
+            ol = one_host["other"][1][0]
+            x = np.concatenate([x, ol[:, None]], 1)
+            kvh = np.concatenate([kvh, np.where(np.isneginf(ol)[:, None], 0.0, one_host["other"][0][0])[:, None, :]], 1)
+        with np.errstate(invalid="ignore"):
+            w = np.where(none[:, None], 0.0, np.exp(x - rlse[:, None]))
+        tol, ltol = tolerance((x, ex), kvh, w, ref, dtype, opts.get("cap", 0.0))
+        assert np.all(np.isfinite(g[t][~none])), t
+        worst = (np.abs(g[t] - ref) / tol).max()
+        assert worst <= 1, (t, len(at), worst)
+        assert np.all(np.abs(gl[t] - rlse)[~none] <= ltol[~none]), (t, np.abs(gl[t] - rlse).max())
+
+
+def queries(rng, T, dtype, size=1.0):
+    return torch.from_numpy(rng.standard_normal((T, 64, 512)) * size).to(DT[dtype]).cuda()
+
+
+def on_gpu(opts, lists):
+    kw = {k: (v if k in ("ratio", "window") or v is None else i32(v)) for k, v in lists.items()}
+    for k, v in opts.items():
+        kw[k] = v if k in ("cap", "other") else gpu(np.asarray(v, dtype=np.float32))
+    return kw
+
+
+def run_attn(q, pool, opts, lists, **kw):
+    return ds4x.kv16_attn(q, *pool.dev, pool.ps, **on_gpu(opts, lists), **kw)
+
+
+def options(rng, T, dtype, cap=False, slopes=False, sinks=False, other=False):
+    o = {}
+    if cap:
+        o["cap"] = 1.5
+    if slopes:
+        o["slopes"] = np.float32(np.exp2(-rng.uniform(0, 9, 64)))
+    if sinks:
+        o["sinks"] = np.float32(rng.standard_normal(64) * 3)
+        o["sinks"][5] = -np.inf
+    if other:
+        lse = torch.from_numpy(rng.standard_normal((T, 64)) * 2 + 2).float()
+        out = torch.from_numpy(rng.standard_normal((T, 64, 512))).to(DT[dtype])
+        lse[::3] = float("-inf")               # tokens of which the other attention saw nothing:
+        out[::3] = float("nan")                # what it wrote for them is not looked at
+        o["other"] = out.cuda(), lse.cuda()
+    return o
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,ps", [
+    ([1], 64), ([2], 1), ([15], 8), ([16], 16), ([17], 16), ([64], 64), ([127], 32), ([128], 128), ([129], 4),
+    ([255], 64), ([700], 64), ([300, 1, 65, 0, 128, 129, 31], 16), ([2000, 1500], 256), ([5000], 2),
+])
+def test_attn_all_rows(rows, ps, dtype):
+    """A token a request, every row held; no positions, then the positions that mean the same."""
+    rng = np.random.default_rng(sum(rows) + ps)
+    pool = Pool(rng, rows, ps, dtype)
+    q = queries(rng, len(rows), dtype)
+    out, lse = run_attn(q, pool, {}, {})
+    check_attn(q, pool, out, lse, dtype, SCALE, {}, {})
+    lists = dict(req=np.arange(len(rows)), positions=np.asarray(rows) - 1)
+    out2, lse2 = run_attn(q, pool, {}, lists)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("opt", ["", "cap", "slopes", "sinks", "other", "cap slopes sinks other"])
+def test_attn_options(opt, dtype):
+    rng = np.random.default_rng(len(opt))
+    rows = [400, 0, 130, 129, 1, 77]
+    pool = Pool(rng, rows, 16, dtype)
+    q = queries(rng, 6, dtype)
+    opts = options(rng, 6, dtype, **{k: True for k in opt.split()})
+    out, lse = run_attn(q, pool, opts, {})
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, {})
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("window", [1, 7, 64, 127, 128, 129, 200, 1000])
+def test_attn_window(window, dtype):
+    """Chunks of three requests whose pages before the chunk's first window are gone, sinks and a join."""
+    rng = np.random.default_rng(window)
+    rows, per, ps = [300, 40, 517], 23, 16
+    pos = np.concatenate([np.arange(n - per, n) for n in rows])
+    gone = [max(0, n - per + 1 - window) for n in rows]
+    pool = Pool(rng, rows, ps, dtype, gone=gone)
+    lists = dict(req=np.repeat(np.arange(3), per), positions=pos, window=window)
+    q = queries(rng, 3 * per, dtype)
+    opts = options(rng, 3 * per, dtype, sinks=True, other=True)
+    out, lse = run_attn(q, pool, opts, lists)
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, lists, tokens=range(0, 3 * per, 4))
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, lists, tokens=range(3 * per - 3, 3 * per))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attn_masks_that_meet(dtype):
+    """Documents, a prefix, a window, negative positions, requests that are none, rows not held yet."""
+    rng = np.random.default_rng(8)
+    rows = [260, 33, 0, 150]
+    pool = Pool(rng, rows, 8, dtype)
+    T = 40
+    req = rng.integers(-1, 6, T)
+    pos = rng.integers(-2, 300, T)
+    first = np.where(rng.random(T) < 0.5, 0, rng.integers(0, 280, T))
+    first[3] = -5
+    lists = dict(req=req, positions=pos, first=first, prefix=np.array([90, 50, 7, -3]), window=120)
+    q = queries(rng, T, dtype)
+    opts = options(rng, T, dtype, slopes=True, cap=True)
+    out, lse = run_attn(q, pool, opts, lists)
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, lists)
+    assert torch.isneginf(lse).all(1).any()                       # some token saw nothing
+    for drop in ("first", "prefix", "window"):
+        some = {k: v for k, v in lists.items() if k != drop}
+        out, lse = run_attn(q, pool, opts, some)
+        check_attn(q, pool, out, lse, dtype, SCALE, opts, some, tokens=range(0, T, 3))
+
+
+@pytest.mark.parametrize("ratio", [4, 128])
+def test_attn_pooled_rows(ratio):
+    """Rows of several positions each: the ratio of the pooled rows."""
+    rng = np.random.default_rng(ratio)
+    rows = [70, 300]
+    pool = Pool(rng, rows, 32, "bf16")
+    pos = np.array([0, ratio - 1, 70 * ratio - 1, 69 * ratio, 5, 299 * ratio, 300 * ratio - 1, 2 ** 31 - 1])
+    lists = dict(req=[0, 0, 0, 0, 1, 1, 1, 1], positions=pos, ratio=ratio, window=150)
+    q = queries(rng, 8, "bf16")
+    opts = options(rng, 8, "bf16", slopes=True)
+    out, lse = run_attn(q, pool, opts, lists)
+    check_attn(q, pool, out, lse, "bf16", SCALE, opts, lists)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attn_loud_logits(dtype):
+    """Logits of some hundreds, whose maximum moves from chunk to chunk, and biases that dwarf them."""
+    rng = np.random.default_rng(4)
+    pool = Pool(rng, [900, 700], 64, dtype, size=6.0)
+    q = queries(rng, 2, dtype, size=20.0)
+    for opts in ({}, dict(slopes=np.float32(np.linspace(0, 40, 64)))):
+        out, lse = run_attn(q, pool, opts, {})
+        check_attn(q, pool, out, lse, dtype, SCALE, opts, {})
+    up = dict(slopes=np.float32(np.linspace(0, -40, 64)))          # far rows count most
+    out, lse = run_attn(q, pool, up, {})
+    check_attn(q, pool, out, lse, dtype, SCALE, up, {})
+
+
+@pytest.mark.parametrize("T,rows", [(1, 20001), (3, 3000), (40, 900), (37, 2600), (160, 300)])
+def test_attn_splits(T, rows):
+    """Few tokens over many rows, many over some: tokens whose rows lie in several blocks."""
+    rng = np.random.default_rng(T)
+    n = rng.integers(1, rows + 1, T)
+    n[0] = rows
+    pool = Pool(rng, n, 64, "bf16")
+    q = queries(rng, T, "bf16")
+    opts = options(rng, T, "bf16", sinks=True, other=True)
+    out, lse = run_attn(q, pool, opts, {})
+    check_attn(q, pool, out, lse, "bf16", SCALE, opts, {}, tokens=range(0, T, max(1, T // 12)))
+    again, _ = run_attn(q, pool, opts, {})
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+def test_attn_chunk_of_many_tokens():
+    """More tokens than one launch plans for, over a causal chunk."""
+    rng = np.random.default_rng(6)
+    T = 2300
+    pool = Pool(rng, [T], 32, "bf16")
+    lists = dict(req=np.zeros(T, np.int32), positions=np.arange(T), window=200, first=np.arange(T) // 701 * 701)
+    q = queries(rng, T, "bf16")
+    out, lse = run_attn(q, pool, {}, lists)
+    check_attn(q, pool, out, lse, "bf16", SCALE, {}, lists,
+               tokens=[0, 1, 127, 128, 200, 700, 701, 702, 1500, 2047, 2048, 2049, 2299])
+
+
+def test_attn_nan_rows():
+    """A NaN row reaches the tokens that see it and no others."""
+    rng = np.random.default_rng(5)
+    pool = Pool(rng, [200, 200], 16, "bf16")
+    bad = pool.tables[0, 150 // 16] * 16 + 150 % 16
+    pool.dev[0][bad, 100] = float("nan")
+    pos = np.array([149, 150, 151, 199, 199])
+    lists = dict(req=[0, 0, 0, 0, 1], positions=pos, window=49)
+    q = queries(rng, 5, "bf16")
+    out, lse = run_attn(q, pool, {}, lists)
+    assert torch.isnan(lse).all(1).tolist() == [False, True, True, False, False]     # 199 - 49 + 1 = 151
+    assert torch.isfinite(out).all(2).all(1).tolist() == [True, False, False, True, True]
+    check_attn(q, pool, out, lse, "bf16", SCALE, {}, lists, tokens=[0, 3, 4])
+
+
+def test_attn_nothing_to_see():
+    q = torch.randn((3, 64, 512), device="cuda").half()
+    pool = torch.full((64, 512), float("nan"), dtype=torch.float16, device="cuda")
+    z = i32([0, 0, 0])
+    for tables, rows in ((i32([[0], [1], [2]]), z), (i32([[-1], [-1], [-1]]), i32([9, 9, 9])),
+                         (i32([[77], [64], [100]]), i32([9, 9, 9])), (torch.empty((3, 0), dtype=I32, device="cuda"), z)):
+        out, lse = ds4x.kv16_attn(q, pool, tables, rows, 16)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+    sinks = torch.randn(64, device="cuda")
+    out, lse = ds4x.kv16_attn(q, pool, i32([[0], [1], [2]]), z, 16, sinks=sinks)
+    assert (out == 0).all() and (lse - sinks).abs().max() <= 2.0 ** -20
+    o, l = torch.randn((3, 64, 512), device="cuda").half(), torch.randn((3, 64), device="cuda")
+    out, lse = ds4x.kv16_attn(q, pool, i32([[0], [1], [2]]), z, 16, other=(o, l))
+    assert (out.float() - o.float()).abs().max() <= 2.0 ** -9 and (lse - l).abs().max() <= 2.0 ** -20
+    out, lse = ds4x.kv16_attn(q[:0], pool, i32([[0]]), i32([4]), 16)
+    assert out.shape == (0, 64, 512) and lse.shape == (0, 64)
+    out, lse = ds4x.kv16_attn(q[:1], pool[:0], i32([[0]]), i32([4]), 16)
+    assert (out == 0).all()
+
+
+def test_attn_writes_its_tokens_only():
+    rng = np.random.default_rng(2)
+    pool = Pool(rng, [300, 200], 16, "f16")
+    q = queries(rng, 2, "f16")
+    buf = torch.full((4, 64, 512), 7.0, dtype=torch.float16, device="cuda")
+    lb = torch.full((4, 64), 7.0, device="cuda")
+    run_attn(q, pool, {}, {}, out=buf[1:3], lse=lb[1:3])
+    want, wl = run_attn(q, pool, {}, {})
+    assert torch.equal(buf[1:3], want) and torch.equal(lb[1:3], wl)
+    assert (buf[[0, 3]] == 7).all() and (lb[[0, 3]] == 7).all()
+    alone, none = run_attn(q, pool, {}, {}, want_lse=False)
+    assert none is None and torch.equal(alone, want)
+
+
+def test_rows_far_into_a_large_pool():
+    """Slots whose elements lie beyond 2^31, and beyond 2^32 bytes."""
+    n_slots = (1 << 22) + 4096
+    pool = torch.empty((n_slots, 512), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(rng.standard_normal((130, 512))).bfloat16().cuda()
+    slots = torch.arange(n_slots - 130, n_slots, dtype=I32, device="cuda")
+    ds4x.kv16_append(x, slots, pool)
+    assert torch.equal(pool[-130:], x)
+    small = torch.zeros((192, 512), dtype=torch.bfloat16, device="cuda")
+    small[62:] = x
+    q = queries(rng, 1, "bf16")
+    first = i32([62])
+    a = ds4x.kv16_attn(q, pool, i32([[n_slots // 64 - 3, n_slots // 64 - 2, n_slots // 64 - 1]]), i32([192]), 64, first=first)
+    b = ds4x.kv16_attn(q, small, i32([[0, 1, 2]]), i32([192]), 64, first=first)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_many_tokens_beyond_32_bit_offsets():
+    T = 66000                                                      # 2.16e9 elements
+    pool = torch.randn((64, 512), device="cuda").half()
+    q = torch.zeros((T, 64, 512), dtype=torch.float16, device="cuda")
+    q[-1] = torch.randn((64, 512), device="cuda").half()
+    req = torch.zeros(T, dtype=I32, device="cuda")
+    pos = torch.arange(T, device="cuda", dtype=I32) % 64
+    out, lse = ds4x.kv16_attn(q, pool, i32([[0]]), i32([64]), 64, req=req, positions=pos, window=2)
+    one, l1 = ds4x.kv16_attn(q[-1:].clone(), pool, i32([[0]]), i32([64]), 64, req=req[:1], positions=pos[-1:], window=2)
+    assert torch.equal(out[-1], one[0]) and torch.equal(lse[-1], l1[0])
+    mean = (pool[61].float() + pool[62].float()) / 2               # a query of zeros: the mean of its two rows
+    t = 62 + 64 * 1030
+    assert (out[t].float() - mean).abs().max() <= 2.0 ** -10 * 1.01 * mean.abs().max()
+    back = ds4x.rotate(out, pos, gpu(frequencies(64)), out=out)
+    assert torch.isfinite(back[-1]).all()
+
+
+# ------------------------------------------------------------------------ as they are used together
+def test_captured_step_and_two_streams():
+    """A captured step replayed on new values, and two calls at once on streams of their own."""
+    rng = np.random.default_rng(12)
+    pool = Pool(rng, [500] * 5, 16, "bf16")
+    f = gpu(frequencies(64))
+    q, x = queries(rng, 5, "bf16"), torch.randn((5, 512), device="cuda").bfloat16()
+    slots = i32([pool.tables[b, 499 // 16] * 16 + 499 % 16 for b in range(5)])
+    pos = i32([499] * 5)
+    req = i32(range(5))
+
+    def step():
+        ds4x.kv16_append(x, slots, pool.dev[0], positions=pos, inv_freq=f)
+        out, lse = ds4x.kv16_attn(ds4x.rotate(q, pos, f), *pool.dev, 16, req=req, positions=pos)
+        return ds4x.rotate(out, pos, f, inverse=True), lse
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        q.copy_(torch.randn_like(q))
+        x.copy_(torch.randn_like(x))
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in got]
+        want = step()
+        assert torch.equal(replayed[0], want[0]) and torch.equal(replayed[1], want[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    qs = [queries(rng, 5, "bf16") for _ in range(2)]
+    want = [ds4x.kv16_attn(a, *pool.dev, 16) for a in qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [ds4x.kv16_attn(a, *pool.dev, 16, stream=s) for a, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_serving_step_of_both_caches():
+    """Two steps of a batch: plans of both caches, raw rows rotated into the 16-bit one, pooled rows into the 4-bit
+    one, attention over both in one softmax, and the outputs turned back."""
+    rng = np.random.default_rng(21)
+    B, ratio, ps, rps, window = 4, 4, 8, 16, 50
+    f = frequencies(64)
+    df = gpu(f)
+    dt = torch.bfloat16
+    mk = lambda n, p: (torch.full((B, n), -1, dtype=I32, device="cuda"),  # noqa: E731
+                       i32(rng.permutation(p)), i32([p]))
+    tab, free, n_free = mk(12, 60)
+    rtab, rfree, rn_free = mk(24, 100)
+    codes = torch.zeros((60 * ps, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((60 * ps, 16), dtype=torch.uint8, device="cuda")
+    raw = torch.full((100 * rps, 512), float("nan"), dtype=dt, device="cuda")
+    seen = i32([0] * B)
+    rows, rrows = i32([0] * B), i32([0] * B)
+    history = [np.zeros((0, 512)) for _ in range(B)]
+    pooled = [np.zeros((0, 512)) for _ in range(B)]
+    for new in ([70, 1, 0, 33], [1, 60, 5, 200]):
+        T = sum(new) + 3
+        R = T // ratio + B
+        x = torch.from_numpy(rng.standard_normal((T, 512))).to(dt).cuda()
+        p4 = torch.from_numpy(rng.standard_normal((R, 512))).to(dt).cuda()
+        q = queries(rng, T, "bf16")
+        nn = i32(new)
+        rp = ds4x.page_plan(seen, nn, rrows, rtab, rfree, rn_free, 1, rps, T, T)
+        pos, req, rslots = rp[:3]
+        pp = ds4x.page_plan(seen, nn, rows, tab, free, n_free, ratio, ps, T, R)
+        ds4x.kv16_append(x, rslots, raw, positions=pos, inv_freq=df)
+        ds4x.kv4_append(p4, pp[2], codes, scales)
+        seen, rrows, rn_free = rp[3], rp[4], rp[5]
+        rows, n_free = pp[4], pp[5]
+        qr = ds4x.rotate(q, pos, df)
+        part = ds4x.kv4_attn(qr, codes, scales, tab, rows, ps, req=req, positions=pos, ratio=ratio)
+        out, lse = ds4x.kv16_attn(qr, raw, rtab, rrows, rps, req=req, positions=pos, window=window, other=part)
+        back = ds4x.rotate(out, pos, df, inverse=True)
+        # the same from the definitions, in 64 bits on the operands as the caches hold them
+        hp, hr, hs = (t.cpu().numpy() for t in (pos, req, pp[2]))
+        stored = raw.double().cpu().numpy()[np.maximum(rslots.cpu().numpy(), 0)]
+        vals = kv4.values(codes.cpu().numpy(), scales.cpu().numpy())
+        for t in range(T):
+            if hr[t] >= 0:
+                history[hr[t]] = np.concatenate([history[hr[t]], stored[t:t + 1]])
+        ends = np.cumsum([(s + n) // ratio - s // ratio for s, n in zip(before_of(hp, hr, B, new, seen), new)])
+        k = 0
+        for b in range(B):
+            while k < ends[b]:
+                pooled[b] = np.concatenate([pooled[b], vals[hs[k]][None]])
+                k += 1
+        qd = qr.double().cpu().numpy()
+        go, gl, gb = (t.double().cpu().numpy() for t in (out, lse, back))
+        assert np.all(hr[-3:] == -1) and np.all(go[-3:] == 0) and np.all(np.isneginf(gl[-3:]))
+        for t in range(T - 3):
+            b, p = hr[t], hp[t]
+            kv = np.concatenate([pooled[b][:(p + 1) // ratio], history[b][max(0, p + 1 - window):p + 1]])
+            lg = qd[t] @ kv.T * SCALE
+            m = lg.max(1, keepdims=True)
+            w = np.exp(lg - m)
+            ref = w @ kv / w.sum(1, keepdims=True)
+            # weights and the pooled part's output are rounded to bf16 on the way, the output once more
+            spread = np.stack([(w[h] / w[h].sum()) @ np.abs(kv - ref[h]) for h in range(64)])
+            tol = 2.0 ** -8 * (2.2 * spread + 2.1 * np.abs(ref) + 0.01 * np.abs(kv).max())
+            assert np.all(np.abs(go[t] - ref) <= tol + 2.0 ** -8 * 0.2), t
+            assert np.all(np.abs(gl[t] - (m[:, 0] + np.log(w.sum(1)))) <= 1e-4)
+            turned = kv16.rotate(go[t][None], [p], f, inverse=True)[0]
+            assert np.all(np.abs(gb[t] - turned) <= 2.0 ** -8 * 1.01 * np.abs(turned) + 2.0 ** -20 * 4)
+
+
+def before_of(positions, req, B, new, seen):
+    """Positions of each request before the step."""
+    return [int(s) - n for s, n in zip(seen.cpu().numpy(), new)]
+
+
+def test_agrees_with_the_dense_window_attention():
+    """One request: the pooled rows from the 4-bit cache, the window from the 16-bit one, against the dense entry."""
+    rng = np.random.default_rng(33)
+    S, T, window, L = 96, 12, 40, 400
+    codes = gpu(rng.integers(0, 256, (S, 256), dtype=np.uint8))
+    scales = gpu(rng.integers(124, 127, (S, 16), dtype=np.uint8))
+    kv = ds4x.kv4_read(codes, scales, i32(range(S)), torch.bfloat16)
+    raw = torch.randn((L, 512), device="cuda").bfloat16()
+    pos = np.arange(L - T, L)
+    q = queries(rng, T, "bf16")
+    idx = np.sort(np.stack([rng.permutation(S)[:64] for _ in range(T)]), axis=1)
+    req = i32([0] * T)
+    dense, dlse = ds4x.local_pooled_attn(q, kv, raw, i32(idx), i32(pos), 0, window)
+    part = ds4x.kv4_attn(q, codes, scales, i32([[0]]), i32([S]), 128, req=req, indices=i32(idx))
+    out, lse = ds4x.kv16_attn(q, raw, i32([range(L // 16)]), i32([L]), 16, req=req, positions=i32(pos), window=window,
+                              other=part)
+    # each side rounds weights, parts and outputs to bf16: a few half steps of numbers of order one
+    assert (out.float() - dense.float()).abs().max() <= 4 * 2.0 ** -8
+    assert (lse - dlse).abs().max() <= 4 * 2.0 ** -8
+
+
+def test_refusals_on_the_device():
+    q = torch.zeros((2, 64, 512), dtype=torch.float16, device="cuda")
+    pool = torch.zeros((32, 512), dtype=torch.float16, device="cuda")
+    tab, rows = i32([[0], [1]]), i32([3, 3])
+    call = lambda **kw: ds4x.kv16_attn(q, pool, tab, rows, 16, **kw)  # noqa: E731
+    for bad in (dict(positions=i32([1])), dict(first=i32([0])), dict(prefix=i32([0])), dict(req=torch.zeros(2, device="cuda")),
+                dict(sinks=torch.zeros(3, device="cuda")), dict(slopes=torch.zeros(64, dtype=torch.float64, device="cuda")),
+                dict(other=(q[:1], torch.zeros((2, 64), device="cuda"))), dict(out=q[:1]), dict(window=-1), dict(ratio=0),
+                dict(window=1 << 40), dict(other=(q.bfloat16(), torch.zeros((2, 64), device="cuda")))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(ds4x.Ds4xError):
+        call(cap=-1.0)
+    with pytest.raises(ValueError):
+        ds4x.kv16_attn(q, pool.bfloat16(), tab, rows, 16)
+    with pytest.raises(ValueError):
+        ds4x.kv16_attn(q.transpose(1, 2).contiguous().transpose(1, 2), pool, tab, rows, 16)
+    if ds4x.kv16_attn_workspace_bytes(2, 16):
+        with pytest.raises(ds4x.Ds4xError):
+            call(workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    f = torch.zeros(32, dtype=torch.float64, device="cuda")
+    with pytest.raises(ValueError):
+        ds4x.rotate(q, rows, f.float())
+    with pytest.raises(ValueError):
+        ds4x.rotate(q, rows[:1], f)
+    with pytest.raises(ValueError):
+        ds4x.kv16_append(q[0], rows, pool)                        # 64 rows, two slots
+    with pytest.raises(ValueError):
+        ds4x.kv16_append(q[0, :2], rows, pool, inv_freq=f)
+    with pytest.raises(ds4x.Ds4xError):
+        ds4x.rotate(q, rows, f[:0])
