@@ -29,7 +29,8 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 
 // Device status word: 0 = ok, otherwise (site << 8) | 5 (5 = -DS4X_ERR_TIMEOUT).
 // A site names one wait of one source file: scorer 1-19 and 0x7e, sparse attention 20-49 and 0x7f, top-k 50-69,
-// compressor 70-78, attention over the 4-bit cache 79-99 and 0x7d, self-test 0x7c.
+// compressor 70-78, attention over the 4-bit cache 79-99 and 0x7d, over the 16-bit cache 100-119 and 0x7b,
+// self-test 0x7c.
 __device__ __forceinline__ void report_timeout(int* status, int site) {
   if (status) atomicCAS(status, 0, (site << 8) | 5);
 }
