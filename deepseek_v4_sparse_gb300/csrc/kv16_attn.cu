@@ -20,21 +20,23 @@
 // whole 16-byte pieces: 32 heads of a row.
 //
 // Warps: 0-7 copy rows (16-byte cp.async, 16 rows of a chunk each: one step of the O^T products), 8-15 softmax
-// (rows by quadrant, 32 heads each), 16-19 write the output (O^T lanes by quadrant), 20 issues the S^T products,
-// 21 the O^T products, 22 looks up the rows' slots a few chunks ahead and brings the rows to L2, 23 loads q.
+// (16 rows each), 16-23 write the output (O^T lanes by quadrant, 32 heads each), 24 issues the S^T products,
+// 25 the O^T products, 26 looks up the rows' slots a few chunks ahead and brings the rows to L2, 27 loads q.
 // There is room for one chunk: it is copied and released in quarters of the dims, so that the next chunk comes in
 // while the O^T products go through this one.  O^T rotates over seven 64-column TMEM slots (a token uses four).
 // A chunk that is not full costs its O^T products and copies by 16 rows.
 //
-// The running maximum of a head moves only when a logit exceeds it by more than 2^11 (O^T and the sums are
-// rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them below fp16's
-// largest value and small ones away from its least.  Statistics and sums are fp32.  Weights are rounded to the rows'
+// The running maximum of a head moves only when a logit exceeds it by more than 2^11 in fp16, 2^32 in bf16 (O^T and
+// the sums are rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them below
+// fp16's largest value and small ones away from its least.  Statistics and sums are fp32.  Weights are rounded to the rows'
 // type, which the matrix unit asks for (8 bits in bf16); out is normalised by the sum of the rounded weights, so that
 // what a weight's rounding does to a row it does to the normaliser too; lse takes the exact ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "ds4x_internal.h"
 #include "ds4x_ptx.cuh"
@@ -53,12 +55,12 @@ constexpr int kQBlockBytes = kHq * 128;          // 8 KB (64 heads x 64 dims)
 constexpr int kQBytes = kSlots * kQBlockBytes;   // 64 KB
 constexpr int kPBytes = kRows * 128;             // 16 KB: P[row][head]
 constexpr int kTokens = 2048;                    // tokens a launch plans for
-constexpr int kSoftWarp = 8, kOutWarp = 16, kSWarp = 20, kOWarp = 21, kSlotWarp = 22, kQWarp = 23;
-constexpr int kCopyWarps = 8, kSoftWarps = 8, kOutWarps = 4;
-constexpr int kWarps = 24, kThreads = 32 * kWarps;
-// registers a thread: 80 at launch; the sum over the six warpgroups stays what it was
-constexpr int kLaunchRegs = 80, kCopyRegs = 56, kMiscRegs = 40, kSoftRegs = 120, kOutRegs = 88;
-static_assert(kThreads * kLaunchRegs <= 65536 && 2 * kCopyRegs + 2 * kSoftRegs + kOutRegs + kMiscRegs <= 6 * kLaunchRegs, "registers");
+constexpr int kSoftWarp = 8, kOutWarp = 16, kSWarp = 24, kOWarp = 25, kSlotWarp = 26, kQWarp = 27;
+constexpr int kCopyWarps = 8, kSoftWarps = 8, kOutWarps = 8;
+constexpr int kWarps = 28, kThreads = 32 * kWarps;
+// registers a thread: 72 at launch; the sum over the seven warpgroups stays what it was
+constexpr int kLaunchRegs = 72, kCopyRegs = 48, kMiscRegs = 40, kSoftRegs = 104, kOutRegs = 80;
+static_assert(kThreads * kLaunchRegs <= 65536 && 2 * (kCopyRegs + kSoftRegs + kOutRegs) + kMiscRegs <= 7 * kLaunchRegs, "registers");
 constexpr int kRing = 4;                         // chunks whose slots are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
@@ -69,13 +71,12 @@ constexpr int kOffP = kOffKV + kKvBytes;
 constexpr int kOffRows = kOffP + kPBytes;        // int[kTokens]: rows of each token's list
 constexpr int kOffSlots = kOffRows + kTokens * 4;      // int[kRing][kRows]: slot of each row of the chunk, -1 for none
 constexpr int kOffAhead = kOffSlots + kRing * kRows * 4;  // int[kRing]: e - hi of the chunk's token
-constexpr int kOffStat = kOffAhead + kRing * 4;        // float[2 items][4 quadrants][sum of rounded weights, sum][64]
-constexpr int kOffM = kOffStat + 2 * 4 * 2 * kHq * 4;  // float[2 items][64]: offsets
-constexpr int kOffMax = kOffM + 2 * kHq * 4;     // float[4 quadrants][64]: maxima of one chunk
-constexpr int kOffAlpha = kOffMax + 4 * kHq * 4; // float[64]: rescale factors of one chunk
+constexpr int kOffStat = kOffAhead + kRing * 4;        // float[softmax warps][sum of rounded weights, sum][64] of an item
+constexpr int kOffM = kOffStat + kSoftWarps * 2 * kHq * 4;  // float[2 items][64]: offsets
+constexpr int kOffAlpha = kOffM + 2 * kHq * 4;   // float[64]: rescale factors of one chunk
 constexpr int kOffSlope = kOffAlpha + kHq * 4;   // float[64]: slopes in log2 units
 constexpr int kOffJoin = kOffSlope + kHq * 4;    // float[5][64]: a token's offset, sum of rounded weights and sum so far; factors
-                                                 // of the sums so far (or of the other attention) and of the item's
+                                                 // of the sums so far and of the item's
 constexpr int kOffScan = kOffJoin + 5 * kHq * 4; // int64[kWarps] warp sums, then int[4]: the block's part
 constexpr int kOffBars = kOffScan + kWarps * 8 + 16;
 constexpr int kNumBars = 2 + 2 * kRing + 2 * kPairs + 4 + 2 * kOSlots + 4;
@@ -83,7 +84,7 @@ constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kColO = 64;  // S^T in columns [0, 64), O^T from 64
-constexpr float kRescaleLog2 = 11.0f, kWeightLog2 = 4.0f;
+constexpr float kWeightLog2 = 4.0f;
 // A head's offset is its maximum less kWeightLog2, kNone before its first row: finite, so that differences with it are
 // numbers or infinities, and 2^(x - kNone) is 0 for the -infinity of a masked row.
 constexpr float kNone = -3.402823466e38f;
@@ -104,7 +105,7 @@ struct Params {
                    // NULL without a workspace, when there can be no rows at all
   float* part;     // [2 grid][kPartFloats]
   float* stat;     // [2 grid][kStatFloats]
-  int n_slots, n_req, max_pages, log_page, ratio, window, t0, T;
+  int n_slots, n_req, max_pages, log_page, ratio, window, t0, T, fetch_ahead;
   float scale, cap;
 };
 
@@ -145,12 +146,15 @@ __device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint32_t b, ui
       "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
       : "memory");
 }
+template <int kDst, int kSrc>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(kDst),
+               "n"(kSrc)
+               : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
 // Rows [lo, hi) of its request that token t sees, and the row e that it stands before.
 struct Span {
@@ -172,24 +176,29 @@ __device__ __forceinline__ Span span_of(const Params& p, int t) {
   s.hi = max(s.hi, s.lo);
   return s;
 }
-__device__ __forceinline__ int chunks_of(int rows) { return rows > kRows ? (rows - 1) / kRows + 1 : 1; }
+// Chunks of a token with `rows` rows in its list; `extra` 1 with another attention to join (its first chunk), else 0.
+__device__ __forceinline__ int chunks_of(int rows, int extra) {
+  return rows > 0 ? (rows - 1) / kRows + 1 + extra : 1;
+}
 
 // A block's part of the chunk sequence, walked item by item: chunks [c0, c1) of token t, of which the block
 // has the chunks up to `end`.  What is read from shared memory goes through a warp reduction, whose result is a
 // uniform register: the loops over it are then known to be the same in every lane, and the issuing warps'
 // operands stay in such registers.
 struct Walk {
-  int t, c0, c1, end, left;
+  int t, c0, c1, end, left, n, extra;
   const int* rows;
   __device__ __forceinline__ static int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
-  __device__ __forceinline__ Walk(const int* rows_s, const int* start)
-      : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), rows(rows_s) {
+  __device__ __forceinline__ Walk(const int* rows_s, const int* start, const Params& p)
+      : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), extra(p.other ? 1 : 0), rows(rows_s) {
     cut();
   }
   __device__ __forceinline__ void cut() {
-    end = left > 0 ? min(chunks_of(uniform(rows[t])), c0 + left) : c0;
+    n = left > 0 ? uniform(rows[t]) : 0;
+    end = left > 0 ? min(chunks_of(n, extra), c0 + left) : c0;
     c1 = min(end, c0 + kItemChunks);
   }
+  __device__ __forceinline__ bool is_other(int c) const { return c < extra; }
   __device__ __forceinline__ void next() {
     const int over = c1 == end;
     left -= c1 - c0;
@@ -199,8 +208,8 @@ struct Walk {
   }
   // steps of 16 rows in chunk c: one at least, whose rows are all masked where the list is empty
   __device__ __forceinline__ int steps(int c) const {
-    const int n = min(uniform(rows[t]) - c * kRows, kRows);
-    return n > 16 ? (n + 15) >> 4 : 1;
+    const int m = is_other(c) ? kHq : min(n - (c - extra) * kRows, kRows);
+    return m > 16 ? (m + 15) >> 4 : 1;
   }
 };
 
@@ -214,49 +223,56 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-template <bool kBf16>
-__device__ __forceinline__ float2 unpack16(uint32_t u) {
-  if constexpr (kBf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  else return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-// Column sums over the warp by transposing: v[c] of every lane -> lane c holds the sum over all lanes of column c.
-__device__ __forceinline__ float columns_sum(float (&v)[32]) {
+// v[i] of the eight lanes g = lane / 4 (of one lane % 4) reduced: lane g ends with elements 2 g and 2 g + 1.
+template <bool kMax>
+__device__ __forceinline__ float2 reduce_rows(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int step = 16; step >= 1; step >>= 1) {
+  for (int step = 16, n = 8; n >= 2; step >>= 1, n >>= 1) {
     const bool upper = (lane & step) != 0;
 #pragma unroll
-    for (int i = 0; i < step; ++i) {
-      const float send = upper ? v[i] : v[i + step];
-      const float keep = upper ? v[i + step] : v[i];
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n];
+      const float keep = upper ? v[i + n] : v[i];
       const float recv = __shfl_xor_sync(0xffffffffu, send, step);
-      v[i] = keep + recv;
+      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
     }
   }
-  return v[0];
+  return make_float2(v[0], v[1]);
 }
-// The largest x of the warp (NaN do not count), in every lane.
-__device__ __forceinline__ float warp_max(float x) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
-  return m;
+// a and b each plus one half of the pair u, in fp32.
+template <bool kBf16>
+__device__ __forceinline__ void add_pair(float& a, float& b, uint32_t u) {
+  if constexpr (kBf16)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(u));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %1, hi, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(u));
 }
-// What joins a head's own rows (offset m in log2 units, sums r of the rounded and l of the exact weights 2^(x - m)) to
-// its sink and to the other attention: factors of the unnormalised sums and of other's output, and lse.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A head's rows (offset m in log2 units, sums r of the rounded and l of the exact weights 2^(x - m)) and its sink:
+// the factor of the unnormalised sums, and lse.
 struct Joined {
-  float own, other, lse;
+  float own, lse;
 };
-__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink2, float other2) {
-  const float M = fmaxf(m, fmaxf(sink2, other2));
-  const float a = exp2f(m - M), s = exp2f(sink2 - M), o = exp2f(other2 - M);
-  const float d = fmaf(a, r, s + o), e = fmaf(a, l, s + o);
-  const float inv = d == 0.f ? 0.f : 1.f / d;
-  return Joined{a * inv, o * inv, e == 0.f ? -INFINITY : (M + log2f(e)) * kLn2};
+__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink2) {
+  const float M = fmaxf(m, sink2);
+  const float a = exp2f(m - M), s = exp2f(sink2 - M);
+  const float d = fmaf(a, r, s), e = fmaf(a, l, s);
+  return Joined{d == 0.f ? 0.f : a / d, e == 0.f ? -INFINITY : (M + log2f(e)) * kLn2};
 }
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     kv16_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
+  constexpr float kRescale = kBf16 ? 32.f : 11.f;  // log2 of what a logit may exceed its head's maximum by
   constexpr uint32_t kIdescS = idesc_f16(128, kHq, kBf16 ? 1 : 0, 0, 0);
   constexpr uint32_t kIdescO = idesc_f16(128, kHq, kBf16 ? 1 : 0, 1, 1);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -272,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* ahead_s = reinterpret_cast<int*>(smem + kOffAhead);
   float* stat_s = reinterpret_cast<float*>(smem + kOffStat);
   float* m_s = reinterpret_cast<float*>(smem + kOffM);
-  float* max_s = reinterpret_cast<float*>(smem + kOffMax);
+  float* max_s = reinterpret_cast<float*>(sp);  // [softmax warps][64] maxima of one chunk, while no weights are there
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
   float* slope_s = reinterpret_cast<float*>(smem + kOffSlope);
   float* join_s = reinterpret_cast<float*>(smem + kOffJoin);
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* qempty = qfull + 1;
   uint64_t* slfull = qempty + 1;         // [ring] slots of a chunk
   uint64_t* slempty = slfull + kRing;    // by the copying and the softmax warps
-  uint64_t* kvfull = slempty + kRing;    // [quarter], by every copying thread
+  uint64_t* kvfull = slempty + kRing;    // [quarter]
   uint64_t* kvempty = kvfull + kPairs;   // [quarter]
   uint64_t* sfull = kvempty + kPairs;
   uint64_t* sempty = sfull + 1;
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < kNumBars) {  // one barrier a thread
     uint64_t* bar = qfull + tid;
     mbar_init(bar, bar >= slempty && bar < kvfull ? kCopyWarps + kSoftWarps
-                   : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps
+                   : bar >= kvfull && bar < kvempty ? kCopyWarps
                    : bar == sempty || bar == pfull || (bar >= lready && bar < lfree) ? kSoftWarps
                    : bar >= oempty ? kOutWarps : 1);
     fence_mbarrier_init();
@@ -321,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Span s = span_of(p, t);
       const int n = s.hi - s.lo;
       rows_s[t] = n;
-      sum += chunks_of(n);
+      sum += chunks_of(n, p.other ? 1 : 0);
     }
     long long incl = sum;
 #pragma unroll
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long at = before;
 #pragma unroll 1
       for (int t = first; t < last; ++t) {
-        const int nch = chunks_of(rows_s[t]);
+        const int nch = chunks_of(rows_s[t], p.other ? 1 : 0);
         if (at <= g0 && g0 < at + nch) {
           start[0] = t;
           start[1] = (int)(g0 - at);
@@ -378,32 +394,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = 2 * i + hi;
       dst[i] = smem_u32(skv) + (piece >> 3) * kSlotBytes + (16 * warp + r) * 128 + (((piece & 7) ^ r) << 4);
     }
-    const char* pool = reinterpret_cast<const char*>(p.pool) + piece * 16;
+    const char* src[8];
+    uint32_t bytes = 0;  // bit i: row i is there (else it is filled with zeros)
+    auto issue = [&](auto quarter) {
+      constexpr int kQuarter = decltype(quarter)::value, kTo = kQuarter * 2 * kSlotBytes, kFrom = kQuarter * 256;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cp_async16<kTo, kFrom>(dst[i], src[i], (bytes >> i & 1u) << 4);
+        cp_async16<kTo + 1024, kFrom>(dst[i], src[i + 4], (bytes >> (i + 4) & 1u) << 4);
+      }
+    };
+    auto landed = [&](int pr) {
+      fence_proxy_async();  // copied rows -> visible to the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kvfull[pr]);
+    };
     uint32_t g = 0;
     bool ok = true;
-    for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
+    for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next()) {
 #pragma unroll 1
       for (int c = w.c0; c < w.c1 && ok; ++c, ++g) {
         const bool mine = warp < w.steps(c);
         ok = wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 100);
         const int* sl = slot_s + (g % kRing) * kRows + 16 * warp + hi;
-        int at[8];
+        const char* from = reinterpret_cast<const char*>(w.is_other(c) ? p.other : p.pool) + piece * 16;
+        bytes = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) at[i] = sl[2 * i];
+        for (int i = 0; i < 8; ++i) {
+          const int at = sl[2 * i];
+          src[i] = at < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at << 10);
+          bytes |= at < 0 ? 0u : 1u << i;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
-#pragma unroll 1
-        for (int pr = 0; pr < kPairs && ok; ++pr) {
-          ok = wait_bar_warp(&kvempty[pr], (g & 1) ^ 1, p.status, 101);
-          if (mine && ok) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // a row without a slot is filled with zeros
-              const char* src = at[i] < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at[i] << 10) + pr * 256;
-              cp_async16(dst[i & 3] + (i >> 2) * 1024 + pr * 2 * kSlotBytes, src, at[i] < 0 ? 0u : 16u);
-            }
-          }
-          cp_async_arrive(&kvfull[pr]);
-        }
+        // A quarter is handed on when the next one is on its way, the last at once.  (One arrival a warp: cp.async's
+        // own arrivals are one a thread, 256 on a barrier.)
+        const uint32_t par = (g & 1) ^ 1;
+        ok = ok && wait_bar_warp(&kvempty[0], par, p.status, 101);
+        if (mine && ok) issue(std::integral_constant<int, 0>());
+        cp_async_commit();
+        ok = ok && wait_bar_warp(&kvempty[1], par, p.status, 101);
+        if (mine && ok) issue(std::integral_constant<int, 1>());
+        cp_async_commit();
+        cp_async_wait<1>();
+        landed(0);
+        ok = ok && wait_bar_warp(&kvempty[2], par, p.status, 101);
+        if (mine && ok) issue(std::integral_constant<int, 2>());
+        cp_async_commit();
+        cp_async_wait<1>();
+        landed(1);
+        ok = ok && wait_bar_warp(&kvempty[3], par, p.status, 101);
+        if (mine && ok) issue(std::integral_constant<int, 3>());
+        cp_async_commit();
+        cp_async_wait<1>();
+        landed(2);
+        cp_async_wait<0>();
+        landed(3);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -414,16 +460,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, item = 0;
       bool ok = true;
       const uint32_t q_lo = (uint32_t)desc_sw128(smem_u32(sq), 16, 1024), k_lo = (uint32_t)desc_sw128(smem_u32(skv), 16, 1024);
-      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+      for (Walk w(rows_s, start, p); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
           if (!wait_bar_warp(sempty, (g & 1) ^ 1, p.status, 102)) { ok = false; break; }
           if (c == w.c0 && !wait_bar_warp(qfull, item & 1, p.status, 103)) { ok = false; break; }
 #pragma unroll 1
           for (int pr = 0; pr < kPairs; ++pr) {
             if (!wait_bar_warp(&kvfull[pr], g & 1, p.status, 104)) { ok = false; break; }
-            fence_proxy_async();  // copied rows -> visible to the tensor core
             tc_fence_after();
             const uint32_t a = k_lo + (pr * 2 * kSlotBytes >> 4), b = q_lo + (pr * 2 * kQBlockBytes >> 4);
+            if (w.is_other(c)) continue;  // whose weights are known
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               mma_elect(tmem, a + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), b + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
@@ -440,11 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
       bool ok = true;
       const uint32_t v_lo = (uint32_t)desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_lo = (uint32_t)desc_sw128(smem_u32(sp), 16, 1024);
-      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+      for (Walk w(rows_s, start, p); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
           const int steps = w.steps(c);
           if (!wait_bar_warp(pfull, g & 1, p.status, 105)) { ok = false; break; }
-          fence_proxy_async();
           tc_fence_after();
 #pragma unroll 1
           for (int db = 0; db < kPairs; ++db) {
@@ -477,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------------------------------- slots of the rows, a few chunks ahead
       uint32_t g = 0;
       bool ok = true;
-      for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
+      for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next()) {
         const Span s = span_of(p, w.t);
         const int n = s.hi - s.lo;
         const int32_t* table = p.tables + (int64_t)(n > 0 ? s.b : 0) * p.max_pages;
@@ -485,9 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           int slot[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = c * kRows + lane + 32 * i;
+            const int j = (c - w.extra) * kRows + lane + 32 * i;
             slot[i] = -1;
-            if (j < n) {
+            if (j < 0) {  // row h of the other attention's output, if that saw anything
+              const int at = w.t * kHq + lane + 32 * i;
+              if (i < kHq / 32 && p.other_lse[at] != -INFINITY) slot[i] = at;
+            } else if (j < n) {
               const int row = s.hi - 1 - j;
               const int page = __ldg(table + (row >> p.log_page));
               const int64_t at = ((int64_t)page << p.log_page) + (row & ((1 << p.log_page) - 1));
@@ -499,7 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             slot_s[(g % kRing) * kRows + lane + 32 * i] = slot[i];
-            if (slot[i] >= 0) prefetch_l2(p.pool + (int64_t)slot[i] * kDim, kDim * 2);
+            // Runs of rows that lie together (the list runs backwards) are brought to L2, one request a run: a
+            // request takes its warp about 70 clocks, whatever its size.
+            const int behind = __shfl_up_sync(0xffffffffu, slot[i], 1);
+            const uint32_t begins = __ballot_sync(0xffffffffu, lane == 0 || slot[i] != behind - 1 || behind < 0);
+            if (p.fetch_ahead && !w.is_other(c) && slot[i] >= 0 && (begins >> lane & 1)) {
+              const uint32_t later = begins & (0xfffffffeu << lane);
+              const int len = (later ? __ffs(later) - 1 : 32) - lane;
+              prefetch_l2(p.pool + (int64_t)(slot[i] - len + 1) * kDim, len * kDim * 2);
+            }
           }
           if (lane == 0) ahead_s[g % kRing] = s.e - s.hi;
           __syncwarp();
@@ -510,15 +566,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------------------ q
       uint32_t item = 0;
       bool ok = true;
-      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
+      for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next(), ++item) {
         ok = wait_bar_warp(qempty, (item & 1) ^ 1, p.status, 108);
         if (!ok) break;
         mbar_arrive_expect_tx_elect(qfull, kQBytes);
 #pragma unroll 1
         for (int i = 0; i < kSlots; ++i) tma_load_2d_elect(sq + i * kQBlockBytes, &tm_q, qfull, i * 64, w.t * kHq);
-        if (lane == 0) {  // what the item's output and the next item will ask for
-          if (p.other && w.c0 == 0) prefetch_l2(p.other + (int64_t)w.t * kHq * kDim, kHq * kDim * 2);
-          if (w.c1 == w.end && w.left > w.c1 - w.c0) prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
+        if (lane == 0) {  // what the next token will ask for
+          if (w.c1 == w.end && w.left > w.c1 - w.c0) {
+            prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
+            if (p.other) prefetch_l2(p.other + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
+          }
         }
         __syncwarp();
       }
@@ -526,172 +584,239 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kOutWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------------------- softmax
-    // thread: row 32 quad + lane of the chunk, heads 32 half .. + 31
-    const int quad = warp & 3, half = (warp - kSoftWarp) >> 2;
-    const int row = 32 * quad + lane, h0 = 32 * half;
-    const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-    const float scale2 = p.scale * kLog2e;
-    const float cap2 = p.cap * kLog2e, in_cap = p.cap > 0.f ? 2.f * kLog2e * (p.scale / p.cap) : 0.f;
+    // S^T holds row 32 quad + i of the chunk on TMEM lane 32 quad + i.  A warp takes 16 of its quadrant's lanes; the
+    // 16x256b load gives thread (g = lane / 4, e = lane % 4) rows g and g + 8 of them (A and B) and of each the heads
+    // 8 k + 2 e + {0, 1}, k = 0..7.  So a thread's 32 weights add up to 16 running sums of its own, and lanes meet
+    // at an item's end only: a shuffle takes its turn at shared memory like the products' operands.
+    const int quad = warp & 3, sub = (warp - kSoftWarp) >> 2, rows16 = 2 * quad + sub;
+    const int g8 = lane >> 2, e2 = 2 * (lane & 3);
+    const int rowA = 16 * rows16 + g8, rowB = rowA + 8;
+    const uint32_t t_lane = static_cast<uint32_t>(quad * 32 + sub * 16) << 16;
     const bool capped = p.cap > 0.f, sloped = p.slopes != nullptr;
-    uint8_t* line = sp + row * 128;
+    // logits in log2 units: a product times `unit`, less the offset in one fused step (an offset's rounding cancels
+    // between weights and lse); capped or sloped ones are formed first
+    const float scale2 = p.scale * kLog2e, unit = capped || sloped ? 1.f : scale2;
+    const float cap2 = p.cap * kLog2e, in_cap = capped ? 2.f * kLog2e * (p.scale / p.cap) : 0.f;
+    // rows A and B have the same swizzle: they lie 8 apart
+    const uint32_t line = smem_u32(sp) + rowA * 128 + 2 * e2, swz = (rowA & 7) << 4;
+    const int hr = 8 * g8 + e2;  // the first of the two heads whose reduced values this lane ends with
     uint32_t g = 0, item = 0;
     // a wait that gave up is acted on where the eight warps meet, so that they leave together
     bool ok = true, leave = false;
-    for (Walk w(rows_s, start); w.left > 0 && !leave; w.next(), ++item) {
+    for (Walk w(rows_s, start, p); w.left > 0 && !leave; w.next(), ++item) {
       float* m_row = m_s + (item & 1) * kHq;
-      float l = 0.f, r = 0.f;  // of head h0 + lane over the quadrant's rows: sums of the weights, and of the rounded ones
-      // the slot of this item's parity was last read by the output of item - 2
-      ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 109);
+      float l[16], r[16];  // sums of this thread's weights of a head, and of the rounded ones
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l[i] = r[i] = 0.f;
 #pragma unroll 1
       for (int c = w.c0; c < w.c1; ++c, ++g) {
         ok = ok && wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 110);
-        const bool live = slot_s[(g % kRing) * kRows + row] >= 0;
+        const int* sl = slot_s + (g % kRing) * kRows + rowA;
+        const bool liveA = sl[0] >= 0, liveB = sl[8] >= 0;
         const int ahead = ahead_s[g % kRing];
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
         ok = ok && wait_bar_warp(sfull, g & 1, p.status, 111);
         tc_fence_after();
+        if (w.is_other(c)) {
+          // The other attention's output of head h as a row that head h alone sees, with a logit of that attention's
+          // log-sum-exp: the token's first chunk, its weights 2^4 on the diagonal.
+          if (lane == 0) mbar_arrive(sempty);
+          ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 116);
+          const float* lse_row = p.other_lse + (int64_t)w.t * kHq;
+          const int th = tid - 32 * kSoftWarp;
+          if (th < kHq) m_row[th] = fmaxf(lse_row[th] * kLog2e - kWeightLog2, kNone);
+          leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
+          if (leave) break;
+          if (rows16 < kHq / 16) {
+            const float wa = liveA ? ex2_approx(lse_row[rowA] * kLog2e - m_row[rowA]) : 0.f;
+            const float wb = liveB ? ex2_approx(lse_row[rowB] * kLog2e - m_row[rowB]) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int h = 8 * k + e2;
+              const float a0 = h == rowA ? wa : 0.f, a1 = h + 1 == rowA ? wa : 0.f;
+              const float b0 = h == rowB ? wb : 0.f, b1 = h + 1 == rowB ? wb : 0.f;
+              const uint32_t at = line + ((k << 4) ^ swz);
+              asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0 + 1024], %2;" ::"r"(at), "r"(pack16<kBf16>(a0, a1)),
+                           "r"(pack16<kBf16>(b0, b1))
+                           : "memory");
+              l[2 * k] = r[2 * k] = a0 + b0;
+              l[2 * k + 1] = r[2 * k + 1] = a1 + b1;
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull);
+          continue;
+        }
         float x[32];
-        tmem_ld32(tmem + t_lane + h0, x);
+        tmem_ld_16x256b_x8(tmem + t_lane, x);
         tc_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty);
         if (capped) {  // tanh y = 1 - 2 / (e^2y + 1)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = fmaf(-2.f * cap2, __frcp_rn(ex2_approx(x[i] * in_cap) + 1.f), cap2);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] *= scale2;
+          for (int i = 0; i < 32; ++i) x[i] = fmaf(-2.f * cap2, rcp_approx(ex2_approx(x[i] * in_cap) + 1.f), cap2);
         }
-        if (sloped) {
-          const float dist = fabsf((float)(ahead + c * kRows + row));  // e - 1 - r, r = hi - 1 - list index
+        if (sloped) {  // e - 1 - r, r = hi - 1 - list index
+          const float distA = fabsf((float)(ahead + (c - w.extra) * kRows + rowA));
+          const float distB = fabsf((float)(ahead + (c - w.extra) * kRows + rowB));
+          const float mul = capped ? 1.f : scale2;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(slope_s + h0 + i);
-            x[i] = fmaf(-s.x, dist, x[i]);
-            x[i + 1] = fmaf(-s.y, dist, x[i + 1]);
-            x[i + 2] = fmaf(-s.z, dist, x[i + 2]);
-            x[i + 3] = fmaf(-s.w, dist, x[i + 3]);
+          for (int k = 0; k < 8; ++k) {
+            const float2 s = *reinterpret_cast<const float2*>(slope_s + 8 * k + e2);
+            x[4 * k] = fmaf(x[4 * k], mul, -s.x * distA);
+            x[4 * k + 1] = fmaf(x[4 * k + 1], mul, -s.y * distA);
+            x[4 * k + 2] = fmaf(x[4 * k + 2], mul, -s.x * distB);
+            x[4 * k + 3] = fmaf(x[4 * k + 3], mul, -s.y * distB);
           }
         }
-        if (!live) {
+        const bool part = !(liveA && liveB);
+        if (c == w.c0) {
+          // the item's first offsets: of its first row in bf16, of the largest of eight rows in fp16, whose range is less
+          if (g8 == 0 && (!kBf16 || rowA == 0)) {
+            ok = ok && wait_bar(pempty, (g & 1) ^ 1, p.status, 117);  // P is free (and S^T would not be there otherwise)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = -INFINITY;
-        }
-        bool moved = c == w.c0 || !ok;
-        if (c > w.c0) {
-          float over = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(m_row + h0 + i);
-            over = fmaxf(over, fmaxf(fmaxf(x[i] - m.x, x[i + 1] - m.y), fmaxf(x[i + 2] - m.z, x[i + 3] - m.w)));
+            for (int k = 0; k < 8; ++k) {
+              const float2 m = make_float2(fmaxf(x[4 * k] * unit - kWeightLog2, kNone), fmaxf(x[4 * k + 1] * unit - kWeightLog2, kNone));
+              *reinterpret_cast<float2*>((kBf16 ? m_row : max_s + rows16 * kHq) + 8 * k + e2) = liveA ? m : make_float2(kNone, kNone);
+            }
           }
-          moved = moved || over > kRescaleLog2 + kWeightLog2;
+          named_sync(kSoftBar, 32 * kSoftWarps);
+          if constexpr (!kBf16) {
+            const int th = tid - 32 * kSoftWarp;
+            if (th < kHq) {
+              float mx = max_s[th];
+#pragma unroll
+              for (int i = 1; i < kSoftWarps; ++i) mx = fmaxf(mx, max_s[i * kHq + th]);
+              m_row[th] = mx;
+            }
+            named_sync(kSoftBar, 32 * kSoftWarps);
+          }
+        }
+        bool moved = !ok;
+        {
+          float overA = -INFINITY, overB = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 m = *reinterpret_cast<const float2*>(m_row + 8 * k + e2);
+            overA = fmaxf(overA, fmaxf(fmaf(x[4 * k], unit, -m.x), fmaf(x[4 * k + 1], unit, -m.y)));
+            overB = fmaxf(overB, fmaxf(fmaf(x[4 * k + 2], unit, -m.x), fmaf(x[4 * k + 3], unit, -m.y)));
+          }
+          moved = moved || (liveA && overA > kRescale + kWeightLog2) || (liveB && overB > kRescale + kWeightLog2);
         }
         if (named_or(kSoftBar, 32 * kSoftWarps, moved)) {
+          ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 112);  // P is free for the maxima, O^T complete
           leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
           if (leave) break;
-          float mine = -INFINITY;
+          {
+            float v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float mx = warp_max(x[i]);
-            if (lane == i) mine = mx;
+            for (int k = 0; k < 8; ++k) {
+              v[2 * k] = fmaxf(liveA ? x[4 * k] * unit : -INFINITY, liveB ? x[4 * k + 2] * unit : -INFINITY);
+              v[2 * k + 1] = fmaxf(liveA ? x[4 * k + 1] * unit : -INFINITY, liveB ? x[4 * k + 3] * unit : -INFINITY);
+            }
+            *reinterpret_cast<float2*>(max_s + rows16 * kHq + hr) = reduce_rows<true>(v);
           }
-          max_s[quad * kHq + h0 + lane] = mine;
           named_sync(kSoftBar, 32 * kSoftWarps);
           const int th = tid - 32 * kSoftWarp;
           if (th < kHq) {
-            const float mx = fmaxf(fmaxf(max_s[th], max_s[kHq + th]), fmaxf(max_s[2 * kHq + th], max_s[3 * kHq + th]));
-            const float m = c == w.c0 ? kNone : m_row[th];
-            const bool up = mx - m > kRescaleLog2 + kWeightLog2;
+            float mx = max_s[th];
+#pragma unroll
+            for (int i = 1; i < kSoftWarps; ++i) mx = fmaxf(mx, max_s[i * kHq + th]);
+            const float m = m_row[th];
+            const bool up = mx - m > kRescale + kWeightLog2;
             alpha_s[th] = up ? ex2_approx(m - (mx - kWeightLog2)) : 1.f;
             m_row[th] = up ? mx - kWeightLog2 : m;
           }
           named_sync(kSoftBar, 32 * kSoftWarps);
           if (c > w.c0) {
-            l *= alpha_s[h0 + lane];
-            r *= alpha_s[h0 + lane];
-            // O^T must hold all of the previous chunk before its columns are rescaled
-            ok = wait_bar_warp(pempty, (g - 1) & 1, p.status, 112);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 a = *reinterpret_cast<const float2*>(alpha_s + 8 * k + e2);
+              l[2 * k] *= a.x;
+              l[2 * k + 1] *= a.y;
+              r[2 * k] *= a.x;
+              r[2 * k + 1] *= a.y;
+            }
             tc_fence_after();
+            const uint32_t t_half = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + 32 * sub;
 #pragma unroll 1
-            for (int db = 0; db < kPairs; ++db) {
-              float v[32];
-              const uint32_t ta = tmem + t_lane + kColO + oslot(item, db) * kHq + h0;
-              tmem_ld32(ta, v);
+            for (int q = 0; q < 2 * kPairs; ++q) {  // all lanes of the quadrant, half of the heads, 16 at a time
+              float v[16];
+              const uint32_t ta = t_half + oslot(item, q >> 1) * kHq + 16 * (q & 1);
+              tmem_ld16(ta, v);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= alpha_s[h0 + i];
-              tmem_st32(ta, v);
+              for (int i = 0; i < 16; ++i) v[i] *= alpha_s[32 * sub + 16 * (q & 1) + i];
+              tmem_st16(ta, v);
             }
             tc_wait_st();
           }
         }
-        // weights 2^(x - offset), rounded for the product
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(m_row + h0 + i);
-          x[i] = ex2_approx(x[i] - m.x);
-          x[i + 1] = ex2_approx(x[i + 1] - m.y);
-          x[i + 2] = ex2_approx(x[i + 2] - m.z);
-          x[i + 3] = ex2_approx(x[i + 3] - m.w);
-          pk[i / 2] = pack16<kBf16>(x[i], x[i + 1]);
-          pk[i / 2 + 1] = pack16<kBf16>(x[i + 2], x[i + 3]);
-        }
         ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 113);
+        // weights 2^(x - offset), rounded for the product
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(line + (((4 * half + k) ^ (row & 7)) << 4)) =
-              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        for (int k = 0; k < 8; ++k) {
+          const float2 m = *reinterpret_cast<const float2*>(m_row + 8 * k + e2);
+          float a0 = ex2_approx(fmaf(x[4 * k], unit, -m.x)), a1 = ex2_approx(fmaf(x[4 * k + 1], unit, -m.y));
+          float b0 = ex2_approx(fmaf(x[4 * k + 2], unit, -m.x)), b1 = ex2_approx(fmaf(x[4 * k + 3], unit, -m.y));
+          if (part) {
+            if (!liveA) a0 = a1 = 0.f;
+            if (!liveB) b0 = b1 = 0.f;
+          }
+          const uint32_t wa = pack16<kBf16>(a0, a1), wb = pack16<kBf16>(b0, b1);
+          const uint32_t at = line + ((k << 4) ^ swz);
+          asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0 + 1024], %2;" ::"r"(at), "r"(wa), "r"(wb) : "memory");
+          l[2 * k] += a0 + b0;
+          l[2 * k + 1] += a1 + b1;
+          add_pair<kBf16>(r[2 * k], r[2 * k + 1], wa);
+          add_pair<kBf16>(r[2 * k], r[2 * k + 1], wb);
+        }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull);
-        // the sums over the rows, while the products run
-        l += columns_sum(x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 u = unpack16<kBf16>(pk[i]);
-          x[2 * i] = u.x;
-          x[2 * i + 1] = u.y;
-        }
-        r += columns_sum(x);
       }
       if (leave) break;
-      float* st = stat_s + ((item & 1) * 4 + quad) * 2 * kHq + h0 + lane;
-      st[0] = r;
-      st[kHq] = l;
+      // the statistics of the item before are read (and so, an item later, are these offsets)
+      ok = ok && (item == 0 || wait_bar_warp(&lfree[(item & 1) ^ 1], ((item - 1) >> 1) & 1, p.status, 109));
+      float* st = stat_s + rows16 * 2 * kHq + hr;
+      *reinterpret_cast<float2*>(st) = reduce_rows<false>(r);
+      *reinterpret_cast<float2*>(st + kHq) = reduce_rows<false>(l);
       __syncwarp();
       if (lane == 0) mbar_arrive(&lready[item & 1]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // --------------------------------------------------------------------------- output
-    const int quad = warp & 3, to = tid - 32 * kOutWarp;
-    const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-    const bool odd = lane & 1;
+    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 5, to = tid - 32 * kOutWarp;
+    const uint32_t t_lane = (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
     float *so_far = join_s, *f_first = join_s + 3 * kHq, *f_item = join_s + 4 * kHq;
     uint32_t item = 0;
     uint32_t f_ph = 0;  // bit s: phase of O^T slot s's full barrier
     bool ok = true;
     int from = 0;       // the block's first chunk of the token
-    for (Walk w(rows_s, start); w.left > 0; w.next(), ++item) {
+    for (Walk w(rows_s, start, p); w.left > 0; w.next(), ++item) {
       const int par = item & 1;
       ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
       // chunks before the block, or behind it: the sums go to the block's first or second part
       if (w.c0 == 0 || item == 0) from = w.c0;
       const bool begins = w.c0 == from, ends = w.c1 == w.end;
-      const bool whole = ends && from == 0 && w.c1 == chunks_of(rows_s[w.t]);
+      const bool whole = ends && from == 0 && w.c1 == chunks_of(w.n, w.extra);
       const bool joins = !(begins && ends);  // one of several items: joined to those so far
       const int64_t part = 2 * (int64_t)blockIdx.x + (from == 0);
       // the factors of the item before are read by all
       if (!named_and(kOutBar, 32 * kOutWarps, ok)) break;
       if (to < kHq) {
-        const float* st = stat_s + par * 8 * kHq + to;
-        float r = (st[0] + st[2 * kHq]) + (st[4 * kHq] + st[6 * kHq]);
-        float l = (st[kHq] + st[3 * kHq]) + (st[5 * kHq] + st[7 * kHq]);
+        const float* st = stat_s + to;
+        float r = 0.f, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSoftWarps; ++i) {
+          r += st[2 * i * kHq];
+          l += st[(2 * i + 1) * kHq];
+        }
         float m = m_s[par * kHq + to];
         float f0 = 0.f, fi = 1.f;
         if (joins) {
@@ -707,12 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (whole) {
           const float sink2 = p.sinks ? p.sinks[to] * kLog2e : -INFINITY;
-          const float other2 = p.other ? p.other_lse[(int64_t)w.t * kHq + to] * kLog2e : -INFINITY;
-          const Joined j = join_head(m, r, l, sink2, other2);
+          const Joined j = join_head(m, r, l, sink2);
           if (p.lse) p.lse[(int64_t)w.t * kHq + to] = j.lse;
-          f0 = joins ? f0 * j.own : j.other;
+          f0 *= j.own;
           fi *= j.own;
-          if (joins) so_far[to] = j.other;  // a token's last item: nothing is joined to it any more
         } else if (ends) {
           float* ps = p.stat + part * kStatFloats;
           ps[to] = r;
@@ -725,68 +848,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(kOutBar, 32 * kOutWarps);
       if (lane == 0) mbar_arrive(&lfree[par]);
 #pragma unroll 1
-      for (int step = 0; step < 2 * kPairs; ++step) {  // quarters of the dims by halves of the heads
-        const int db = step >> 1, hb = (step & 1) * 32;
+      for (int db = 0; db < kPairs; ++db) {
         const int os = oslot(item, db);
-        const int d = db * 128 + quad * 32 + lane;
-        // neighbouring lanes exchange, so that each reads and writes two dims of one head: of an even lane the
-        // even head of a pair, of an odd one the odd head
-        const int64_t at = (((int64_t)w.t * kHq + hb + (odd ? 1 : 0)) * kDim + d) >> 1;
-        uint32_t o2[16];
-        const float* f_other = joins ? so_far : f_first;
-        if (whole && p.other) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(p.other) + at;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o2[i] = f_other[hb + 2 * i + odd] == 0.f ? 0u : __ldg(src + i * kDim);
-        }
-        if (hb == 0) {
-          ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 115);
-          if (!ok) break;
-          f_ph ^= 1u << os;
-          tc_fence_after();
-        }
+        const int64_t at = ((int64_t)w.t * kHq + hb) * kDim + db * 128 + quad * 32 + lane;  // of the first head
+        ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 115);
+        if (!ok) break;
+        f_ph ^= 1u << os;
+        tc_fence_after();
         float v[32];
-        tmem_ld32(tmem + t_lane + kColO + os * kHq + hb, v);
+        tmem_ld32(t_lane + tmem + os * kHq, v);
         tc_wait_ld();
-        if (hb) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&oempty[os]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&oempty[os]);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(f_item + hb + i);
+          v[i] *= f.x;
+          v[i + 1] *= f.y;
+          v[i + 2] *= f.z;
+          v[i + 3] *= f.w;
         }
-        if (joins || !whole) {
+        if (!whole || joins) {
           // Sums so far lie where the part's go: the second part's own token is the block's last, behind all that
           // lie whole in the block.  A thread reads back only what it wrote.
-          float* sums = p.part + part * kPartFloats + hb * kDim + d;
+          float* sums = p.part + part * kPartFloats + hb * kDim + db * 128 + quad * 32 + lane;
+          if (!begins) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] *= f_item[hb + i];
-            if (!begins) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
           }
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) sums[i * kDim] = v[i];
             continue;
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= f_item[hb + i];
         }
-        if (p.other) {
+        uint16_t* to_out = p.out + at;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t theirs = __shfl_xor_sync(0xffffffffu, o2[i], 1);
-            // heads 2 i and 2 i + 1 at this lane's dim
-            const float2 a = unpack16<kBf16>(__byte_perm(o2[i], theirs, odd ? 0x3276u : 0x5410u));
-            v[2 * i] = fmaf(f_other[hb + 2 * i], a.x, v[2 * i]);
-            v[2 * i + 1] = fmaf(f_other[hb + 2 * i + 1], a.y, v[2 * i + 1]);
-          }
-        }
-        uint32_t* orow = reinterpret_cast<uint32_t*>(p.out) + at;
-        const uint32_t sel = odd ? 0x3276u : 0x5410u;  // even: both first heads; odd: both second ones
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t mine = pack16<kBf16>(v[2 * i], v[2 * i + 1]);
-          orow[i * kDim] = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), sel);
+        for (int i = 0; i < 32; i += 2) {
+          const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
+          to_out[i * kDim] = (uint16_t)u;
+          to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
         }
       }
     }
@@ -803,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a token that several blocks worked on: part k holds O_k = sum_j 2^(x_j - m_k) kv_j and
 // the sums r_k of its rounded weights and l_k of the exact ones, so with M = max_k m_k the token's are
 //   O = sum_k 2^(m_k - M) O_k, r and l alike,
-// and the sink and the other attention join them as they do in the kernel above.  A thread holds 4 dims; kGroups
+// and the sink joins them as it does in the kernel above.  A thread holds 4 dims; kGroups
 // groups of threads take the parts in turn and are added up at the end, in an order that depends on the parts'
 // number alone: the same bits on every run.
 //   Many tokens (two or three parts each): a block per boundary between two blocks and four heads, one group
@@ -814,12 +916,10 @@ constexpr int kMaxParts = 256;
 template <bool kBf16, bool kByToken, int kGroups, int kHeads, int kDimBlocks>
 __global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
     kv16_combine_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
-                        const float* __restrict__ stat, const float* __restrict__ sinks,
-                        const uint16_t* __restrict__ other, const float* __restrict__ other_lse, uint16_t* out,
-                        float* lse) {
+                        const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
   constexpr int kLane4 = kDim / 4 / kDimBlocks, kTeam = kGroups * kLane4;
   static_assert(kTeam >= 32 && (kHeads == 1 || kGroups == 1), "a team's first warp takes its statistics");
-  __shared__ float weight[kHeads][kMaxParts], own_s[kHeads], other_s[kHeads];
+  __shared__ float weight[kHeads][kMaxParts], own_s[kHeads];
   __shared__ float4 acc_s[kGroups > 1 ? kGroups - 1 : 1][kLane4];
   __shared__ int found;
   pdl_wait();
@@ -863,10 +963,8 @@ __global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
     if (tid == 0) {
-      const Joined j = join_head(mx, r, l, sinks ? sinks[h] * kLog2e : -INFINITY,
-                                 other ? other_lse[row] * kLog2e : -INFINITY);
+      const Joined j = join_head(mx, r, l, sinks ? sinks[h] * kLog2e : -INFINITY);
       own_s[team] = j.own;
-      other_s[team] = j.other;
       if (lse && blockIdx.z == 0) lse[row] = j.lse;
     }
   }
@@ -896,20 +994,9 @@ __global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
       acc.w += o.w;
     }
   }
-  const float own = own_s[team], fo = other_s[team];
-  acc.x *= own;
-  acc.y *= own;
-  acc.z *= own;
-  acc.w *= own;
-  if (other && fo != 0.f) {
-    const uint2 u = *reinterpret_cast<const uint2*>(other + row * kDim + 4 * x);
-    const float2 a = unpack16<kBf16>(u.x), b = unpack16<kBf16>(u.y);
-    acc.x = fmaf(fo, a.x, acc.x);
-    acc.y = fmaf(fo, a.y, acc.y);
-    acc.z = fmaf(fo, b.x, acc.z);
-    acc.w = fmaf(fo, b.y, acc.w);
-  }
-  *reinterpret_cast<uint2*>(out + row * kDim + 4 * x) = make_uint2(pack16<kBf16>(acc.x, acc.y), pack16<kBf16>(acc.z, acc.w));
+  const float own = own_s[team];
+  const uint32_t lo = pack16<kBf16>(acc.x * own, acc.y * own), hi = pack16<kBf16>(acc.z * own, acc.w * own);
+  *reinterpret_cast<uint2*>(out + row * kDim + 4 * x) = make_uint2(lo, hi);
 }
 
 // Blocks for T tokens of up to max_rows rows: one an SM, at most one a chunk.
@@ -951,6 +1038,7 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.scale = a.scale;
   p.cap = a.cap;
+  p.fetch_ahead = a.log_page >= 3;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.parts_of = reinterpret_cast<int4*>(ws);
   for (int t0 = 0; t0 < a.T; t0 += kTokens) {  // launches on one stream: they may share the workspace
@@ -982,7 +1070,7 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
     if (grid > 1 && a.max_rows > kRows) {  // a token of one chunk is never split
       auto join = [&](auto kernel, dim3 blocks, int threads) {
         return launch_pdl(kernel, blocks, dim3(threads), 0, stream, (const int4*)p.parts_of, grid, (const float*)p.part,
-                          (const float*)p.stat, p.sinks, p.other, p.other_lse, p.out, p.lse);
+                          (const float*)p.stat, p.sinks, p.out, p.lse);
       };
       cudaError_t e;
       if (4 * p.T < grid && p.T < 8)  // few tokens: four blocks a head fill more of the GPU
@@ -1037,6 +1125,7 @@ int ds4x_kv16_attn(const void* q_attn, ds4x_dtype dtype, const void* pool, int32
     if (!aligned4(w)) return DS4X_ERR_INVALID;
   int max_rows = max_pages * page_rows;
   if (!prefix && window > 0 && window < max_rows) max_rows = window;
+  if (other_out) max_rows = max_rows > INT32_MAX - kRows ? INT32_MAX : max_rows + kRows;  // a chunk of its own
   const size_t need = ds4x_kv16_attn_workspace_bytes(T, max_rows);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DS4X_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return DS4X_ERR_INVALID;
