@@ -843,8 +843,7 @@ def kv16_append(rows, slots, pool, positions=None, inv_freq=None, stream=None):
 
 
 def kv16_attn_workspace_bytes(T: int, max_rows: int) -> int:
-    """Workspace of kv16_attn: max_rows = max_pages * page_rows, or min(window, that) with a window and no prefix; 128
-    more with `other`."""
+    """Workspace of kv16_attn: max_rows = max_pages * page_rows, or min(window, that) with a window and no prefix."""
     return int(load().ds4x_kv16_attn_workspace_bytes(T, max_rows))
 
 
@@ -903,8 +902,6 @@ def kv16_attn(q_attn, pool, tables, rows, page_rows: int, req=None, positions=No
     max_rows = max_pages * page_rows
     if prefix is None and 0 < window < max_rows:
         max_rows = window
-    if other is not None:
-        max_rows = min(max_rows + 128, 2**31 - 1)
     if workspace is None and 0 <= max_rows < 2**31:
         need = lib.ds4x_kv16_attn_workspace_bytes(T, max_rows)
         if need > 0:

@@ -7,36 +7,32 @@
 // list runs backwards from hi - 1, so that with a bias that grows with the distance the largest logits come first
 // and the running maximum seldom moves.
 //
-// One block an SM.  The tokens' lists are cut into chunks of 128 rows; all chunks of all tokens form one sequence,
+// One block an SM.  The tokens' lists are cut into chunks of 64 rows; all chunks of all tokens form one sequence,
 // and each block takes an equal, contiguous part of it.  A token whose chunks lie in several blocks leaves its
 // unnormalised sums there in fp32 and kv16_combine_kernel joins them, so one long cache, a ragged batch and a
 // prefill chunk are all spread evenly.  A token's chunks in a block are an item (several, if they are many:
 // kItemChunks).  Per chunk:
-//   S^T [128 rows x 64 heads] = K . Q^T       tcgen05, M = 128 (rows on TMEM lanes), both K-major
-//   O^T [512 x 64 heads]     += V^T . P       tcgen05, M = 128 (dims), both MN-major
-// with K = V = the chunk in 128B-swizzled shared memory (8 slots of 64 dims, 128 KB).  With the rows on the lanes of
-// S^T a product of 16 dims serves 128 rows at the price of 64 (the matrix unit takes about 64 clocks for any
-// product of up to 64 columns), a row's mask and distance belong to a thread, and P goes back to shared memory in
-// whole 16-byte pieces: 32 heads of a row.
+//   S   [64 heads x 64 rows] = Q . K^T       tcgen05, M = 64 (heads on TMEM lanes), K-major
+//   O^T [512 x 64 heads]    += V^T . P^T     tcgen05, M = 128 (dims), A MN-major, B K-major
+// with K = V = the chunk in 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
 //
-// Warps: 0-7 copy rows (16-byte cp.async, 16 rows of a chunk each: one step of the O^T products), 8-15 softmax
-// (16 rows each), 16-23 write the output (O^T lanes by quadrant, 32 heads each), 24 issues the S^T products,
-// 25 the O^T products, 26 looks up the rows' slots a few chunks ahead and brings the rows to L2, 27 loads q.
-// There is room for one chunk: it is copied and released in quarters of the dims, so that the next chunk comes in
-// while the O^T products go through this one.  O^T rotates over seven 64-column TMEM slots (a token uses four).
-// A chunk that is not full costs its O^T products and copies by 16 rows.
+// Warps: 0-7 copy rows (16-byte cp.async; half of the dims of 16 rows each, one step of the O^T products), 8-11
+// softmax (heads 16*(warp-8) .. +15, 4 threads a head), 12-19 write the output (O^T lanes by quadrant, 32 heads
+// each), 20 issues the S products, 21 the O^T products, 22 looks up the rows' slots a few chunks ahead and brings
+// the rows to L2, 23 loads q.  Buffers are released in halves of the dims, O^T rotates over six 64-column TMEM
+// slots (a token uses four), so neighbouring tokens overlap.  A chunk that is not full costs its O^T products and
+// copies by 16 rows.  The other attention's output is where a token's sums begin: the output warps put it, times
+// 2^(o - m), into the O^T slots that they have emptied.
 //
 // The running maximum of a head moves only when a logit exceeds it by more than 2^11 in fp16, 2^32 in bf16 (O^T and
 // the sums are rescaled then, which stalls the products); weights are 2^4 times 2^(x - m), which keeps them below
-// fp16's largest value and small ones away from its least.  Statistics and sums are fp32.  Weights are rounded to the rows'
-// type, which the matrix unit asks for (8 bits in bf16); out is normalised by the sum of the rounded weights, so that
-// what a weight's rounding does to a row it does to the normaliser too; lse takes the exact ones.
+// fp16's largest value and small ones away from its least.  Statistics and sums are fp32.  Weights are rounded to the
+// rows' type, which the matrix unit asks for (8 bits in bf16); out is normalised by the sum of the rounded weights, so
+// that what a weight's rounding does to a row it does to the normaliser too; lse takes the exact ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
-
-#include <type_traits>
 
 #include "ds4x_internal.h"
 #include "ds4x_ptx.cuh"
@@ -46,44 +42,45 @@ namespace {
 
 constexpr int kHq = 64;
 constexpr int kDim = 512;
-constexpr int kRows = 128;                       // rows per chunk
+constexpr int kRows = 64;                        // rows per chunk
 constexpr int kSlots = kDim / 64;                // 8 slots of 64 dims
-constexpr int kPairs = kSlots / 2;               // quarters of 128 dims: what is copied and released together
-constexpr int kSlotBytes = kRows * 128;          // 16 KB
-constexpr int kKvBytes = kSlots * kSlotBytes;    // 128 KB
+constexpr int kPairs = kSlots / 2;               // quarters of 128 dims
+constexpr int kHalves = 2;                       // of the dims: what is copied and released together
+constexpr int kSlotBytes = kRows * 128;          // 8 KB
+constexpr int kBufBytes = kSlots * kSlotBytes;   // 64 KB a chunk
 constexpr int kQBlockBytes = kHq * 128;          // 8 KB (64 heads x 64 dims)
 constexpr int kQBytes = kSlots * kQBlockBytes;   // 64 KB
-constexpr int kPBytes = kRows * 128;             // 16 KB: P[row][head]
+constexpr int kPBytes = kHq * 128;               // 8 KB: P[h][j]
 constexpr int kTokens = 2048;                    // tokens a launch plans for
-constexpr int kSoftWarp = 8, kOutWarp = 16, kSWarp = 24, kOWarp = 25, kSlotWarp = 26, kQWarp = 27;
-constexpr int kCopyWarps = 8, kSoftWarps = 8, kOutWarps = 8;
-constexpr int kWarps = 28, kThreads = 32 * kWarps;
-// registers a thread: 72 at launch; the sum over the seven warpgroups stays what it was
-constexpr int kLaunchRegs = 72, kCopyRegs = 48, kMiscRegs = 40, kSoftRegs = 104, kOutRegs = 80;
-static_assert(kThreads * kLaunchRegs <= 65536 && 2 * (kCopyRegs + kSoftRegs + kOutRegs) + kMiscRegs <= 7 * kLaunchRegs, "registers");
-constexpr int kRing = 4;                         // chunks whose slots are looked up ahead
+constexpr int kOutWarp = 12, kSWarp = 20, kOWarp = 21, kSlotWarp = 22, kQWarp = 23;
+constexpr int kCopyWarps = 8, kSoftWarps = 4, kOutWarps = 8;
+constexpr int kWarps = 24, kThreads = 32 * kWarps;
+// registers a thread: 80 at launch; the sum over the six warpgroups stays what it was
+constexpr int kLaunchRegs = 80, kCopyRegs = 64, kMiscRegs = 40, kSoftRegs = 112, kOutRegs = 96;
+static_assert(kThreads * kLaunchRegs <= 65536 && 2 * kCopyRegs + kSoftRegs + 2 * kOutRegs + kMiscRegs <= 6 * kLaunchRegs, "registers");
+constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
-constexpr int kItemChunks = 128;
-constexpr int kOSlots = 7;                       // O^T slots of 64 TMEM columns
+constexpr int kItemChunks = 256;
+constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
-constexpr int kOffP = kOffKV + kKvBytes;
-constexpr int kOffRows = kOffP + kPBytes;        // int[kTokens]: rows of each token's list
+constexpr int kOffP = kOffKV + 2 * kBufBytes;
+constexpr int kOffRows = kOffP + 2 * kPBytes;    // int[kTokens]: rows of each token's list
 constexpr int kOffSlots = kOffRows + kTokens * 4;      // int[kRing][kRows]: slot of each row of the chunk, -1 for none
-constexpr int kOffAhead = kOffSlots + kRing * kRows * 4;  // int[kRing]: e - hi of the chunk's token
-constexpr int kOffStat = kOffAhead + kRing * 4;        // float[softmax warps][sum of rounded weights, sum][64] of an item
-constexpr int kOffM = kOffStat + kSoftWarps * 2 * kHq * 4;  // float[2 items][64]: offsets
-constexpr int kOffAlpha = kOffM + 2 * kHq * 4;   // float[64]: rescale factors of one chunk
-constexpr int kOffSlope = kOffAlpha + kHq * 4;   // float[64]: slopes in log2 units
-constexpr int kOffJoin = kOffSlope + kHq * 4;    // float[5][64]: a token's offset, sum of rounded weights and sum so far; factors
-                                                 // of the sums so far and of the item's
-constexpr int kOffScan = kOffJoin + 5 * kHq * 4; // int64[kWarps] warp sums, then int[4]: the block's part
+constexpr int kOffMask = kOffSlots + kRing * kRows * 4;  // uint32[kMaskRing][2]: rows of the chunk that count
+constexpr int kOffAhead = kOffMask + kMaskRing * 8;    // int[kMaskRing]: e - hi of the chunk's token
+constexpr int kOffStat = kOffAhead + kMaskRing * 4;    // float[2 items][sum of rounded weights, sum, offset][64]
+constexpr int kOffAlpha = kOffStat + 2 * 3 * kHq * 4;  // float[64]: rescale factors of one chunk
+constexpr int kOffJoin = kOffAlpha + kHq * 4;    // float[6][64]: a token's offset, sum of rounded weights and sum so far; factors
+                                                 // of the sums so far, of the item's, and of the next token's other output
+constexpr int kOffScan = kOffJoin + 6 * kHq * 4; // int64[kWarps] warp sums, then int[4]: the block's part, and the
+                                                 // last chunk (+ 1) in which a maximum moved
 constexpr int kOffBars = kOffScan + kWarps * 8 + 16;
-constexpr int kNumBars = 2 + 2 * kRing + 2 * kPairs + 4 + 2 * kOSlots + 4;
+constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 5 * 2 + 2 * kOSlots + 2 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
-constexpr uint32_t kTmemCols = 512, kColO = 64;  // S^T in columns [0, 64), O^T from 64
+constexpr uint32_t kTmemCols = 512, kColO = 128;  // S in columns [0, 128), O^T from 128
 constexpr float kWeightLog2 = 4.0f;
 // A head's offset is its maximum less kWeightLog2, kNone before its first row: finite, so that differences with it are
 // numbers or infinities, and 2^(x - kNone) is 0 for the -infinity of a masked row.
@@ -133,28 +130,38 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, in
   return __all_sync(0xffffffffu, wait_bar(bar, parity, status, site));
 }
 
-// D (+)= A B by an elected lane of a converged warp; descriptors by their low words (the addresses): the high
+// D (+)= A B^T by an elected lane of a converged warp; descriptors by their low words (the addresses): the high
 // words are the same for all operands here.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool kAdd>
 __device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
-      : "memory");
+  if constexpr (kAdd)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
+        : "memory");
 }
-template <int kDst, int kSrc>
+template <int kDst>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(kDst),
-               "n"(kSrc)
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(kDst)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // Rows [lo, hi) of its request that token t sees, and the row e that it stands before.
 struct Span {
@@ -162,43 +169,35 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Params& p, int t) {
   Span s{p.req ? __ldg(p.req + t) : p.t0 + t, 0, 0, 0};
-  if (s.b < 0 || s.b >= p.n_req) return s;
+  const int pos = p.positions ? __ldg(p.positions + t) : 0;
+  const int first = p.first ? __ldg(p.first + t) : 0;
+  if (s.b < 0 || s.b >= p.n_req || pos < 0) return s;
   const int held = min(max(__ldg(p.rows + s.b), 0), p.max_pages << p.log_page);
-  s.e = held;
-  if (p.positions) {
-    const int pos = __ldg(p.positions + t);
-    if (pos < 0) return s;
-    s.e = (int)min(((uint32_t)pos + 1u) / (uint32_t)p.ratio, 0x7fffffffu);
-  }
+  s.e = p.positions ? (int)min(((uint32_t)pos + 1u) / (uint32_t)p.ratio, 0x7fffffffu) : held;
   s.hi = min(held, p.prefix ? max(s.e, __ldg(p.prefix + s.b)) : s.e);
-  s.lo = p.window > 0 ? max(s.e - p.window, 0) : 0;
-  if (p.first) s.lo = max(s.lo, __ldg(p.first + t));
+  s.lo = max(p.window > 0 ? max(s.e - p.window, 0) : 0, first);
   s.hi = max(s.hi, s.lo);
   return s;
 }
-// Chunks of a token with `rows` rows in its list; `extra` 1 with another attention to join (its first chunk), else 0.
-__device__ __forceinline__ int chunks_of(int rows, int extra) {
-  return rows > 0 ? (rows - 1) / kRows + 1 + extra : 1;
-}
+__device__ __forceinline__ int chunks_of(int rows) { return rows > kRows ? (rows - 1) / kRows + 1 : 1; }
 
 // A block's part of the chunk sequence, walked item by item: chunks [c0, c1) of token t, of which the block
 // has the chunks up to `end`.  What is read from shared memory goes through a warp reduction, whose result is a
 // uniform register: the loops over it are then known to be the same in every lane, and the issuing warps'
 // operands stay in such registers.
 struct Walk {
-  int t, c0, c1, end, left, n, extra;
+  int t, c0, c1, end, left, n;
   const int* rows;
   __device__ __forceinline__ static int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
-  __device__ __forceinline__ Walk(const int* rows_s, const int* start, const Params& p)
-      : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), extra(p.other ? 1 : 0), rows(rows_s) {
+  __device__ __forceinline__ Walk(const int* rows_s, const int* start)
+      : t(uniform(start[0])), c0(uniform(start[1])), left(uniform(start[2])), rows(rows_s) {
     cut();
   }
   __device__ __forceinline__ void cut() {
     n = left > 0 ? uniform(rows[t]) : 0;
-    end = left > 0 ? min(chunks_of(n, extra), c0 + left) : c0;
+    end = left > 0 ? min(chunks_of(n), c0 + left) : c0;
     c1 = min(end, c0 + kItemChunks);
   }
-  __device__ __forceinline__ bool is_other(int c) const { return c < extra; }
   __device__ __forceinline__ void next() {
     const int over = c1 == end;
     left -= c1 - c0;
@@ -208,7 +207,7 @@ struct Walk {
   }
   // steps of 16 rows in chunk c: one at least, whose rows are all masked where the list is empty
   __device__ __forceinline__ int steps(int c) const {
-    const int m = is_other(c) ? kHq : min(n - (c - extra) * kRows, kRows);
+    const int m = min(n - c * kRows, kRows);
     return m > 16 ? (m + 15) >> 4 : 1;
   }
 };
@@ -223,34 +222,18 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// v[i] of the eight lanes g = lane / 4 (of one lane % 4) reduced: lane g ends with elements 2 g and 2 g + 1.
-template <bool kMax>
-__device__ __forceinline__ float2 reduce_rows(float (&v)[16]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int step = 16, n = 8; n >= 2; step >>= 1, n >>= 1) {
-    const bool upper = (lane & step) != 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = upper ? v[i] : v[i + n];
-      const float keep = upper ? v[i + n] : v[i];
-      const float recv = __shfl_xor_sync(0xffffffffu, send, step);
-      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-    }
-  }
-  return make_float2(v[0], v[1]);
-}
-// a and b each plus one half of the pair u, in fp32.
 template <bool kBf16>
-__device__ __forceinline__ void add_pair(float& a, float& b, uint32_t u) {
+__device__ __forceinline__ float from16(uint16_t u) {
+  if constexpr (kBf16) return __uint_as_float((uint32_t)u << 16);
+  else return __half2float(*reinterpret_cast<const __half*>(&u));
+}
+// a plus both halves of the pair u, in fp32.
+template <bool kBf16>
+__device__ __forceinline__ void add_pair(float& a, uint32_t u) {
   if constexpr (kBf16)
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %1, hi, %1;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "r"(u));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}" : "+f"(a) : "r"(u));
   else
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %1, hi, %1;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "r"(u));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %0, hi, %0;\n\t}" : "+f"(a) : "r"(u));
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -268,13 +251,18 @@ __device__ __forceinline__ Joined join_head(float m, float r, float l, float sin
   const float d = fmaf(a, r, s), e = fmaf(a, l, s);
   return Joined{d == 0.f ? 0.f : a / d, e == 0.f ? -INFINITY : (M + log2f(e)) * kLn2};
 }
+// Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output.
+__device__ __forceinline__ float first_offset(float lse) { return fmaxf(lse * kLog2e - kWeightLog2, kNone); }
+__device__ __forceinline__ float first_weight(float lse) {
+  return lse == -INFINITY ? 0.f : ex2_approx(lse * kLog2e - first_offset(lse));
+}
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     kv16_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   constexpr float kRescale = kBf16 ? 32.f : 11.f;  // log2 of what a logit may exceed its head's maximum by
-  constexpr uint32_t kIdescS = idesc_f16(128, kHq, kBf16 ? 1 : 0, 0, 0);
-  constexpr uint32_t kIdescO = idesc_f16(128, kHq, kBf16 ? 1 : 0, 1, 1);
+  constexpr uint32_t kIdescS = idesc_f16(64, kHq, kBf16 ? 1 : 0, 0, 0);
+  constexpr uint32_t kIdescO = idesc_f16(128, kHq, kBf16 ? 1 : 0, 1, 0);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled layouts need a 1024-byte aligned base
     if (threadIdx.x == 0) report_timeout(p.status, 0x7b);
@@ -285,40 +273,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sp = smem + kOffP;
   int* rows_s = reinterpret_cast<int*>(smem + kOffRows);
   int* slot_s = reinterpret_cast<int*>(smem + kOffSlots);
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + kOffMask);
   int* ahead_s = reinterpret_cast<int*>(smem + kOffAhead);
   float* stat_s = reinterpret_cast<float*>(smem + kOffStat);
-  float* m_s = reinterpret_cast<float*>(smem + kOffM);
-  float* max_s = reinterpret_cast<float*>(sp);  // [softmax warps][64] maxima of one chunk, while no weights are there
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
-  float* slope_s = reinterpret_cast<float*>(smem + kOffSlope);
   float* join_s = reinterpret_cast<float*>(smem + kOffJoin);
   long long* scan = reinterpret_cast<long long*>(smem + kOffScan);
   int* start = reinterpret_cast<int*>(smem + kOffScan + kWarps * 8);
   uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* qempty = qfull + 1;
-  uint64_t* slfull = qempty + 1;         // [ring] slots of a chunk
-  uint64_t* slempty = slfull + kRing;    // by the copying and the softmax warps
-  uint64_t* kvfull = slempty + kRing;    // [quarter]
-  uint64_t* kvempty = kvfull + kPairs;   // [quarter]
-  uint64_t* sfull = kvempty + kPairs;
-  uint64_t* sempty = sfull + 1;
-  uint64_t* pfull = sempty + 1;
-  uint64_t* pempty = pfull + 1;
-  uint64_t* ofull = pempty + 1;          // [O^T slot]
-  uint64_t* oempty = ofull + kOSlots;    // [O^T slot]
-  uint64_t* lready = oempty + kOSlots;   // [item parity] statistics written
-  uint64_t* lfree = lready + 2;          // [item parity] ... and read
+  uint64_t* slfull = qempty + 1;            // [ring] slots of a chunk
+  uint64_t* slempty = slfull + kRing;
+  uint64_t* kvfull = slempty + kRing;       // [buffer][half], by every thread that copies it
+  uint64_t* kvempty = kvfull + 2 * kHalves; // [buffer][half]
+  uint64_t* sfull = kvempty + 2 * kHalves;
+  uint64_t* sempty = sfull + 2;
+  uint64_t* pfull = sempty + 2;
+  uint64_t* pempty = pfull + 2;
+  uint64_t* looked = pempty + 2;            // every softmax warp has seen whether its maxima move
+  uint64_t* ofull = looked + 2;             // [O^T slot]
+  uint64_t* oready = ofull + kOSlots;       // [O^T slot] emptied, and filled with what the sums begin with
+  uint64_t* lready = oready + kOSlots;      // [item parity] statistics written
+  uint64_t* lfree = lready + 2;             // [item parity] ... and read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmemSlot);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto oslot = [](uint32_t item, int db) { return (int)((4u * (item % 7u) + (uint32_t)db) % kOSlots); };
+  // use u = 4 item + quarter of an O^T slot: the slot is u % 6, and this is the slot's (u / 6)-th use
+  auto oslot = [](uint32_t item, int db) { return (int)((4u * item + (uint32_t)db) % kOSlots); };
+  auto ophase = [](uint32_t item, int db) { return ((4u * item + (uint32_t)db) / kOSlots) & 1u; };
 
   if (tid < kNumBars) {  // one barrier a thread
     uint64_t* bar = qfull + tid;
-    mbar_init(bar, bar >= slempty && bar < kvfull ? kCopyWarps + kSoftWarps
-                   : bar >= kvfull && bar < kvempty ? kCopyWarps
-                   : bar == sempty || bar == pfull || (bar >= lready && bar < lfree) ? kSoftWarps
-                   : bar >= oempty ? kOutWarps : 1);
+    mbar_init(bar, bar >= slempty && bar < kvfull ? kCopyWarps
+                   : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps / kHalves
+                   : bar >= sfull && bar < sempty ? 2  // the products' completion and the issuing warp itself
+                   : (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || (bar >= lready && bar < lfree) ? kSoftWarps
+                   : bar >= oready ? kOutWarps : 1);
     fence_mbarrier_init();
   }
   if (warp == kSWarp) tmem_alloc(tmem_slot, kTmemCols);
@@ -328,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // --------------------------------------------------- every token's rows; this block's part
   {
-    if (tid < kHq) slope_s[tid] = p.slopes ? p.slopes[tid] * kLog2e : 0.f;
     const int per = (p.T + kThreads - 1) / kThreads;
     const int first = tid * per, last = min(first + per, p.T);
     long long sum = 0;
@@ -337,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Span s = span_of(p, t);
       const int n = s.hi - s.lo;
       rows_s[t] = n;
-      sum += chunks_of(n, p.other ? 1 : 0);
+      sum += chunks_of(n);
     }
     long long incl = sum;
 #pragma unroll
@@ -346,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane >= d) incl += o;
     }
     if (lane == 31) scan[warp] = incl;
-    if (tid == 0) start[0] = start[1] = start[2] = 0;
+    if (tid == 0) start[0] = start[1] = start[2] = start[3] = 0;
     __syncthreads();
     long long before = lane < kWarps ? scan[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
@@ -364,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long at = before;
 #pragma unroll 1
       for (int t = first; t < last; ++t) {
-        const int nch = chunks_of(rows_s[t], p.other ? 1 : 0);
+        const int nch = chunks_of(rows_s[t]);
         if (at <= g0 && g0 < at + nch) {
           start[0] = t;
           start[1] = (int)(g0 - at);
@@ -385,198 +374,173 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kCopyWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     // ------------------------------------------------------------------------------- copies
-    // rows 16 warp .. + 15 of the chunk, two at a time: lane / 16 the row, lane % 16 the 16-byte piece of the
-    // quarter's 256 bytes.  Rows 8 apart lie 1024 bytes apart with the same swizzle.
-    const int hi = lane >> 4, piece = lane & 15;
-    uint32_t dst[4];
+    // half warp / 4 of the dims of rows 16 (warp % 4) .. + 15 of the chunk: the 32 lanes copy the 512 bytes of a row
+    // at a time, 16 each.  Rows 8 apart lie 1024 bytes apart with the same swizzle.
+    const int half = warp >> 2, step = warp & 3;
+    uint32_t dst[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * i + hi;
-      dst[i] = smem_u32(skv) + (piece >> 3) * kSlotBytes + (16 * warp + r) * 128 + (((piece & 7) ^ r) << 4);
-    }
-    const char* src[8];
-    uint32_t bytes = 0;  // bit i: row i is there (else it is filled with zeros)
-    auto issue = [&](auto quarter) {
-      constexpr int kQuarter = decltype(quarter)::value, kTo = kQuarter * 2 * kSlotBytes, kFrom = kQuarter * 256;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cp_async16<kTo, kFrom>(dst[i], src[i], (bytes >> i & 1u) << 4);
-        cp_async16<kTo + 1024, kFrom>(dst[i], src[i + 4], (bytes >> (i + 4) & 1u) << 4);
-      }
-    };
-    auto landed = [&](int pr) {
-      fence_proxy_async();  // copied rows -> visible to the tensor core
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kvfull[pr]);
-    };
+    for (int i = 0; i < 8; ++i)
+      dst[i] = smem_u32(skv) + (4 * half + (lane >> 3)) * kSlotBytes + (16 * step + i) * 128 + (((lane & 7) ^ i) << 4);
+    const char* pool = reinterpret_cast<const char*>(p.pool) + half * 512 + lane * 16;
     uint32_t g = 0;
     bool ok = true;
-    for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next()) {
+    for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
 #pragma unroll 1
-      for (int c = w.c0; c < w.c1 && ok; ++c, ++g) {
-        const bool mine = warp < w.steps(c);
+      for (int c = w.c0; c < w.c1; ++c, ++g) {
+        const uint32_t b = g & 1, to = b * kBufBytes;
+        const bool mine = step < w.steps(c);
         ok = wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 100);
-        const int* sl = slot_s + (g % kRing) * kRows + 16 * warp + hi;
-        const char* from = reinterpret_cast<const char*>(w.is_other(c) ? p.other : p.pool) + piece * 16;
-        bytes = 0;
+        int at[16];  // the same in every lane
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = sl[2 * i];
-          src[i] = at < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at << 10);
-          bytes |= at < 0 ? 0u : 1u << i;
-        }
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<int4*>(at + i) = *reinterpret_cast<const int4*>(slot_s + (g % kRing) * kRows + 16 * step + i);
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
-        // A quarter is handed on when the next one is on its way, the last at once.  (One arrival a warp: cp.async's
-        // own arrivals are one a thread, 256 on a barrier.)
-        const uint32_t par = (g & 1) ^ 1;
-        ok = ok && wait_bar_warp(&kvempty[0], par, p.status, 101);
-        if (mine && ok) issue(std::integral_constant<int, 0>());
-        cp_async_commit();
-        ok = ok && wait_bar_warp(&kvempty[1], par, p.status, 101);
-        if (mine && ok) issue(std::integral_constant<int, 1>());
-        cp_async_commit();
-        cp_async_wait<1>();
-        landed(0);
-        ok = ok && wait_bar_warp(&kvempty[2], par, p.status, 101);
-        if (mine && ok) issue(std::integral_constant<int, 2>());
-        cp_async_commit();
-        cp_async_wait<1>();
-        landed(1);
-        ok = ok && wait_bar_warp(&kvempty[3], par, p.status, 101);
-        if (mine && ok) issue(std::integral_constant<int, 3>());
-        cp_async_commit();
-        cp_async_wait<1>();
-        landed(2);
-        cp_async_wait<0>();
-        landed(3);
+        ok = ok && wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 101);
+        if (!ok) break;
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // a row without a slot is filled with zeros
+            const char* s0 = at[i] < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at[i] << 10);
+            const char* s1 = at[i + 8] < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at[i + 8] << 10);
+            cp_async16<0>(dst[i] + to, s0, at[i] < 0 ? 0u : 16u);
+            cp_async16<1024>(dst[i] + to, s1, at[i + 8] < 0 ? 0u : 16u);
+          }
+        }
+        cp_async_arrive(&kvfull[b * kHalves + half]);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kSWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMiscRegs));
     if (warp == kSWarp) {
-      // -------------------------------------------------------------------- S^T = K Q^T
+      // ------------------------------------------------------------------------ S = Q K^T
       uint32_t g = 0, item = 0;
       bool ok = true;
       const uint32_t q_lo = (uint32_t)desc_sw128(smem_u32(sq), 16, 1024), k_lo = (uint32_t)desc_sw128(smem_u32(skv), 16, 1024);
-      for (Walk w(rows_s, start, p); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
-          if (!wait_bar_warp(sempty, (g & 1) ^ 1, p.status, 102)) { ok = false; break; }
+          const int b = g & 1;
+          if (!wait_bar_warp(&sempty[b], ((g >> 1) & 1) ^ 1, p.status, 102)) { ok = false; break; }
           if (c == w.c0 && !wait_bar_warp(qfull, item & 1, p.status, 103)) { ok = false; break; }
 #pragma unroll 1
-          for (int pr = 0; pr < kPairs; ++pr) {
-            if (!wait_bar_warp(&kvfull[pr], g & 1, p.status, 104)) { ok = false; break; }
+          for (int half = 0; half < kHalves; ++half) {
+            if (!wait_bar_warp(&kvfull[b * kHalves + half], (g >> 1) & 1, p.status, 104)) { ok = false; break; }
+            fence_proxy_async();  // copied rows -> visible to the tensor core
             tc_fence_after();
-            const uint32_t a = k_lo + (pr * 2 * kSlotBytes >> 4), b = q_lo + (pr * 2 * kQBlockBytes >> 4);
-            if (w.is_other(c)) continue;  // whose weights are known
+            const uint32_t a = q_lo + half * (4 * kQBlockBytes >> 4), k = k_lo + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
+            mma_elect<false>(tmem + b * kHq, a, k, kIdescS, half);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              mma_elect(tmem, a + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), b + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
-                        kIdescS, (uint32_t)(pr | i));
+            for (int i = 1; i < 16; ++i)
+              mma_elect<true>(tmem + b * kHq, a + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
+                              k + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), kIdescS, 1);
           }
           if (!ok) break;
           if (c == w.c1 - 1) tc_commit_elect(qempty);  // the next item's q may replace this one's
-          tc_commit_elect(sfull);
+          // the arrival of this warp hands on what it waited for (the chunk's mask)
+          if (lane == 0) mbar_arrive(&sfull[b]);
+          tc_commit_elect(&sfull[b]);
         }
       }
     } else if (warp == kOWarp) {
-      // ------------------------------------------------------------------- O^T += V^T P
+      // --------------------------------------------------------------------- O^T += V^T P^T
       uint32_t g = 0, item = 0;
-      uint32_t o_ph = 0;  // bit s: phase of O^T slot s's empty barrier
       bool ok = true;
       const uint32_t v_lo = (uint32_t)desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_lo = (uint32_t)desc_sw128(smem_u32(sp), 16, 1024);
-      for (Walk w(rows_s, start, p); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+      for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+        const int begun = p.other != nullptr && w.c0 == 0;  // the slots hold what the sums begin with
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
-          const int steps = w.steps(c);
-          if (!wait_bar_warp(pfull, g & 1, p.status, 105)) { ok = false; break; }
+          const int b = g & 1, steps = w.steps(c);
+          if (!wait_bar_warp(&pfull[b], (g >> 1) & 1, p.status, 105)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int db = 0; db < kPairs; ++db) {
             const int os = oslot(item, db);
-            // an item's first product overwrites its slot: the output that last read it is done
             if (c == w.c0) {
-              if (!wait_bar_warp(&oempty[os], ((o_ph >> os) & 1u) ^ 1u, p.status, 106)) { ok = false; break; }
-              o_ph ^= 1u << os;
+              if (!wait_bar_warp(&oready[os], ophase(item, db), p.status, 106)) { ok = false; break; }
               tc_fence_after();
             }
-            const uint32_t a = v_lo + (db * 2 * kSlotBytes >> 4);
+            const uint32_t a = v_lo + (b * kBufBytes + 2 * db * kSlotBytes >> 4), k = p_lo + (b * kPBytes >> 4);
             const uint32_t d = tmem + kColO + os * kHq;
-            if (steps == kRows / 16) {
+            mma_elect<false>(d, a, k, kIdescO, (uint32_t)((c > w.c0) | begun));
+            if (__all_sync(0xffffffffu, steps == kRows / 16)) {
 #pragma unroll
-              for (int ks = 0; ks < kRows / 16; ++ks)
-                mma_elect(d, a + (ks * 2048 >> 4), p_lo + (ks * 2048 >> 4), kIdescO, (uint32_t)((c > w.c0) | ks));
+              for (int ks = 1; ks < kRows / 16; ++ks) mma_elect<true>(d, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             } else {
 #pragma unroll 1
-              for (int ks = 0; __all_sync(0xffffffffu, ks < steps); ++ks)
-                mma_elect(d, a + (ks * 2048 >> 4), p_lo + (ks * 2048 >> 4), kIdescO, (uint32_t)((c > w.c0) | ks));
+              for (int ks = 1; __all_sync(0xffffffffu, ks < steps); ++ks)
+                mma_elect<true>(d, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             }
-            tc_commit_elect(&kvempty[db]);  // this quarter of the chunk is free
+            if (db & 1) tc_commit_elect(&kvempty[b * kHalves + (db >> 1)]);  // this half of the chunk is free
             if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
           }
           if (!ok) break;
-          tc_commit_elect(pempty);
+          tc_commit_elect(&pempty[b]);
         }
       }
     } else if (warp == kSlotWarp) {
       // --------------------------------------------------------- slots of the rows, a few chunks ahead
       uint32_t g = 0;
       bool ok = true;
-      for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next()) {
+      for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
         const Span s = span_of(p, w.t);
-        const int n = s.hi - s.lo;
-        const int32_t* table = p.tables + (int64_t)(n > 0 ? s.b : 0) * p.max_pages;
+        const int32_t* table = p.tables + (int64_t)(w.n > 0 ? s.b : 0) * p.max_pages;
+#pragma unroll 1
         for (int c = w.c0; c < w.c1; ++c, ++g) {
-          int slot[4];
+          int slot[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = (c - w.extra) * kRows + lane + 32 * i;
+          for (int i = 0; i < 2; ++i) {
+            const int j = c * kRows + lane + 32 * i;
             slot[i] = -1;
-            if (j < 0) {  // row h of the other attention's output, if that saw anything
-              const int at = w.t * kHq + lane + 32 * i;
-              if (i < kHq / 32 && p.other_lse[at] != -INFINITY) slot[i] = at;
-            } else if (j < n) {
+            if (j < w.n) {
               const int row = s.hi - 1 - j;
               const int page = __ldg(table + (row >> p.log_page));
               const int64_t at = ((int64_t)page << p.log_page) + (row & ((1 << p.log_page) - 1));
               if (page >= 0 && at < p.n_slots) slot[i] = (int)at;
             }
           }
+          const uint32_t m0 = __ballot_sync(0xffffffffu, slot[0] >= 0), m1 = __ballot_sync(0xffffffffu, slot[1] >= 0);
           ok = wait_bar_warp(&slempty[g % kRing], ((g / kRing) & 1) ^ 1, p.status, 107);
           if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            slot_s[(g % kRing) * kRows + lane + 32 * i] = slot[i];
-            // Runs of rows that lie together (the list runs backwards) are brought to L2, one request a run: a
-            // request takes its warp about 70 clocks, whatever its size.
-            const int behind = __shfl_up_sync(0xffffffffu, slot[i], 1);
-            const uint32_t begins = __ballot_sync(0xffffffffu, lane == 0 || slot[i] != behind - 1 || behind < 0);
-            if (p.fetch_ahead && !w.is_other(c) && slot[i] >= 0 && (begins >> lane & 1)) {
-              const uint32_t later = begins & (0xfffffffeu << lane);
-              const int len = (later ? __ffs(later) - 1 : 32) - lane;
-              prefetch_l2(p.pool + (int64_t)(slot[i] - len + 1) * kDim, len * kDim * 2);
-            }
+          for (int i = 0; i < 2; ++i) slot_s[(g % kRing) * kRows + lane + 32 * i] = slot[i];
+          // a mask is overwritten eight chunks later: its slots were read then four chunks ago, by warps that
+          // are at most two chunks ahead of the softmax
+          if (lane == 0) {
+            *reinterpret_cast<uint2*>(mask_s + (g % kMaskRing) * 2) = make_uint2(m0, m1);
+            ahead_s[g % kMaskRing] = s.e - s.hi;
           }
-          if (lane == 0) ahead_s[g % kRing] = s.e - s.hi;
           __syncwarp();
           if (lane == 0) mbar_arrive(&slfull[g % kRing]);
+          if (p.fetch_ahead) {
+            // Runs of rows that lie together (the list runs backwards) are brought to L2, one request a run: a
+            // request takes its warp about 70 clocks, whatever its size.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int behind = __shfl_up_sync(0xffffffffu, slot[i], 1);
+              const uint32_t begins = __ballot_sync(0xffffffffu, lane == 0 || slot[i] != behind - 1 || behind < 0);
+              if (slot[i] >= 0 && (begins >> lane & 1)) {
+                const uint32_t later = begins & (0xfffffffeu << lane);
+                const int len = (later ? __ffs(later) - 1 : 32) - lane;
+                prefetch_l2(p.pool + (int64_t)(slot[i] - len + 1) * kDim, len * kDim * 2);
+              }
+            }
+          }
         }
       }
     } else {
       // ------------------------------------------------------------------------------ q
       uint32_t item = 0;
       bool ok = true;
-      for (Walk w(rows_s, start, p); w.left > 0 && ok; w.next(), ++item) {
+      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
         ok = wait_bar_warp(qempty, (item & 1) ^ 1, p.status, 108);
         if (!ok) break;
         mbar_arrive_expect_tx_elect(qfull, kQBytes);
 #pragma unroll 1
         for (int i = 0; i < kSlots; ++i) tma_load_2d_elect(sq + i * kQBlockBytes, &tm_q, qfull, i * 64, w.t * kHq);
-        if (lane == 0) {  // what the next token will ask for
-          if (w.c1 == w.end && w.left > w.c1 - w.c0) {
-            prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
-            if (p.other) prefetch_l2(p.other + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
-          }
+        if (lane == 0 && w.c1 == w.end && w.left > w.c1 - w.c0) {  // what the next token will ask for
+          prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
+          if (p.other) prefetch_l2(p.other + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
         }
         __syncwarp();
       }
@@ -584,207 +548,183 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kOutWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------------------- softmax
-    // S^T holds row 32 quad + i of the chunk on TMEM lane 32 quad + i.  A warp takes 16 of its quadrant's lanes; the
-    // 16x256b load gives thread (g = lane / 4, e = lane % 4) rows g and g + 8 of them (A and B) and of each the heads
-    // 8 k + 2 e + {0, 1}, k = 0..7.  So a thread's 32 weights add up to 16 running sums of its own, and lanes meet
-    // at an item's end only: a shuffle takes its turn at shared memory like the products' operands.
-    const int quad = warp & 3, sub = (warp - kSoftWarp) >> 2, rows16 = 2 * quad + sub;
-    const int g8 = lane >> 2, e2 = 2 * (lane & 3);
-    const int rowA = 16 * rows16 + g8, rowB = rowA + 8;
-    const uint32_t t_lane = static_cast<uint32_t>(quad * 32 + sub * 16) << 16;
+    // S holds head 16 quad + i on TMEM lane 32 quad + i (i < 16).  The 16x256b load gives thread
+    // (g8 = lane / 4, e = lane % 4) the heads hA = 16 quad + g8 and hB = hA + 8 and, of each, the
+    // columns 8 k + 2 e + {0, 1}, k = 0..7: a head's 64 logits are spread over 4 threads.
+    const int quad = warp & 3;
+    const int g8 = lane >> 2, e = lane & 3;
+    const int hA = 16 * quad + g8, hB = hA + 8;
+    const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
     const bool capped = p.cap > 0.f, sloped = p.slopes != nullptr;
-    // logits in log2 units: a product times `unit`, less the offset in one fused step (an offset's rounding cancels
-    // between weights and lse); capped or sloped ones are formed first
-    const float scale2 = p.scale * kLog2e, unit = capped || sloped ? 1.f : scale2;
+    const float scale2 = p.scale * kLog2e;
     const float cap2 = p.cap * kLog2e, in_cap = capped ? 2.f * kLog2e * (p.scale / p.cap) : 0.f;
-    // rows A and B have the same swizzle: they lie 8 apart
-    const uint32_t line = smem_u32(sp) + rowA * 128 + 2 * e2, swz = (rowA & 7) << 4;
-    const int hr = 8 * g8 + e2;  // the first of the two heads whose reduced values this lane ends with
+    const float slopeA = sloped ? p.slopes[hA] * kLog2e : 0.f, slopeB = sloped ? p.slopes[hB] * kLog2e : 0.f;
     uint32_t g = 0, item = 0;
-    // a wait that gave up is acted on where the eight warps meet, so that they leave together
+    // a wait that gave up is acted on where the four warps meet, so that they leave together
     bool ok = true, leave = false;
-    for (Walk w(rows_s, start, p); w.left > 0 && !leave; w.next(), ++item) {
-      float* m_row = m_s + (item & 1) * kHq;
-      float l[16], r[16];  // sums of this thread's weights of a head, and of the rounded ones
-#pragma unroll
-      for (int i = 0; i < 16; ++i) l[i] = r[i] = 0.f;
+    for (Walk w(rows_s, start); w.left > 0 && !leave; w.next(), ++item) {
+      float oA = kNone, oB = kNone;                  // offsets
+      float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of the weights, and of the rounded ones
+      const bool begun = p.other != nullptr && w.c0 == 0;
+      if (begun) {
+        const float a = __ldg(p.other_lse + (int64_t)w.t * kHq + hA), b = __ldg(p.other_lse + (int64_t)w.t * kHq + hB);
+        oA = first_offset(a);
+        oB = first_offset(b);
+        if (e == 0) {
+          lA = rA = first_weight(a);
+          lB = rB = first_weight(b);
+        }
+      }
 #pragma unroll 1
       for (int c = w.c0; c < w.c1; ++c, ++g) {
-        ok = ok && wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 110);
-        const int* sl = slot_s + (g % kRing) * kRows + rowA;
-        const bool liveA = sl[0] >= 0, liveB = sl[8] >= 0;
-        const int ahead = ahead_s[g % kRing];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&slempty[g % kRing]);
-        ok = ok && wait_bar_warp(sfull, g & 1, p.status, 111);
+        const int b = g & 1;
+        ok = ok && wait_bar_warp(&sfull[b], (g >> 1) & 1, p.status, 111);
         tc_fence_after();
-        if (w.is_other(c)) {
-          // The other attention's output of head h as a row that head h alone sees, with a logit of that attention's
-          // log-sum-exp: the token's first chunk, its weights 2^4 on the diagonal.
-          if (lane == 0) mbar_arrive(sempty);
-          ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 116);
-          const float* lse_row = p.other_lse + (int64_t)w.t * kHq;
-          const int th = tid - 32 * kSoftWarp;
-          if (th < kHq) m_row[th] = fmaxf(lse_row[th] * kLog2e - kWeightLog2, kNone);
-          leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
-          if (leave) break;
-          if (rows16 < kHq / 16) {
-            const float wa = liveA ? ex2_approx(lse_row[rowA] * kLog2e - m_row[rowA]) : 0.f;
-            const float wb = liveB ? ex2_approx(lse_row[rowB] * kLog2e - m_row[rowB]) : 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int h = 8 * k + e2;
-              const float a0 = h == rowA ? wa : 0.f, a1 = h + 1 == rowA ? wa : 0.f;
-              const float b0 = h == rowB ? wb : 0.f, b1 = h + 1 == rowB ? wb : 0.f;
-              const uint32_t at = line + ((k << 4) ^ swz);
-              asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0 + 1024], %2;" ::"r"(at), "r"(pack16<kBf16>(a0, a1)),
-                           "r"(pack16<kBf16>(b0, b1))
-                           : "memory");
-              l[2 * k] = r[2 * k] = a0 + b0;
-              l[2 * k + 1] = r[2 * k + 1] = a1 + b1;
-            }
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull);
-          continue;
-        }
         float x[32];
-        tmem_ld_16x256b_x8(tmem + t_lane, x);
+        tmem_ld_16x256b_x8(tmem + t_lane + b * kHq, x);
+        const uint2 live = *reinterpret_cast<const uint2*>(mask_s + (g % kMaskRing) * 2);
+        const int ahead = ahead_s[g % kMaskRing];
         tc_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sempty);
+        if (lane == 0) mbar_arrive(&sempty[b]);
+        // logits in log2 units
         if (capped) {  // tanh y = 1 - 2 / (e^2y + 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = fmaf(-2.f * cap2, rcp_approx(ex2_approx(x[i] * in_cap) + 1.f), cap2);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] *= scale2;
         }
-        if (sloped) {  // e - 1 - r, r = hi - 1 - list index
-          const float distA = fabsf((float)(ahead + (c - w.extra) * kRows + rowA));
-          const float distB = fabsf((float)(ahead + (c - w.extra) * kRows + rowB));
-          const float mul = capped ? 1.f : scale2;
+        if (sloped) {  // e - 1 - r of row r = hi - 1 - list index
+          const int d0 = ahead + c * kRows + 2 * e;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float2 s = *reinterpret_cast<const float2*>(slope_s + 8 * k + e2);
-            x[4 * k] = fmaf(x[4 * k], mul, -s.x * distA);
-            x[4 * k + 1] = fmaf(x[4 * k + 1], mul, -s.y * distA);
-            x[4 * k + 2] = fmaf(x[4 * k + 2], mul, -s.x * distB);
-            x[4 * k + 3] = fmaf(x[4 * k + 3], mul, -s.y * distB);
+            const float near = fabsf((float)(d0 + 8 * k)), far = fabsf((float)(d0 + 8 * k + 1));
+            x[4 * k] = fmaf(-slopeA, near, x[4 * k]);
+            x[4 * k + 1] = fmaf(-slopeA, far, x[4 * k + 1]);
+            x[4 * k + 2] = fmaf(-slopeB, near, x[4 * k + 2]);
+            x[4 * k + 3] = fmaf(-slopeB, far, x[4 * k + 3]);
           }
         }
-        const bool part = !(liveA && liveB);
-        if (c == w.c0) {
-          // the item's first offsets: of its first row in bf16, of the largest of eight rows in fp16, whose range is less
-          if (g8 == 0 && (!kBf16 || rowA == 0)) {
-            ok = ok && wait_bar(pempty, (g & 1) ^ 1, p.status, 117);  // P is free (and S^T would not be there otherwise)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 m = make_float2(fmaxf(x[4 * k] * unit - kWeightLog2, kNone), fmaxf(x[4 * k + 1] * unit - kWeightLog2, kNone));
-              *reinterpret_cast<float2*>((kBf16 ? m_row : max_s + rows16 * kHq) + 8 * k + e2) = liveA ? m : make_float2(kNone, kNone);
-            }
-          }
-          named_sync(kSoftBar, 32 * kSoftWarps);
-          if constexpr (!kBf16) {
-            const int th = tid - 32 * kSoftWarp;
-            if (th < kHq) {
-              float mx = max_s[th];
-#pragma unroll
-              for (int i = 1; i < kSoftWarps; ++i) mx = fmaxf(mx, max_s[i * kHq + th]);
-              m_row[th] = mx;
-            }
-            named_sync(kSoftBar, 32 * kSoftWarps);
-          }
-        }
-        bool moved = !ok;
-        {
-          float overA = -INFINITY, overB = -INFINITY;
+        if ((live.x & live.y) != 0xffffffffu) {
+          const uint32_t v0 = live.x >> (2 * e), v1 = live.y >> (2 * e);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float2 m = *reinterpret_cast<const float2*>(m_row + 8 * k + e2);
-            overA = fmaxf(overA, fmaxf(fmaf(x[4 * k], unit, -m.x), fmaf(x[4 * k + 1], unit, -m.y)));
-            overB = fmaxf(overB, fmaxf(fmaf(x[4 * k + 2], unit, -m.x), fmaf(x[4 * k + 3], unit, -m.y)));
-          }
-          moved = moved || (liveA && overA > kRescale + kWeightLog2) || (liveB && overB > kRescale + kWeightLog2);
-        }
-        if (named_or(kSoftBar, 32 * kSoftWarps, moved)) {
-          ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 112);  // P is free for the maxima, O^T complete
-          leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
-          if (leave) break;
-          {
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              v[2 * k] = fmaxf(liveA ? x[4 * k] * unit : -INFINITY, liveB ? x[4 * k + 2] * unit : -INFINITY);
-              v[2 * k + 1] = fmaxf(liveA ? x[4 * k + 1] * unit : -INFINITY, liveB ? x[4 * k + 3] * unit : -INFINITY);
-            }
-            *reinterpret_cast<float2*>(max_s + rows16 * kHq + hr) = reduce_rows<true>(v);
-          }
-          named_sync(kSoftBar, 32 * kSoftWarps);
-          const int th = tid - 32 * kSoftWarp;
-          if (th < kHq) {
-            float mx = max_s[th];
-#pragma unroll
-            for (int i = 1; i < kSoftWarps; ++i) mx = fmaxf(mx, max_s[i * kHq + th]);
-            const float m = m_row[th];
-            const bool up = mx - m > kRescale + kWeightLog2;
-            alpha_s[th] = up ? ex2_approx(m - (mx - kWeightLog2)) : 1.f;
-            m_row[th] = up ? mx - kWeightLog2 : m;
-          }
-          named_sync(kSoftBar, 32 * kSoftWarps);
-          if (c > w.c0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 a = *reinterpret_cast<const float2*>(alpha_s + 8 * k + e2);
-              l[2 * k] *= a.x;
-              l[2 * k + 1] *= a.y;
-              r[2 * k] *= a.x;
-              r[2 * k + 1] *= a.y;
-            }
-            tc_fence_after();
-            const uint32_t t_half = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + 32 * sub;
-#pragma unroll 1
-            for (int q = 0; q < 2 * kPairs; ++q) {  // all lanes of the quadrant, half of the heads, 16 at a time
-              float v[16];
-              const uint32_t ta = t_half + oslot(item, q >> 1) * kHq + 16 * (q & 1);
-              tmem_ld16(ta, v);
-              tc_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= alpha_s[32 * sub + 16 * (q & 1) + i];
-              tmem_st16(ta, v);
-            }
-            tc_wait_st();
+            const uint32_t bits = (k < 4 ? v0 : v1) >> (8 * (k & 3));
+            if (!(bits & 1u)) x[4 * k] = x[4 * k + 2] = -INFINITY;
+            if (!(bits & 2u)) x[4 * k + 1] = x[4 * k + 3] = -INFINITY;
           }
         }
-        ok = ok && wait_bar_warp(pempty, (g & 1) ^ 1, p.status, 113);
-        // weights 2^(x - offset), rounded for the product
+        float mxA = -INFINITY, mxB = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float2 m = *reinterpret_cast<const float2*>(m_row + 8 * k + e2);
-          float a0 = ex2_approx(fmaf(x[4 * k], unit, -m.x)), a1 = ex2_approx(fmaf(x[4 * k + 1], unit, -m.y));
-          float b0 = ex2_approx(fmaf(x[4 * k + 2], unit, -m.x)), b1 = ex2_approx(fmaf(x[4 * k + 3], unit, -m.y));
-          if (part) {
-            if (!liveA) a0 = a1 = 0.f;
-            if (!liveB) b0 = b1 = 0.f;
+          mxA = fmaxf(mxA, fmaxf(x[4 * k], x[4 * k + 1]));
+          mxB = fmaxf(mxB, fmaxf(x[4 * k + 2], x[4 * k + 3]));
+        }
+        mxA = fmaxf(mxA, __shfl_xor_sync(0xffffffffu, mxA, 1));
+        mxB = fmaxf(mxB, __shfl_xor_sync(0xffffffffu, mxB, 1));
+        mxA = fmaxf(mxA, __shfl_xor_sync(0xffffffffu, mxA, 2));
+        mxB = fmaxf(mxB, __shfl_xor_sync(0xffffffffu, mxB, 2));
+        float aA = 1.f, aB = 1.f;
+        if (mxA - oA > kRescale + kWeightLog2) {
+          aA = ex2_approx(oA - (mxA - kWeightLog2));
+          oA = mxA - kWeightLog2;
+        }
+        if (mxB - oB > kRescale + kWeightLog2) {
+          aB = ex2_approx(oB - (mxB - kWeightLog2));
+          oB = mxB - kWeightLog2;
+        }
+        // Whether any head's maximum moves is said now and asked for when the weights are ready (the same answer in
+        // all four warps: a later chunk's word is written after all have read this one's).  Before an item's first
+        // product there is nothing to move, unless its sums have begun.
+        const bool moved = __any_sync(0xffffffffu, ((aA != 1.f || aB != 1.f) && (c > w.c0 || begun)) || !ok);
+        if (lane == 0) {
+          if (moved) *const_cast<volatile int*>(start + 3) = (int)(g + 1);
+          mbar_arrive(&looked[b]);
+        }
+        lA *= aA;
+        rA *= aA;
+        lB *= aB;
+        rB *= aB;
+        // weights 2^(x - offset), rounded for the product
+        uint32_t pkA[8], pkB[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float a0 = ex2_approx(x[4 * k] - oA), a1 = ex2_approx(x[4 * k + 1] - oA);
+          const float b0 = ex2_approx(x[4 * k + 2] - oB), b1 = ex2_approx(x[4 * k + 3] - oB);
+          lA += a0 + a1;
+          lB += b0 + b1;
+          pkA[k] = pack16<kBf16>(a0, a1);
+          pkB[k] = pack16<kBf16>(b0, b1);
+          add_pair<kBf16>(rA, pkA[k]);
+          add_pair<kBf16>(rB, pkB[k]);
+        }
+        ok = ok && wait_bar_warp(&looked[b], (g >> 1) & 1, p.status, 110);
+        if (*const_cast<volatile int*>(start + 3) == (int)(g + 1)) {
+          leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
+          if (leave) break;
+          if (e == 0) {
+            alpha_s[hA] = aA;
+            alpha_s[hB] = aB;
           }
-          const uint32_t wa = pack16<kBf16>(a0, a1), wb = pack16<kBf16>(b0, b1);
-          const uint32_t at = line + ((k << 4) ^ swz);
-          asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0 + 1024], %2;" ::"r"(at), "r"(wa), "r"(wb) : "memory");
-          l[2 * k] += a0 + b0;
-          l[2 * k + 1] += a1 + b1;
-          add_pair<kBf16>(r[2 * k], r[2 * k + 1], wa);
-          add_pair<kBf16>(r[2 * k], r[2 * k + 1], wb);
+          named_sync(kSoftBar, 32 * kSoftWarps);
+          // O^T must hold all of the previous chunk, or what the sums begin with, before its columns are rescaled
+          if (c > w.c0) {
+            const uint32_t prev = g - 1;
+            ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 112);
+          } else {
+            for (int db = 0; db < kPairs; ++db)
+              ok = ok && wait_bar_warp(&oready[oslot(item, db)], ophase(item, db), p.status, 116);
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q2 = 0; q2 < 2 * kPairs; ++q2) {  // 4 quarters x 2 halves of 32 heads
+            float v[32];
+            const uint32_t ta = tmem + t_lane + kColO + oslot(item, q2 >> 1) * kHq + (q2 & 1) * 32;
+            tmem_ld32(ta, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= alpha_s[(q2 & 1) * 32 + i];
+            tmem_st32(ta, v);
+          }
+          tc_wait_st();
+          named_sync(kSoftBar, 32 * kSoftWarps);
+        }
+        ok = ok && wait_bar_warp(&pempty[b], ((g >> 1) & 1) ^ 1, p.status, 113);
+        {
+          // P[h][j], K-major with the 128-byte swizzle: 16-byte chunk k of line h at (k ^ (h & 7)); hA and hB alike
+          uint8_t* line = sp + b * kPBytes + hA * 128 + 4 * e;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            *reinterpret_cast<uint32_t*>(line + ((k ^ g8) << 4)) = pkA[k];
+            *reinterpret_cast<uint32_t*>(line + ((k ^ g8) << 4) + 1024) = pkB[k];
+          }
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull);
+        if (lane == 0) mbar_arrive(&pfull[b]);
       }
       if (leave) break;
-      // the statistics of the item before are read (and so, an item later, are these offsets)
-      ok = ok && (item == 0 || wait_bar_warp(&lfree[(item & 1) ^ 1], ((item - 1) >> 1) & 1, p.status, 109));
-      float* st = stat_s + rows16 * 2 * kHq + hr;
-      *reinterpret_cast<float2*>(st) = reduce_rows<false>(r);
-      *reinterpret_cast<float2*>(st + kHq) = reduce_rows<false>(l);
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) {
+        lA += __shfl_xor_sync(0xffffffffu, lA, d);
+        lB += __shfl_xor_sync(0xffffffffu, lB, d);
+        rA += __shfl_xor_sync(0xffffffffu, rA, d);
+        rB += __shfl_xor_sync(0xffffffffu, rB, d);
+      }
+      // the statistics of this item's parity were last read by the output of item - 2
+      ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 109);
+      if (e == 0) {
+        float* st = stat_s + (item & 1) * 3 * kHq;
+        st[hA] = rA;
+        st[kHq + hA] = lA;
+        st[2 * kHq + hA] = oA;
+        st[hB] = rB;
+        st[kHq + hB] = lB;
+        st[2 * kHq + hB] = oB;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&lready[item & 1]);
     }
@@ -792,32 +732,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // --------------------------------------------------------------------------- output
     const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 5, to = tid - 32 * kOutWarp;
-    const uint32_t t_lane = (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
-    float *so_far = join_s, *f_first = join_s + 3 * kHq, *f_item = join_s + 4 * kHq;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
+    const int at0 = hb * kDim + quad * 32 + lane;  // this thread's first head and dim of a quarter, within a token
+    float *so_far = join_s, *f_first = join_s + 3 * kHq, *f_item = join_s + 4 * kHq, *f_other = join_s + 5 * kHq;
     uint32_t item = 0;
-    uint32_t f_ph = 0;  // bit s: phase of O^T slot s's full barrier
     bool ok = true;
     int from = 0;       // the block's first chunk of the token
-    for (Walk w(rows_s, start, p); w.left > 0; w.next(), ++item) {
+    uint16_t theirs[32];
+    // the other attention's output of token t at this thread's dim of quarter db, where it counts
+    auto load_other = [&](int t, int db) {
+      const uint16_t* src = p.other + (int64_t)t * kHq * kDim + db * 128 + at0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) theirs[i] = f_other[hb + i] == 0.f ? 0 : __ldg(src + i * kDim);
+    };
+    // slot of quarter db of item n is empty; with another attention to join its sums begin with that
+    auto ready = [&](uint32_t n, int db, bool begun) {
+      if (begun) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = f_other[hb + i] * from16<kBf16>(theirs[i]);
+        tmem_st32(t_lane + oslot(n, db) * kHq, v);
+        tc_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&oready[oslot(n, db)]);
+    };
+    Walk w(rows_s, start);
+    {
+      const bool begun = w.left > 0 && p.other && w.c0 == 0;
+      if (begun) {
+        if (to < kHq) f_other[to] = first_weight(p.other_lse[(int64_t)w.t * kHq + to]);
+        named_sync(kOutBar, 32 * kOutWarps);
+      }
+#pragma unroll 1
+      for (int db = 0; db < kPairs; ++db) {
+        if (begun) load_other(w.t, db);
+        ready(0, db, begun);
+      }
+    }
+    while (w.left > 0) {
       const int par = item & 1;
-      ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
       // chunks before the block, or behind it: the sums go to the block's first or second part
       if (w.c0 == 0 || item == 0) from = w.c0;
       const bool begins = w.c0 == from, ends = w.c1 == w.end;
-      const bool whole = ends && from == 0 && w.c1 == chunks_of(w.n, w.extra);
+      const bool whole = ends && from == 0 && w.c1 == chunks_of(w.n);
       const bool joins = !(begins && ends);  // one of several items: joined to those so far
       const int64_t part = 2 * (int64_t)blockIdx.x + (from == 0);
+      const int t = w.t;
+      w.next();
+      const bool more = w.left > 0, begun = more && p.other && w.c0 == 0;  // the next item
+      const float next_lse = begun && to < kHq ? __ldg(p.other_lse + (int64_t)w.t * kHq + to) : 0.f;
+      ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
       // the factors of the item before are read by all
       if (!named_and(kOutBar, 32 * kOutWarps, ok)) break;
       if (to < kHq) {
-        const float* st = stat_s + to;
-        float r = 0.f, l = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSoftWarps; ++i) {
-          r += st[2 * i * kHq];
-          l += st[(2 * i + 1) * kHq];
-        }
-        float m = m_s[par * kHq + to];
+        const float* st = stat_s + par * 3 * kHq + to;
+        float r = st[0], l = st[kHq], m = st[2 * kHq];
         float f0 = 0.f, fi = 1.f;
         if (joins) {
           const float m0 = begins ? kNone : so_far[to], mi = m;
@@ -831,9 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           so_far[2 * kHq + to] = l;
         }
         if (whole) {
-          const float sink2 = p.sinks ? p.sinks[to] * kLog2e : -INFINITY;
-          const Joined j = join_head(m, r, l, sink2);
-          if (p.lse) p.lse[(int64_t)w.t * kHq + to] = j.lse;
+          const Joined j = join_head(m, r, l, p.sinks ? p.sinks[to] * kLog2e : -INFINITY);
+          if (p.lse) p.lse[(int64_t)t * kHq + to] = j.lse;
           f0 *= j.own;
           fi *= j.own;
         } else if (ends) {
@@ -844,23 +814,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         f_first[to] = f0;
         f_item[to] = fi;
+        if (begun) f_other[to] = first_weight(next_lse);
       }
       named_sync(kOutBar, 32 * kOutWarps);
       if (lane == 0) mbar_arrive(&lfree[par]);
 #pragma unroll 1
       for (int db = 0; db < kPairs; ++db) {
         const int os = oslot(item, db);
-        const int64_t at = ((int64_t)w.t * kHq + hb) * kDim + db * 128 + quad * 32 + lane;  // of the first head
-        ok = wait_bar_warp(&ofull[os], (f_ph >> os) & 1u, p.status, 115);
+        if (begun) load_other(w.t, db);  // on its way while this quarter goes out
+        ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
         if (!ok) break;
-        f_ph ^= 1u << os;
         tc_fence_after();
         float v[32];
-        tmem_ld32(t_lane + tmem + os * kHq, v);
+        tmem_ld32(t_lane + os * kHq, v);
         tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&oempty[os]);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(f_item + hb + i);
@@ -872,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole || joins) {
           // Sums so far lie where the part's go: the second part's own token is the block's last, behind all that
           // lie whole in the block.  A thread reads back only what it wrote.
-          float* sums = p.part + part * kPartFloats + hb * kDim + db * 128 + quad * 32 + lane;
+          float* sums = p.part + part * kPartFloats + db * 128 + at0;
           if (!begins) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
@@ -880,17 +847,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) sums[i * kDim] = v[i];
-            continue;
           }
         }
-        uint16_t* to_out = p.out + at;
+        if (whole) {
+          uint16_t* to_out = p.out + (int64_t)t * kHq * kDim + db * 128 + at0;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
-          to_out[i * kDim] = (uint16_t)u;
-          to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
+            to_out[i * kDim] = (uint16_t)u;
+            to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
+          }
         }
+        if (more) ready(item + 1, db, begun);
       }
+      ++item;
     }
   }
 
@@ -1125,7 +1095,6 @@ int ds4x_kv16_attn(const void* q_attn, ds4x_dtype dtype, const void* pool, int32
     if (!aligned4(w)) return DS4X_ERR_INVALID;
   int max_rows = max_pages * page_rows;
   if (!prefix && window > 0 && window < max_rows) max_rows = window;
-  if (other_out) max_rows = max_rows > INT32_MAX - kRows ? INT32_MAX : max_rows + kRows;  // a chunk of its own
   const size_t need = ds4x_kv16_attn_workspace_bytes(T, max_rows);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DS4X_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return DS4X_ERR_INVALID;

@@ -524,14 +524,14 @@ int ds4x_kv16_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, c
  *       out[t,h,:] = (sum_r exp(x_r) row_r + exp(other_lse[t,h]) other_out[t,h,:]) / w,   lse[t,h] = log w
  *   so `other`, the out and lse of an attention over other rows (ds4x_kv4_attn over the pooled ones), is joined
  *   into one softmax.  Where w is an empty sum: out = 0 and lse = -INFINITY.  Where other_lse is -INFINITY
- *   other_out is not read; elsewhere it has to be finite (a NaN or infinity of one head reaches the token's others).
+ *   other_out is not read.
  *
  *   q_attn, out, other_out [T, Hq, Dkv] of `dtype`; lse (or NULL), other_lse [T, Hq] fp32; slopes, sinks [Hq]
  *   fp32 or NULL; req, positions, first [T], rows, prefix [n_req] int32, tables [n_req, max_pages].
  *   Hq = 64, Dkv = 512, cap >= 0 and finite.  out and lse overlap no input.
  *   workspace: at least ds4x_kv16_attn_workspace_bytes(T, max_rows) bytes, max_rows the most rows that a token
- *   can see: max_pages * page_rows, or min(window, that) with a window and no prefix; 128 more (INT32_MAX at most)
- *   with other (may be NULL when the size is 0).  Nothing is kept in it between calls; calls that may overlap on the GPU need one each.
+ *   can see: max_pages * page_rows, or min(window, that) with a window and no prefix (may be NULL when the size is
+ *   0).  Nothing is kept in it between calls; calls that may overlap on the GPU need one each.
  *   Sums are fp32.  Softmax weights are rounded to `dtype` for the second product, in numerator and normaliser
  *   alike.  The same arguments give the same bits on every run.  A call may be captured into a CUDA graph after
  *   a first call on the device.
