@@ -16,10 +16,10 @@
 //   O^T [512 x 64 heads]    += V^T . P^T     tcgen05, M = 128 (dims), A MN-major, B K-major
 // with K = V = the chunk in 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
 //
-// Warps: 0-7 copy rows (16-byte cp.async; half of the dims of 16 rows each, one step of the O^T products), 8-11
-// softmax (heads 16*(warp-8) .. +15, 4 threads a head), 12-19 write the output (O^T lanes by quadrant, 32 heads
-// each), 20 issues the S products, 21 the O^T products, 22 looks up the rows' slots a few chunks ahead and brings
-// the rows to L2, 23 loads q.  Buffers are released in halves of the dims, O^T rotates over six 64-column TMEM
+// Warps: 0-3 copy rows (16-byte cp.async; 16 rows each, one step of the O^T products), 4-7 softmax (heads
+// 16*(warp-4) .. +15, 4 threads a head), 8-23 write the output (O^T lanes by quadrant, 16 heads each), 24 issues the
+// S products, 25 the O^T products, 26 looks up the rows' slots a few chunks ahead and brings the rows to L2, 27
+// loads q.  Buffers are released in halves of the dims, O^T rotates over six 64-column TMEM
 // slots (a token uses four), so neighbouring tokens overlap.  A chunk that is not full costs its O^T products and
 // copies by 16 rows.  The other attention's output is where a token's sums begin: the output warps put it, times
 // 2^(o - m), into the O^T slots that they have emptied.
@@ -52,16 +52,18 @@ constexpr int kQBlockBytes = kHq * 128;          // 8 KB (64 heads x 64 dims)
 constexpr int kQBytes = kSlots * kQBlockBytes;   // 64 KB
 constexpr int kPBytes = kHq * 128;               // 8 KB: P[h][j]
 constexpr int kTokens = 2048;                    // tokens a launch plans for
-constexpr int kOutWarp = 12, kSWarp = 20, kOWarp = 21, kSlotWarp = 22, kQWarp = 23;
-constexpr int kCopyWarps = 8, kSoftWarps = 4, kOutWarps = 8;
-constexpr int kWarps = 24, kThreads = 32 * kWarps;
-// registers a thread: 80 at launch; the sum over the six warpgroups stays what it was
-constexpr int kLaunchRegs = 80, kCopyRegs = 64, kMiscRegs = 40, kSoftRegs = 112, kOutRegs = 96;
-static_assert(kThreads * kLaunchRegs <= 65536 && 2 * kCopyRegs + kSoftRegs + 2 * kOutRegs + kMiscRegs <= 6 * kLaunchRegs, "registers");
+constexpr int kOutWarp = 8, kSWarp = 24, kOWarp = 25, kSlotWarp = 26, kQWarp = 27;
+constexpr int kCopyWarps = 4, kSoftWarps = 4, kOutWarps = 16;
+constexpr int kWarps = 28, kThreads = 32 * kWarps;
+// registers a thread: 72 at launch; the sum over the seven warpgroups stays what it was
+constexpr int kLaunchRegs = 72, kMiscRegs = 40, kSoftRegs = 112, kOutRegs = 64;  // and 72 for the copies
+static_assert(kOutRegs < kLaunchRegs && kMiscRegs < kLaunchRegs && kSoftRegs > kLaunchRegs, "dec, dec and inc below");
+static_assert(kThreads * kLaunchRegs <= 65536 && kLaunchRegs + kSoftRegs + 4 * kOutRegs + kMiscRegs <= 7 * kLaunchRegs, "registers");
 constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
 constexpr int kItemChunks = 256;
+constexpr int kTokenUnits = 2;
 constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
 constexpr int kOffP = kOffKV + 2 * kBufBytes;
@@ -73,9 +75,10 @@ constexpr int kOffStat = kOffAhead + kMaskRing * 4;    // float[2 items][sum of 
 constexpr int kOffAlpha = kOffStat + 2 * 3 * kHq * 4;  // float[64]: rescale factors of one chunk
 constexpr int kOffJoin = kOffAlpha + kHq * 4;    // float[6][64]: a token's offset, sum of rounded weights and sum so far; factors
                                                  // of the sums so far, of the item's, and of the next token's other output
-constexpr int kOffScan = kOffJoin + 6 * kHq * 4; // int64[kWarps] warp sums, then int[4]: the block's part, and the
-                                                 // last chunk (+ 1) in which a maximum moved
-constexpr int kOffBars = kOffScan + kWarps * 8 + 16;
+constexpr int kOffScan = kOffJoin + 6 * kHq * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
+                                                 // then int[4]: the block's part, and the last chunk (+ 1) in which a
+                                                 // maximum moved
+constexpr int kOffBars = kOffScan + (kWarps + 2) * 8 + 16;
 constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 5 * 2 + 2 * kOSlots + 2 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
@@ -279,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
   float* join_s = reinterpret_cast<float*>(smem + kOffJoin);
   long long* scan = reinterpret_cast<long long*>(smem + kOffScan);
-  int* start = reinterpret_cast<int*>(smem + kOffScan + kWarps * 8);
+  int* start = reinterpret_cast<int*>(smem + kOffScan + (kWarps + 2) * 8);
   uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* qempty = qfull + 1;
   uint64_t* slfull = qempty + 1;            // [ring] slots of a chunk
   uint64_t* slempty = slfull + kRing;
-  uint64_t* kvfull = slempty + kRing;       // [buffer][half], by every thread that copies it
+  uint64_t* kvfull = slempty + kRing;       // [buffer][half], by every copying thread
   uint64_t* kvempty = kvfull + 2 * kHalves; // [buffer][half]
   uint64_t* sfull = kvempty + 2 * kHalves;
   uint64_t* sempty = sfull + 2;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < kNumBars) {  // one barrier a thread
     uint64_t* bar = qfull + tid;
     mbar_init(bar, bar >= slempty && bar < kvfull ? kCopyWarps
-                   : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps / kHalves
+                   : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps
                    : bar >= sfull && bar < sempty ? 2  // the products' completion and the issuing warp itself
                    : (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || (bar >= lready && bar < lfree) ? kSoftWarps
                    : bar >= oready ? kOutWarps : 1);
@@ -318,6 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // --------------------------------------------------- every token's rows; this block's part
   {
+    // A token costs its chunks and, where there are many tokens a block, about two chunks' time to begin and end: each
+    // counts as that many units, the token's own first, and the blocks take equal numbers of units.
+    const int own = 2 * p.T >= (int)gridDim.x ? kTokenUnits : 0;
     const int per = (p.T + kThreads - 1) / kThreads;
     const int first = tid * per, last = min(first + per, p.T);
     long long sum = 0;
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Span s = span_of(p, t);
       const int n = s.hi - s.lo;
       rows_s[t] = n;
-      sum += chunks_of(n);
+      sum += chunks_of(n) + own;
     }
     long long incl = sum;
 #pragma unroll
@@ -349,22 +355,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long quota = total >> 31 ? (total + gridDim.x - 1) / gridDim.x
                                         : (long long)(((uint32_t)total + gridDim.x - 1u) / gridDim.x);
     const long long g0 = quota * blockIdx.x, g1 = min(total, g0 + quota);
-    if (g0 < total) {
-      long long at = before;
+    // the block's first chunk, and how many chunks lie before its first and its last unit
+    long long at = before, chunks = before - (long long)min(first, p.T) * own;
 #pragma unroll 1
-      for (int t = first; t < last; ++t) {
-        const int nch = chunks_of(rows_s[t]);
-        if (at <= g0 && g0 < at + nch) {
-          start[0] = t;
-          start[1] = (int)(g0 - at);
-          start[2] = (int)(g1 - g0);
-          if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(t, (int)(g0 - at), nch, (int)quota);
-        }
-        at += nch;
+    for (int t = first; t < last; ++t) {
+      const int nch = chunks_of(rows_s[t]);
+      if (at <= g0 && g0 < at + own + nch) {
+        const int c0 = (int)max(g0 - at - own, 0ll);
+        start[0] = t;
+        start[1] = c0;
+        scan[kWarps] = chunks + c0;
+        if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(t, c0, nch, (int)quota);
       }
-    } else if (tid == 0 && p.parts_of) {
-      p.parts_of[blockIdx.x] = make_int4(-1, 0, 0, (int)quota);
+      if (g0 < total && at < g1 && g1 <= at + own + nch) scan[kWarps + 1] = chunks + max(g1 - at - own, 0ll);
+      at += own + nch;
+      chunks += nch;
     }
+    if (g0 >= total && tid == 0) {
+      scan[kWarps] = scan[kWarps + 1] = 0;
+      if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(-1, 0, 0, (int)quota);
+    }
+    __syncthreads();
+    if (tid == 0) start[2] = (int)(scan[kWarps + 1] - scan[kWarps]);
   }
   tc_fence_before();
   __syncthreads();
@@ -372,42 +384,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < kCopyWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     // ------------------------------------------------------------------------------- copies
-    // half warp / 4 of the dims of rows 16 (warp % 4) .. + 15 of the chunk: the 32 lanes copy the 512 bytes of a row
-    // at a time, 16 each.  Rows 8 apart lie 1024 bytes apart with the same swizzle.
-    const int half = warp >> 2, step = warp & 3;
+    // rows 16 warp .. + 15 of the chunk, half of the dims at a time: the 32 lanes copy 512 bytes of a row, 16 each.
+    // Rows 8 apart lie 1024 bytes apart with the same swizzle.
     uint32_t dst[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      dst[i] = smem_u32(skv) + (4 * half + (lane >> 3)) * kSlotBytes + (16 * step + i) * 128 + (((lane & 7) ^ i) << 4);
-    const char* pool = reinterpret_cast<const char*>(p.pool) + half * 512 + lane * 16;
+      dst[i] = smem_u32(skv) + (lane >> 3) * kSlotBytes + (16 * warp + i) * 128 + (((lane & 7) ^ i) << 4);
+    const char* pool = reinterpret_cast<const char*>(p.pool) + lane * 16;
     uint32_t g = 0;
     bool ok = true;
     for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
 #pragma unroll 1
       for (int c = w.c0; c < w.c1; ++c, ++g) {
-        const uint32_t b = g & 1, to = b * kBufBytes;
-        const bool mine = step < w.steps(c);
+        const uint32_t b = g & 1;
+        const bool mine = warp < w.steps(c);
         ok = wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 100);
         int at[16];  // the same in every lane
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<int4*>(at + i) = *reinterpret_cast<const int4*>(slot_s + (g % kRing) * kRows + 16 * step + i);
+          *reinterpret_cast<int4*>(at + i) = *reinterpret_cast<const int4*>(slot_s + (g % kRing) * kRows + 16 * warp + i);
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
-        ok = ok && wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 101);
-        if (!ok) break;
-        if (mine) {
+#pragma unroll 1
+        for (int half = 0; half < kHalves && ok; ++half) {
+          ok = wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 101);
+          if (mine && ok) {
+            const char* from = pool + half * 512;
+            const uint32_t to = b * kBufBytes + half * 4 * kSlotBytes;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // a row without a slot is filled with zeros
-            const char* s0 = at[i] < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at[i] << 10);
-            const char* s1 = at[i + 8] < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at[i + 8] << 10);
-            cp_async16<0>(dst[i] + to, s0, at[i] < 0 ? 0u : 16u);
-            cp_async16<1024>(dst[i] + to, s1, at[i + 8] < 0 ? 0u : 16u);
+            for (int i = 0; i < 8; ++i) {  // a row without a slot is filled with zeros
+              const char* s0 = at[i] < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at[i] << 10);
+              const char* s1 = at[i + 8] < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at[i + 8] << 10);
+              cp_async16<0>(dst[i] + to, s0, at[i] < 0 ? 0u : 16u);
+              cp_async16<1024>(dst[i] + to, s1, at[i + 8] < 0 ? 0u : 16u);
+            }
           }
+          cp_async_arrive(&kvfull[b * kHalves + half]);
         }
-        cp_async_arrive(&kvfull[b * kHalves + half]);
+        if (!ok) break;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -729,29 +744,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&lready[item & 1]);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // --------------------------------------------------------------------------- output
-    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 5, to = tid - 32 * kOutWarp;
+    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 4, to = tid - 32 * kOutWarp;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
     const int at0 = hb * kDim + quad * 32 + lane;  // this thread's first head and dim of a quarter, within a token
     float *so_far = join_s, *f_first = join_s + 3 * kHq, *f_item = join_s + 4 * kHq, *f_other = join_s + 5 * kHq;
     uint32_t item = 0;
     bool ok = true;
     int from = 0;       // the block's first chunk of the token
-    uint16_t theirs[32];
+    uint16_t theirs[16];
     // the other attention's output of token t at this thread's dim of quarter db, where it counts
     auto load_other = [&](int t, int db) {
       const uint16_t* src = p.other + (int64_t)t * kHq * kDim + db * 128 + at0;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) theirs[i] = f_other[hb + i] == 0.f ? 0 : __ldg(src + i * kDim);
+      for (int i = 0; i < 16; ++i) theirs[i] = f_other[hb + i] == 0.f ? 0 : __ldg(src + i * kDim);
     };
     // slot of quarter db of item n is empty; with another attention to join its sums begin with that
     auto ready = [&](uint32_t n, int db, bool begun) {
       if (begun) {
-        float v[32];
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = f_other[hb + i] * from16<kBf16>(theirs[i]);
-        tmem_st32(t_lane + oslot(n, db) * kHq, v);
+        for (int i = 0; i < 16; ++i) v[i] = f_other[hb + i] * from16<kBf16>(theirs[i]);
+        tmem_st16(t_lane + oslot(n, db) * kHq, v);
         tc_wait_st();
       }
       tc_fence_before();
@@ -825,11 +840,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
         if (!ok) break;
         tc_fence_after();
-        float v[32];
-        tmem_ld32(t_lane + os * kHq, v);
+        float v[16];
+        tmem_ld16(t_lane + os * kHq, v);
         tc_wait_ld();
+        if (more && !begun) ready(item + 1, db, false);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(f_item + hb + i);
           v[i] *= f.x;
           v[i + 1] *= f.y;
@@ -842,23 +858,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* sums = p.part + part * kPartFloats + db * 128 + at0;
           if (!begins) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
           }
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sums[i * kDim] = v[i];
+            for (int i = 0; i < 16; ++i) sums[i * kDim] = v[i];
           }
         }
         if (whole) {
           uint16_t* to_out = p.out + (int64_t)t * kHq * kDim + db * 128 + at0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 16; i += 2) {
             const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
             to_out[i * kDim] = (uint16_t)u;
             to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
           }
         }
-        if (more) ready(item + 1, db, begun);
+        if (begun) ready(item + 1, db, true);
       }
       ++item;
     }
@@ -1008,7 +1024,7 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.scale = a.scale;
   p.cap = a.cap;
-  p.fetch_ahead = a.log_page >= 3;
+  p.fetch_ahead = 0;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.parts_of = reinterpret_cast<int4*>(ws);
   for (int t0 = 0; t0 < a.T; t0 += kTokens) {  // launches on one stream: they may share the workspace
