@@ -16,10 +16,10 @@
 //   O^T [512 x 64 heads]    += V^T . P^T     tcgen05, M = 128 (dims), A MN-major, B K-major
 // with K = V = the chunk in 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
 //
-// Warps: 0-3 copy rows (16-byte cp.async; 16 rows each, one step of the O^T products), 4-7 softmax (heads
-// 16*(warp-4) .. +15, 4 threads a head), 8-23 write the output (O^T lanes by quadrant, 16 heads each), 24 issues the
-// S products, 25 the O^T products, 26 looks up the rows' slots a few chunks ahead and brings the rows to L2, 27
-// loads q.  Buffers are released in halves of the dims, O^T rotates over six 64-column TMEM
+// Warps: 0-3 copy rows (16-byte cp.async; 16 rows each, one step of the O^T products), 4-11 softmax (16 heads by
+// quadrant and half of the rows each, 4 threads a head), 12-27 write the output (O^T lanes by quadrant, 16 heads
+// each), 28 issues the S products, 29 the O^T products, 30 looks up the rows' slots a few chunks ahead, 31 loads q.
+// Buffers are copied and released in quarters of the dims, O^T rotates over six 64-column TMEM
 // slots (a token uses four), so neighbouring tokens overlap.  A chunk that is not full costs its O^T products and
 // copies by 16 rows.  The other attention's output is where a token's sums begin: the output warps put it, times
 // 2^(o - m), into the O^T slots that they have emptied.
@@ -44,21 +44,20 @@ constexpr int kHq = 64;
 constexpr int kDim = 512;
 constexpr int kRows = 64;                        // rows per chunk
 constexpr int kSlots = kDim / 64;                // 8 slots of 64 dims
-constexpr int kPairs = kSlots / 2;               // quarters of 128 dims
-constexpr int kHalves = 2;                       // of the dims: what is copied and released together
+constexpr int kPairs = kSlots / 2;               // quarters of 128 dims: what is copied and released together
 constexpr int kSlotBytes = kRows * 128;          // 8 KB
 constexpr int kBufBytes = kSlots * kSlotBytes;   // 64 KB a chunk
 constexpr int kQBlockBytes = kHq * 128;          // 8 KB (64 heads x 64 dims)
 constexpr int kQBytes = kSlots * kQBlockBytes;   // 64 KB
 constexpr int kPBytes = kHq * 128;               // 8 KB: P[h][j]
 constexpr int kTokens = 2048;                    // tokens a launch plans for
-constexpr int kOutWarp = 8, kSWarp = 24, kOWarp = 25, kSlotWarp = 26, kQWarp = 27;
-constexpr int kCopyWarps = 4, kSoftWarps = 4, kOutWarps = 16;
-constexpr int kWarps = 28, kThreads = 32 * kWarps;
-// registers a thread: 72 at launch; the sum over the seven warpgroups stays what it was
-constexpr int kLaunchRegs = 72, kMiscRegs = 40, kSoftRegs = 112, kOutRegs = 64;  // and 72 for the copies
+constexpr int kSoftWarp = 4, kOutWarp = 12, kSWarp = 28, kOWarp = 29, kSlotWarp = 30, kQWarp = 31;
+constexpr int kCopyWarps = 4, kSoftWarps = 8, kOutWarps = 16;
+constexpr int kWarps = 32, kThreads = 32 * kWarps;
+// registers a thread: 64 at launch; the sum over the eight warpgroups stays what it was
+constexpr int kLaunchRegs = 64, kMiscRegs = 40, kSoftRegs = 88, kOutRegs = 56;  // and 64 for the copies
 static_assert(kOutRegs < kLaunchRegs && kMiscRegs < kLaunchRegs && kSoftRegs > kLaunchRegs, "dec, dec and inc below");
-static_assert(kThreads * kLaunchRegs <= 65536 && kLaunchRegs + kSoftRegs + 4 * kOutRegs + kMiscRegs <= 7 * kLaunchRegs, "registers");
+static_assert(kThreads * kLaunchRegs <= 65536 && kLaunchRegs + 2 * kSoftRegs + 4 * kOutRegs + kMiscRegs <= 8 * kLaunchRegs, "registers");
 constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
@@ -71,15 +70,16 @@ constexpr int kOffRows = kOffP + 2 * kPBytes;    // int[kTokens]: rows of each t
 constexpr int kOffSlots = kOffRows + kTokens * 4;      // int[kRing][kRows]: slot of each row of the chunk, -1 for none
 constexpr int kOffMask = kOffSlots + kRing * kRows * 4;  // uint32[kMaskRing][2]: rows of the chunk that count
 constexpr int kOffAhead = kOffMask + kMaskRing * 8;    // int[kMaskRing]: e - hi of the chunk's token
-constexpr int kOffStat = kOffAhead + kMaskRing * 4;    // float[2 items][sum of rounded weights, sum, offset][64]
-constexpr int kOffAlpha = kOffStat + 2 * 3 * kHq * 4;  // float[64]: rescale factors of one chunk
-constexpr int kOffJoin = kOffAlpha + kHq * 4;    // float[6][64]: a token's offset, sum of rounded weights and sum so far; factors
+// float[2 items][2 halves of the rows' sums of rounded weights, 2 halves' sums, offset][64]
+constexpr int kOffStat = kOffAhead + kMaskRing * 4;
+constexpr int kOffMax = kOffStat + 2 * 5 * kHq * 4;    // float[2 halves of the rows][64]: maxima of one chunk
+constexpr int kOffJoin = kOffMax + 2 * kHq * 4;    // float[6][64]: a token's offset, sum of rounded weights and sum so far; factors
                                                  // of the sums so far, of the item's, and of the next token's other output
 constexpr int kOffScan = kOffJoin + 6 * kHq * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
                                                  // then int[4]: the block's part, and the last chunk (+ 1) in which a
                                                  // maximum moved
 constexpr int kOffBars = kOffScan + (kWarps + 2) * 8 + 16;
-constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kHalves + 5 * 2 + 2 * kOSlots + 2 * 2;
+constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kPairs + 5 * 2 + 2 * kOSlots + 2 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -105,7 +105,7 @@ struct Params {
                    // NULL without a workspace, when there can be no rows at all
   float* part;     // [2 grid][kPartFloats]
   float* stat;     // [2 grid][kStatFloats]
-  int n_slots, n_req, max_pages, log_page, ratio, window, t0, T, fetch_ahead;
+  int n_slots, n_req, max_pages, log_page, ratio, window, t0, T;
   float scale, cap;
 };
 
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + kOffMask);
   int* ahead_s = reinterpret_cast<int*>(smem + kOffAhead);
   float* stat_s = reinterpret_cast<float*>(smem + kOffStat);
-  float* alpha_s = reinterpret_cast<float*>(smem + kOffAlpha);
+  float* max_s = reinterpret_cast<float*>(smem + kOffMax);
   float* join_s = reinterpret_cast<float*>(smem + kOffJoin);
   long long* scan = reinterpret_cast<long long*>(smem + kOffScan);
   int* start = reinterpret_cast<int*>(smem + kOffScan + (kWarps + 2) * 8);
@@ -287,9 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* qempty = qfull + 1;
   uint64_t* slfull = qempty + 1;            // [ring] slots of a chunk
   uint64_t* slempty = slfull + kRing;
-  uint64_t* kvfull = slempty + kRing;       // [buffer][half], by every copying thread
-  uint64_t* kvempty = kvfull + 2 * kHalves; // [buffer][half]
-  uint64_t* sfull = kvempty + 2 * kHalves;
+  uint64_t* kvfull = slempty + kRing;       // [buffer][quarter], by every copying thread
+  uint64_t* kvempty = kvfull + 2 * kPairs;  // [buffer][quarter]
+  uint64_t* sfull = kvempty + 2 * kPairs;
   uint64_t* sempty = sfull + 2;
   uint64_t* pfull = sempty + 2;
   uint64_t* pempty = pfull + 2;
@@ -385,44 +385,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kCopyWarps) {
     // ------------------------------------------------------------------------------- copies
-    // rows 16 warp .. + 15 of the chunk, half of the dims at a time: the 32 lanes copy 512 bytes of a row, 16 each.
-    // Rows 8 apart lie 1024 bytes apart with the same swizzle.
-    uint32_t dst[8];
+    // rows 16 warp .. + 15 of the chunk, two at a time: lane / 16 the row, lane % 16 the 16-byte piece of the
+    // quarter's 256 bytes.  Rows 8 apart lie 1024 bytes apart with the same swizzle.
+    const int hi = lane >> 4, piece = lane & 15;
+    uint32_t dst[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      dst[i] = smem_u32(skv) + (lane >> 3) * kSlotBytes + (16 * warp + i) * 128 + (((lane & 7) ^ i) << 4);
-    const char* pool = reinterpret_cast<const char*>(p.pool) + lane * 16;
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * i + hi;
+      dst[i] = smem_u32(skv) + (piece >> 3) * kSlotBytes + (16 * warp + r) * 128 + (((piece & 7) ^ r) << 4);
+    }
+    const char* pool = reinterpret_cast<const char*>(p.pool) + piece * 16;
     uint32_t g = 0;
     bool ok = true;
     for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
 #pragma unroll 1
-      for (int c = w.c0; c < w.c1; ++c, ++g) {
+      for (int c = w.c0; c < w.c1 && ok; ++c, ++g) {
         const uint32_t b = g & 1;
         const bool mine = warp < w.steps(c);
         ok = wait_bar_warp(&slfull[g % kRing], (g / kRing) & 1, p.status, 100);
-        int at[16];  // the same in every lane
+        const int* sl = slot_s + (g % kRing) * kRows + 16 * warp + hi;
+        const char* src[8];
+        uint32_t there = 0;  // bit i: row i has a slot (else it is filled with zeros)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<int4*>(at + i) = *reinterpret_cast<const int4*>(slot_s + (g % kRing) * kRows + 16 * warp + i);
+        for (int i = 0; i < 8; ++i) {
+          const int at = sl[2 * i];
+          src[i] = at < 0 ? reinterpret_cast<const char*>(p.q) : pool + ((int64_t)at << 10);
+          there |= at < 0 ? 0u : 1u << i;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
+        const bool all = __all_sync(0xffffffffu, there == 0xffu);
 #pragma unroll 1
-        for (int half = 0; half < kHalves && ok; ++half) {
-          ok = wait_bar_warp(&kvempty[b * kHalves + half], ((g >> 1) & 1) ^ 1, p.status, 101);
+        for (int pr = 0; pr < kPairs && ok; ++pr) {
+          ok = wait_bar_warp(&kvempty[b * kPairs + pr], ((g >> 1) & 1) ^ 1, p.status, 101);
           if (mine && ok) {
-            const char* from = pool + half * 512;
-            const uint32_t to = b * kBufBytes + half * 4 * kSlotBytes;
+            const uint32_t to = b * kBufBytes + pr * 2 * kSlotBytes;
+            if (all) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // a row without a slot is filled with zeros
-              const char* s0 = at[i] < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at[i] << 10);
-              const char* s1 = at[i + 8] < 0 ? reinterpret_cast<const char*>(p.q) : from + ((int64_t)at[i + 8] << 10);
-              cp_async16<0>(dst[i] + to, s0, at[i] < 0 ? 0u : 16u);
-              cp_async16<1024>(dst[i] + to, s1, at[i + 8] < 0 ? 0u : 16u);
+              for (int i = 0; i < 4; ++i) {
+                cp_async16<0>(dst[i] + to, src[i] + pr * 256, 16);
+                cp_async16<1024>(dst[i] + to, src[i + 4] + pr * 256, 16);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                cp_async16<0>(dst[i] + to, src[i] + pr * 256, (there >> i & 1u) << 4);
+                cp_async16<1024>(dst[i] + to, src[i + 4] + pr * 256, (there >> (i + 4) & 1u) << 4);
+              }
             }
           }
-          cp_async_arrive(&kvfull[b * kHalves + half]);
+          cp_async_arrive(&kvfull[b * kPairs + pr]);
         }
-        if (!ok) break;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -439,14 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait_bar_warp(&sempty[b], ((g >> 1) & 1) ^ 1, p.status, 102)) { ok = false; break; }
           if (c == w.c0 && !wait_bar_warp(qfull, item & 1, p.status, 103)) { ok = false; break; }
 #pragma unroll 1
-          for (int half = 0; half < kHalves; ++half) {
-            if (!wait_bar_warp(&kvfull[b * kHalves + half], (g >> 1) & 1, p.status, 104)) { ok = false; break; }
+          for (int pr = 0; pr < kPairs; ++pr) {
+            if (!wait_bar_warp(&kvfull[b * kPairs + pr], (g >> 1) & 1, p.status, 104)) { ok = false; break; }
             fence_proxy_async();  // copied rows -> visible to the tensor core
             tc_fence_after();
-            const uint32_t a = q_lo + half * (4 * kQBlockBytes >> 4), k = k_lo + (b * kBufBytes + half * 4 * kSlotBytes >> 4);
-            mma_elect<false>(tmem + b * kHq, a, k, kIdescS, half);
+            const uint32_t a = q_lo + pr * (2 * kQBlockBytes >> 4), k = k_lo + (b * kBufBytes + pr * 2 * kSlotBytes >> 4);
+            mma_elect<false>(tmem + b * kHq, a, k, kIdescS, pr);
 #pragma unroll
-            for (int i = 1; i < 16; ++i)
+            for (int i = 1; i < 8; ++i)
               mma_elect<true>(tmem + b * kHq, a + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
                               k + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), kIdescS, 1);
           }
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 1; __all_sync(0xffffffffu, ks < steps); ++ks)
                 mma_elect<true>(d, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             }
-            if (db & 1) tc_commit_elect(&kvempty[b * kHalves + (db >> 1)]);  // this half of the chunk is free
+            tc_commit_elect(&kvempty[b * kPairs + db]);  // this quarter of the chunk is free
             if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
           }
           if (!ok) break;
@@ -527,20 +540,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&slfull[g % kRing]);
-          if (p.fetch_ahead) {
-            // Runs of rows that lie together (the list runs backwards) are brought to L2, one request a run: a
-            // request takes its warp about 70 clocks, whatever its size.
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int behind = __shfl_up_sync(0xffffffffu, slot[i], 1);
-              const uint32_t begins = __ballot_sync(0xffffffffu, lane == 0 || slot[i] != behind - 1 || behind < 0);
-              if (slot[i] >= 0 && (begins >> lane & 1)) {
-                const uint32_t later = begins & (0xfffffffeu << lane);
-                const int len = (later ? __ffs(later) - 1 : 32) - lane;
-                prefetch_l2(p.pool + (int64_t)(slot[i] - len + 1) * kDim, len * kDim * 2);
-              }
-            }
-          }
         }
       }
     } else {
@@ -563,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kOutWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------------------- softmax
-    // S holds head 16 quad + i on TMEM lane 32 quad + i (i < 16).  The 16x256b load gives thread
-    // (g8 = lane / 4, e = lane % 4) the heads hA = 16 quad + g8 and hB = hA + 8 and, of each, the
-    // columns 8 k + 2 e + {0, 1}, k = 0..7: a head's 64 logits are spread over 4 threads.
-    const int quad = warp & 3;
+    // S holds head 16 quad + i on TMEM lane 32 quad + i (i < 16).  A warp takes half of the chunk's rows; the 16x256b
+    // load gives thread (g8 = lane / 4, e = lane % 4) the heads hA = 16 quad + g8 and hB = hA + 8 and, of each, the
+    // columns r0 + 8 k + 2 e + {0, 1}, k = 0..3: a head's 64 logits are spread over 4 threads of two warps.
+    const int quad = warp & 3, half = (warp - kSoftWarp) >> 2, r0 = 32 * half;
     const int g8 = lane >> 2, e = lane & 3;
     const int hA = 16 * quad + g8, hB = hA + 8;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
@@ -575,17 +574,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float cap2 = p.cap * kLog2e, in_cap = capped ? 2.f * kLog2e * (p.scale / p.cap) : 0.f;
     const float slopeA = sloped ? p.slopes[hA] * kLog2e : 0.f, slopeB = sloped ? p.slopes[hB] * kLog2e : 0.f;
     uint32_t g = 0, item = 0;
-    // a wait that gave up is acted on where the four warps meet, so that they leave together
+    // a wait that gave up is acted on where the eight warps meet, so that they leave together
     bool ok = true, leave = false;
     for (Walk w(rows_s, start); w.left > 0 && !leave; w.next(), ++item) {
-      float oA = kNone, oB = kNone;                  // offsets
-      float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of the weights, and of the rounded ones
+      float oA = kNone, oB = kNone;                  // offsets, the same in both warps of a head
+      float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of this thread's weights, and of the rounded ones
       const bool begun = p.other != nullptr && w.c0 == 0;
       if (begun) {
         const float a = __ldg(p.other_lse + (int64_t)w.t * kHq + hA), b = __ldg(p.other_lse + (int64_t)w.t * kHq + hB);
         oA = first_offset(a);
         oB = first_offset(b);
-        if (e == 0) {
+        if (e == 0 && half == 0) {
           lA = rA = first_weight(a);
           lB = rB = first_weight(b);
         }
@@ -595,9 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = g & 1;
         ok = ok && wait_bar_warp(&sfull[b], (g >> 1) & 1, p.status, 111);
         tc_fence_after();
-        float x[32];
-        tmem_ld_16x256b_x8(tmem + t_lane + b * kHq, x);
-        const uint2 live = *reinterpret_cast<const uint2*>(mask_s + (g % kMaskRing) * 2);
+        float x[16];
+        tmem_ld_16x256b_x4(tmem + t_lane + b * kHq + r0, x);
+        const uint32_t live = mask_s[(g % kMaskRing) * 2 + half] >> (2 * e);
         const int ahead = ahead_s[g % kMaskRing];
         tc_wait_ld();
         tc_fence_before();
@@ -606,15 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // logits in log2 units
         if (capped) {  // tanh y = 1 - 2 / (e^2y + 1)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = fmaf(-2.f * cap2, rcp_approx(ex2_approx(x[i] * in_cap) + 1.f), cap2);
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.f * cap2, rcp_approx(ex2_approx(x[i] * in_cap) + 1.f), cap2);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] *= scale2;
+          for (int i = 0; i < 16; ++i) x[i] *= scale2;
         }
         if (sloped) {  // e - 1 - r of row r = hi - 1 - list index
-          const int d0 = ahead + c * kRows + 2 * e;
+          const int d0 = ahead + c * kRows + r0 + 2 * e;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const float near = fabsf((float)(d0 + 8 * k)), far = fabsf((float)(d0 + 8 * k + 1));
             x[4 * k] = fmaf(-slopeA, near, x[4 * k]);
             x[4 * k + 1] = fmaf(-slopeA, far, x[4 * k + 1]);
@@ -622,104 +621,127 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[4 * k + 3] = fmaf(-slopeB, far, x[4 * k + 3]);
           }
         }
-        if ((live.x & live.y) != 0xffffffffu) {
-          const uint32_t v0 = live.x >> (2 * e), v1 = live.y >> (2 * e);
+        if ((live & 0x03030303u) != 0x03030303u) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t bits = (k < 4 ? v0 : v1) >> (8 * (k & 3));
-            if (!(bits & 1u)) x[4 * k] = x[4 * k + 2] = -INFINITY;
-            if (!(bits & 2u)) x[4 * k + 1] = x[4 * k + 3] = -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            if (!(live >> (8 * k) & 1u)) x[4 * k] = x[4 * k + 2] = -INFINITY;
+            if (!(live >> (8 * k) & 2u)) x[4 * k + 1] = x[4 * k + 3] = -INFINITY;
           }
         }
-        float mxA = -INFINITY, mxB = -INFINITY;
+        float mxA = fmaxf(x[0], x[1]), mxB = fmaxf(x[2], x[3]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 1; k < 4; ++k) {
           mxA = fmaxf(mxA, fmaxf(x[4 * k], x[4 * k + 1]));
           mxB = fmaxf(mxB, fmaxf(x[4 * k + 2], x[4 * k + 3]));
         }
-        mxA = fmaxf(mxA, __shfl_xor_sync(0xffffffffu, mxA, 1));
-        mxB = fmaxf(mxB, __shfl_xor_sync(0xffffffffu, mxB, 1));
-        mxA = fmaxf(mxA, __shfl_xor_sync(0xffffffffu, mxA, 2));
-        mxB = fmaxf(mxB, __shfl_xor_sync(0xffffffffu, mxB, 2));
-        float aA = 1.f, aB = 1.f;
-        if (mxA - oA > kRescale + kWeightLog2) {
-          aA = ex2_approx(oA - (mxA - kWeightLog2));
-          oA = mxA - kWeightLog2;
-        }
-        if (mxB - oB > kRescale + kWeightLog2) {
-          aB = ex2_approx(oB - (mxB - kWeightLog2));
-          oB = mxB - kWeightLog2;
-        }
         // Whether any head's maximum moves is said now and asked for when the weights are ready (the same answer in
-        // all four warps: a later chunk's word is written after all have read this one's).  Before an item's first
-        // product there is nothing to move, unless its sums have begun.
-        const bool moved = __any_sync(0xffffffffu, ((aA != 1.f || aB != 1.f) && (c > w.c0 || begun)) || !ok);
+        // all eight warps: a later chunk's word is written after all have read this one's).  An item's first chunk
+        // asks at once: without sums that have begun there is no offset yet.
+        const bool moved = __any_sync(0xffffffffu, mxA - oA > kRescale + kWeightLog2 || mxB - oB > kRescale + kWeightLog2 || !ok);
         if (lane == 0) {
           if (moved) *const_cast<volatile int*>(start + 3) = (int)(g + 1);
           mbar_arrive(&looked[b]);
         }
-        lA *= aA;
-        rA *= aA;
-        lB *= aB;
-        rB *= aB;
+        uint32_t pkA[4], pkB[4];
+        float sA, sB;
         // weights 2^(x - offset), rounded for the product
-        uint32_t pkA[8], pkB[8];
+        auto weigh = [&]() {
+          sA = sB = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float a0 = ex2_approx(x[4 * k] - oA), a1 = ex2_approx(x[4 * k + 1] - oA);
-          const float b0 = ex2_approx(x[4 * k + 2] - oB), b1 = ex2_approx(x[4 * k + 3] - oB);
-          lA += a0 + a1;
-          lB += b0 + b1;
-          pkA[k] = pack16<kBf16>(a0, a1);
-          pkB[k] = pack16<kBf16>(b0, b1);
-          add_pair<kBf16>(rA, pkA[k]);
-          add_pair<kBf16>(rB, pkB[k]);
-        }
+          for (int k = 0; k < 4; ++k) {
+            const float a0 = ex2_approx(x[4 * k] - oA), a1 = ex2_approx(x[4 * k + 1] - oA);
+            const float b0 = ex2_approx(x[4 * k + 2] - oB), b1 = ex2_approx(x[4 * k + 3] - oB);
+            sA += a0 + a1;
+            sB += b0 + b1;
+            pkA[k] = pack16<kBf16>(a0, a1);
+            pkB[k] = pack16<kBf16>(b0, b1);
+          }
+        };
+        const bool fresh = c == w.c0 && !begun;
+        if (!fresh) weigh();
         ok = ok && wait_bar_warp(&looked[b], (g >> 1) & 1, p.status, 110);
         if (*const_cast<volatile int*>(start + 3) == (int)(g + 1)) {
           leave = named_or(kSoftBar, 32 * kSoftWarps, !ok);
           if (leave) break;
-          if (e == 0) {
-            alpha_s[hA] = aA;
-            alpha_s[hB] = aB;
-          }
-          named_sync(kSoftBar, 32 * kSoftWarps);
-          // O^T must hold all of the previous chunk, or what the sums begin with, before its columns are rescaled
-          if (c > w.c0) {
-            const uint32_t prev = g - 1;
-            ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 112);
-          } else {
-            for (int db = 0; db < kPairs; ++db)
-              ok = ok && wait_bar_warp(&oready[oslot(item, db)], ophase(item, db), p.status, 116);
-          }
-          tc_fence_after();
-#pragma unroll 1
-          for (int q2 = 0; q2 < 2 * kPairs; ++q2) {  // 4 quarters x 2 halves of 32 heads
-            float v[32];
-            const uint32_t ta = tmem + t_lane + kColO + oslot(item, q2 >> 1) * kHq + (q2 & 1) * 32;
-            tmem_ld32(ta, v);
-            tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= alpha_s[(q2 & 1) * 32 + i];
-            tmem_st32(ta, v);
+          for (int d = 1; d <= 2; d <<= 1) {
+            mxA = fmaxf(mxA, __shfl_xor_sync(0xffffffffu, mxA, d));
+            mxB = fmaxf(mxB, __shfl_xor_sync(0xffffffffu, mxB, d));
           }
-          tc_wait_st();
+          if (e == 0) {
+            max_s[half * kHq + hA] = mxA;
+            max_s[half * kHq + hB] = mxB;
+          }
           named_sync(kSoftBar, 32 * kSoftWarps);
+          // the factor of what head h has so far, from the offset it had, and its new offset
+          auto raise = [&](int h, float& o) {
+            const float mx = fmaxf(max_s[h], max_s[kHq + h]);
+            const bool up = mx - o > kRescale + kWeightLog2;
+            const float f = up ? ex2_approx(o - (mx - kWeightLog2)) : 1.f;
+            if (up) o = mx - kWeightLog2;
+            return f;
+          };
+          const float aA = raise(hA, oA), aB = raise(hB, oB);
+          lA *= aA;
+          rA *= aA;
+          lB *= aB;
+          rB *= aB;
+          if (!fresh) {
+            named_sync(kSoftBar, 32 * kSoftWarps);  // the maxima are read: their place takes the factors
+            if (e == 0 && half == 0) {
+              max_s[hA] = aA;
+              max_s[hB] = aB;
+            }
+            named_sync(kSoftBar, 32 * kSoftWarps);
+            // O^T must hold all of the previous chunk, or what the sums begin with, before its columns are rescaled
+            if (c > w.c0) {
+              const uint32_t prev = g - 1;
+              ok = wait_bar_warp(&pempty[prev & 1], (prev >> 1) & 1, p.status, 112);
+            } else {
+              for (int db = 0; db < kPairs; ++db)
+                ok = ok && wait_bar_warp(&oready[oslot(item, db)], ophase(item, db), p.status, 116);
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 2 * kPairs; ++q) {  // the quarters of this half of the heads, 16 at a time
+              float v[16];
+              const int h0 = r0 + 16 * (q & 1);
+              const uint32_t ta = tmem + t_lane + kColO + oslot(item, q >> 1) * kHq + h0;
+              tmem_ld16(ta, v);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= max_s[h0 + i];
+              tmem_st16(ta, v);
+            }
+            tc_wait_st();
+          }
+          named_sync(kSoftBar, 32 * kSoftWarps);
+          weigh();
+        } else if (fresh) {
+          weigh();  // no row at all
         }
+        lA += sA;
+        lB += sB;
         ok = ok && wait_bar_warp(&pempty[b], ((g >> 1) & 1) ^ 1, p.status, 113);
         {
           // P[h][j], K-major with the 128-byte swizzle: 16-byte chunk k of line h at (k ^ (h & 7)); hA and hB alike
           uint8_t* line = sp + b * kPBytes + hA * 128 + 4 * e;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            *reinterpret_cast<uint32_t*>(line + ((k ^ g8) << 4)) = pkA[k];
-            *reinterpret_cast<uint32_t*>(line + ((k ^ g8) << 4) + 1024) = pkB[k];
+          for (int k = 0; k < 4; ++k) {
+            uint8_t* to = line + (((4 * half + k) ^ g8) << 4);
+            *reinterpret_cast<uint32_t*>(to) = pkA[k];
+            *reinterpret_cast<uint32_t*>(to + 1024) = pkB[k];
           }
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[b]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          add_pair<kBf16>(rA, pkA[k]);
+          add_pair<kBf16>(rB, pkB[k]);
+        }
       }
       if (leave) break;
 #pragma unroll
@@ -732,13 +754,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the statistics of this item's parity were last read by the output of item - 2
       ok = ok && wait_bar_warp(&lfree[item & 1], ((item >> 1) & 1) ^ 1, p.status, 109);
       if (e == 0) {
-        float* st = stat_s + (item & 1) * 3 * kHq;
+        float* st = stat_s + (item & 1) * 5 * kHq + half * kHq;
         st[hA] = rA;
-        st[kHq + hA] = lA;
-        st[2 * kHq + hA] = oA;
+        st[2 * kHq + hA] = lA;
         st[hB] = rB;
-        st[kHq + hB] = lB;
-        st[2 * kHq + hB] = oB;
+        st[2 * kHq + hB] = lB;
+        if (half == 0) {
+          st[4 * kHq + hA] = oA;
+          st[4 * kHq + hB] = oB;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&lready[item & 1]);
@@ -802,8 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the factors of the item before are read by all
       if (!named_and(kOutBar, 32 * kOutWarps, ok)) break;
       if (to < kHq) {
-        const float* st = stat_s + par * 3 * kHq + to;
-        float r = st[0], l = st[kHq], m = st[2 * kHq];
+        const float* st = stat_s + par * 5 * kHq + to;
+        float r = st[0] + st[kHq], l = st[2 * kHq] + st[3 * kHq], m = st[4 * kHq];
         float f0 = 0.f, fi = 1.f;
         if (joins) {
           const float m0 = begins ? kNone : so_far[to], mi = m;
@@ -1024,7 +1048,6 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.scale = a.scale;
   p.cap = a.cap;
-  p.fetch_ahead = 0;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.parts_of = reinterpret_cast<int4*>(ws);
   for (int t0 = 0; t0 < a.T; t0 += kTokens) {  // launches on one stream: they may share the workspace
