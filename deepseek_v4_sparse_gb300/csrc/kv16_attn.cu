@@ -34,6 +34,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "ds4x_internal.h"
 #include "ds4x_ptx.cuh"
 
@@ -157,8 +159,12 @@ __device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint32_t b, ui
         "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"(add)
         : "memory");
 }
+template <int kDst, int kSrc>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc) : "memory");
+}
 template <int kDst>
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(kDst)
                : "memory");
 }
@@ -414,27 +420,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&slempty[g % kRing]);
-        const bool all = __all_sync(0xffffffffu, there == 0xffu);
-#pragma unroll 1
-        for (int pr = 0; pr < kPairs && ok; ++pr) {
-          ok = wait_bar_warp(&kvempty[b * kPairs + pr], ((g >> 1) & 1) ^ 1, p.status, 101);
-          if (mine && ok) {
-            const uint32_t to = b * kBufBytes + pr * 2 * kSlotBytes;
-            if (all) {
+        const uint32_t par = ((g >> 1) & 1) ^ 1;
+        uint64_t *full = kvfull + b * kPairs, *empty = kvempty + b * kPairs;
+        if (__all_sync(0xffffffffu, mine && there == 0xffu)) {
+          uint32_t to[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[i] = dst[i] + b * kBufBytes;
+          auto quarter = [&](auto n) {
+            constexpr int kN = decltype(n)::value, kTo = kN * 2 * kSlotBytes;
+            ok = ok && wait_bar_warp(&empty[kN], par, p.status, 101);
+            if (ok) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                cp_async16<0>(dst[i] + to, src[i] + pr * 256, 16);
-                cp_async16<1024>(dst[i] + to, src[i + 4] + pr * 256, 16);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                cp_async16<0>(dst[i] + to, src[i] + pr * 256, (there >> i & 1u) << 4);
-                cp_async16<1024>(dst[i] + to, src[i + 4] + pr * 256, (there >> (i + 4) & 1u) << 4);
+                cp_async16<kTo, kN * 256>(to[i], src[i]);
+                cp_async16<kTo + 1024, kN * 256>(to[i], src[i + 4]);
               }
             }
+            cp_async_arrive(&full[kN]);
+          };
+          quarter(std::integral_constant<int, 0>());
+          quarter(std::integral_constant<int, 1>());
+          quarter(std::integral_constant<int, 2>());
+          quarter(std::integral_constant<int, 3>());
+        } else {
+#pragma unroll 1
+          for (int pr = 0; pr < kPairs; ++pr) {
+            ok = ok && wait_bar_warp(&empty[pr], par, p.status, 118);
+            if (mine && ok) {
+              const uint32_t to = b * kBufBytes + pr * 2 * kSlotBytes;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                cp_async16_or_zero<0>(dst[i] + to, src[i] + pr * 256, (there >> i & 1u) << 4);
+                cp_async16_or_zero<1024>(dst[i] + to, src[i + 4] + pr * 256, (there >> (i + 4) & 1u) << 4);
+              }
+            }
+            cp_async_arrive(&full[pr]);
           }
-          cp_async_arrive(&kvfull[b * kPairs + pr]);
         }
       }
     }
