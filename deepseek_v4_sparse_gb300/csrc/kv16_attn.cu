@@ -361,20 +361,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long quota = total >> 31 ? (total + gridDim.x - 1) / gridDim.x
                                         : (long long)(((uint32_t)total + gridDim.x - 1u) / gridDim.x);
     const long long g0 = quota * blockIdx.x, g1 = min(total, g0 + quota);
-    // the block's first chunk, and how many chunks lie before its first and its last unit
+    // The block's first chunk, and how many chunks lie before its first and its last unit.  A boundary that falls into
+    // a short token (a few chunks, or an eighth of a block's) moves to the token's nearer end: to join parts costs more.
     long long at = before, chunks = before - (long long)min(first, p.T) * own;
 #pragma unroll 1
     for (int t = first; t < last; ++t) {
-      const int nch = chunks_of(rows_s[t]);
-      if (at <= g0 && g0 < at + own + nch) {
-        const int c0 = (int)max(g0 - at - own, 0ll);
-        start[0] = t;
-        start[1] = c0;
+      const int nch = chunks_of(rows_s[t]), units = own + nch;
+      auto chunk_at = [&](long long unit) {  // of this token's, at a unit of its
+        if (2 * (long long)nch <= quota && (nch <= 8 || 8 * (long long)nch <= quota)) return 2 * unit > units ? nch : 0;
+        return (int)max(unit - own, 0ll);
+      };
+      if (at <= g0 && g0 < at + units) {
+        const int c0 = chunk_at(g0 - at);
+        const bool over = c0 == nch;
         scan[kWarps] = chunks + c0;
-        if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(t, c0, nch, (int)quota);
+        start[0] = t + over;
+        start[1] = over ? 0 : c0;
+        if (p.parts_of) p.parts_of[blockIdx.x] = make_int4(t + over, over ? 0 : c0, nch, (int)quota);
       }
-      if (g0 < total && at < g1 && g1 <= at + own + nch) scan[kWarps + 1] = chunks + max(g1 - at - own, 0ll);
-      at += own + nch;
+      if (g0 < total && at < g1 && g1 <= at + units) scan[kWarps + 1] = chunks + (g1 == at + units ? nch : chunk_at(g1 - at));
+      at += units;
       chunks += nch;
     }
     if (g0 >= total && tid == 0) {

@@ -338,6 +338,29 @@ def test_attn_masks_that_meet(dtype):
         check_attn(q, pool, out, lse, dtype, SCALE, opts, some, tokens=range(0, T, 3))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("ps", [4, 8, 16, 32, 64, 512])
+def test_attn_long_lists(ps, dtype):
+    """Lists long enough to be cut at multiples of 64 rows, that begin and end anywhere, in pages of any size; rows
+    whose pages are gone; the same lists a row too short for it."""
+    rng = np.random.default_rng(ps)
+    rows = [1500, 700, 1024]
+    pool = Pool(rng, rows, ps, dtype, gone=[0, 130, 0])
+    pool.tables[2, 300 // ps] = -1
+    pool.dev = pool.dev[0], i32(pool.tables), pool.dev[2]
+    req = np.array([0, 0, 0, 0, 0, 1, 1, 1, 2, 2, 2])
+    pos = np.array([1499, 1023, 1024, 511, 510, 699, 650, 1400, 1023, 1022, 1000])
+    first = np.array([0, 1, 513, 0, 0, 60, 139, 0, 0, 511, 128])
+    q = queries(rng, len(req), dtype)
+    for opts in ({}, options(rng, len(req), dtype, slopes=True, cap=True, other=True)):
+        lists = dict(req=req, positions=pos, first=first)
+        out, lse = run_attn(q, pool, opts, lists)
+        check_attn(q, pool, out, lse, dtype, SCALE, opts, lists)
+    lists = dict(req=req, positions=pos, first=first, prefix=np.array([600, 0, 0]), window=620)
+    out, lse = run_attn(q, pool, {}, lists)
+    check_attn(q, pool, out, lse, dtype, SCALE, {}, lists)
+
+
 @pytest.mark.parametrize("ratio", [4, 128])
 def test_attn_pooled_rows(ratio):
     """Rows of several positions each: the ratio of the pooled rows."""
