@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* lfree = lready + 2;             // [item parity] ... and read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmemSlot);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp's number through a warp reduction: a branch on it is then known not to divide a warp, and the products of
+  // the issuing warps take five instructions each instead of fifty
+  const int tid = threadIdx.x, warp = Walk::uniform(tid >> 5), lane = tid & 31;
   // use u = 4 item + quarter of an O^T slot: the slot is u % 6, and this is the slot's (u / 6)-th use
   auto oslot = [](uint32_t item, int db) { return (int)((4u * item + (uint32_t)db) % kOSlots); };
   auto ophase = [](uint32_t item, int db) { return ((4u * item + (uint32_t)db) / kOSlots) & 1u; };
@@ -409,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const char* pool = reinterpret_cast<const char*>(p.pool) + piece * 16;
     uint32_t g = 0;
     bool ok = true;
+#pragma unroll 1
     for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
 #pragma unroll 1
       for (int c = w.c0; c < w.c1 && ok; ++c, ++g) {
@@ -473,28 +476,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, item = 0;
       bool ok = true;
       const uint32_t q_lo = (uint32_t)desc_sw128(smem_u32(sq), 16, 1024), k_lo = (uint32_t)desc_sw128(smem_u32(skv), 16, 1024);
+#pragma unroll 1
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
+#pragma unroll 1
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
           const int b = g & 1;
           if (!wait_bar_warp(&sempty[b], ((g >> 1) & 1) ^ 1, p.status, 102)) { ok = false; break; }
           if (c == w.c0 && !wait_bar_warp(qfull, item & 1, p.status, 103)) { ok = false; break; }
-#pragma unroll 1
+          const uint32_t k = k_lo + (b * kBufBytes >> 4), d = tmem + b * kHq;
+#pragma unroll
           for (int pr = 0; pr < kPairs; ++pr) {
-            if (!wait_bar_warp(&kvfull[b * kPairs + pr], (g >> 1) & 1, p.status, 104)) { ok = false; break; }
+            ok = ok && wait_bar_warp(&kvfull[b * kPairs + pr], (g >> 1) & 1, p.status, 104);
             fence_proxy_async();  // copied rows -> visible to the tensor core
             tc_fence_after();
-            const uint32_t a = q_lo + pr * (2 * kQBlockBytes >> 4), k = k_lo + (b * kBufBytes + pr * 2 * kSlotBytes >> 4);
-            mma_elect<false>(tmem + b * kHq, a, k, kIdescS, pr);
+            // the arrival of this warp hands on what it waited for (the chunk's mask)
+            if (pr == kPairs - 1 && lane == 0) mbar_arrive(&sfull[b]);
+            __syncwarp();
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-              mma_elect<true>(tmem + b * kHq, a + ((i >> 2) * kQBlockBytes + (i & 3) * 32 >> 4),
-                              k + ((i >> 2) * kSlotBytes + (i & 3) * 32 >> 4), kIdescS, 1);
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t qa = q_lo + ((2 * pr + (i >> 2)) * kQBlockBytes + (i & 3) * 32 >> 4);
+              const uint32_t ka = k + ((2 * pr + (i >> 2)) * kSlotBytes + (i & 3) * 32 >> 4);
+              if (pr + i == 0) mma_elect<false>(d, qa, ka, kIdescS, 0);
+              else mma_elect<true>(d, qa, ka, kIdescS, 1);
+            }
           }
           if (!ok) break;
-          if (c == w.c1 - 1) tc_commit_elect(qempty);  // the next item's q may replace this one's
-          // the arrival of this warp hands on what it waited for (the chunk's mask)
-          if (lane == 0) mbar_arrive(&sfull[b]);
           tc_commit_elect(&sfull[b]);
+          if (c == w.c1 - 1) tc_commit_elect(qempty);  // the next item's q may replace this one's
         }
       }
     } else if (warp == kOWarp) {
@@ -502,12 +510,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0, item = 0;
       bool ok = true;
       const uint32_t v_lo = (uint32_t)desc_sw128(smem_u32(skv), kSlotBytes, 1024), p_lo = (uint32_t)desc_sw128(smem_u32(sp), 16, 1024);
+#pragma unroll 1
       for (Walk w(rows_s, start); __all_sync(0xffffffffu, w.left > 0 && ok); w.next(), ++item) {
         const int begun = p.other != nullptr && w.c0 == 0;  // the slots hold what the sums begin with
+        uint32_t d[kPairs];
+#pragma unroll
+        for (int db = 0; db < kPairs; ++db) d[db] = Walk::uniform(tmem + kColO + oslot(item, db) * kHq);
+#pragma unroll 1
         for (int c = w.c0; __all_sync(0xffffffffu, c < w.c1); ++c, ++g) {
           const int b = g & 1, steps = w.steps(c);
+          const uint32_t v = v_lo + (b * kBufBytes >> 4), k = p_lo + (b * kPBytes >> 4);
+          const bool plain = __all_sync(0xffffffffu, c > w.c0 && c < w.c1 - 1 && steps == kRows / 16);
           if (!wait_bar_warp(&pfull[b], (g >> 1) & 1, p.status, 105)) { ok = false; break; }
           tc_fence_after();
+          if (plain) {  // neither an item's first chunk nor its last, and full: straight through
+#pragma unroll
+            for (int db = 0; db < kPairs; ++db) {
+#pragma unroll
+              for (int ks = 0; ks < kRows / 16; ++ks)
+                mma_elect<true>(d[db], v + (2 * db * kSlotBytes + ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
+              tc_commit_elect(&kvempty[b * kPairs + db]);  // this quarter of the chunk is free
+            }
+            tc_commit_elect(&pempty[b]);
+            continue;
+          }
 #pragma unroll 1
           for (int db = 0; db < kPairs; ++db) {
             const int os = oslot(item, db);
@@ -515,18 +541,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!wait_bar_warp(&oready[os], ophase(item, db), p.status, 106)) { ok = false; break; }
               tc_fence_after();
             }
-            const uint32_t a = v_lo + (b * kBufBytes + 2 * db * kSlotBytes >> 4), k = p_lo + (b * kPBytes >> 4);
-            const uint32_t d = tmem + kColO + os * kHq;
-            mma_elect<false>(d, a, k, kIdescO, (uint32_t)((c > w.c0) | begun));
+            const uint32_t a = v + (2 * db * kSlotBytes >> 4), to = tmem + kColO + os * kHq;
+            mma_elect<false>(to, a, k, kIdescO, (uint32_t)((c > w.c0) | begun));
             if (__all_sync(0xffffffffu, steps == kRows / 16)) {
 #pragma unroll
-              for (int ks = 1; ks < kRows / 16; ++ks) mma_elect<true>(d, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
+              for (int ks = 1; ks < kRows / 16; ++ks) mma_elect<true>(to, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             } else {
 #pragma unroll 1
               for (int ks = 1; __all_sync(0xffffffffu, ks < steps); ++ks)
-                mma_elect<true>(d, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
+                mma_elect<true>(to, a + (ks * 2048 >> 4), k + 2 * ks, kIdescO, 1);
             }
-            tc_commit_elect(&kvempty[b * kPairs + db]);  // this quarter of the chunk is free
+            tc_commit_elect(&kvempty[b * kPairs + db]);
             if (c == w.c1 - 1) tc_commit_elect(&ofull[os]);
           }
           if (!ok) break;
@@ -537,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------------------------------- slots of the rows, a few chunks ahead
       uint32_t g = 0;
       bool ok = true;
+#pragma unroll 1
       for (Walk w(rows_s, start); w.left > 0 && ok; w.next()) {
         const Span s = span_of(p, w.t);
         const int32_t* table = p.tables + (int64_t)(w.n > 0 ? s.b : 0) * p.max_pages;
@@ -573,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------------------ q
       uint32_t item = 0;
       bool ok = true;
+#pragma unroll 1
       for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
         ok = wait_bar_warp(qempty, (item & 1) ^ 1, p.status, 108);
         if (!ok) break;
@@ -603,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0, item = 0;
     // a wait that gave up is acted on where the eight warps meet, so that they leave together
     bool ok = true, leave = false;
+#pragma unroll 1
     for (Walk w(rows_s, start); w.left > 0 && !leave; w.next(), ++item) {
       float oA = kNone, oB = kNone;                  // offsets, the same in both warps of a head
       float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums of this thread's weights, and of the rounded ones
@@ -749,9 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         lA += sA;
         lB += sB;
-        ok = ok && wait_bar_warp(&pempty[b], ((g >> 1) & 1) ^ 1, p.status, 113);
         {
-          // P[h][j], K-major with the 128-byte swizzle: 16-byte chunk k of line h at (k ^ (h & 7)); hA and hB alike
+          // P's buffer is free: S of this chunk needed rows that were copied over those of two chunks ago, when O^T had
+          // taken all of them and their weights.  P[h][j], K-major with the 128-byte swizzle: 16-byte chunk k of line h at (k ^ (h & 7)); hA and hB alike
           uint8_t* line = sp + b * kPBytes + hA * 128 + 4 * e;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -837,6 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ready(0, db, begun);
       }
     }
+#pragma unroll 1
     while (w.left > 0) {
       const int par = item & 1;
       // chunks before the block, or behind it: the sums go to the block's first or second part
