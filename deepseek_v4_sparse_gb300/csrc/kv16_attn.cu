@@ -75,9 +75,10 @@ constexpr int kOffAhead = kOffMask + kMaskRing * 8;    // int[kMaskRing]: e - hi
 // float[2 items][2 halves of the rows' sums of rounded weights, 2 halves' sums, offset][64]
 constexpr int kOffStat = kOffAhead + kMaskRing * 4;
 constexpr int kOffMax = kOffStat + 2 * 5 * kHq * 4;    // float[2 halves of the rows][64]: maxima of one chunk
-constexpr int kOffJoin = kOffMax + 2 * kHq * 4;    // float[6][64]: a token's offset, sum of rounded weights and sum so far; factors
-                                                 // of the sums so far, of the item's, and of the next token's other output
-constexpr int kOffScan = kOffJoin + 6 * kHq * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
+constexpr int kOutHeads = 16;                    // heads of an output warp
+constexpr int kOffJoin = kOffMax + 2 * kHq * 4;    // float[output warps][3][kOutHeads]: factors of a token's sums so far, of an
+                                                 // item's sums, and of the next token's other output
+constexpr int kOffScan = kOffJoin + kOutWarps * 3 * kOutHeads * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
                                                  // then int[4]: the block's part, and the last chunk (+ 1) in which a
                                                  // maximum moved
 constexpr int kOffBars = kOffScan + (kWarps + 2) * 8 + 16;
@@ -91,7 +92,7 @@ constexpr float kWeightLog2 = 4.0f;
 // numbers or infinities, and 2^(x - kNone) is 0 for the -infinity of a masked row.
 constexpr float kNone = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kSoftBar = 1, kOutBar = 2;
+constexpr int kSoftBar = 1;
 constexpr int kPartFloats = kHq * kDim;          // unnormalised sums of a part, then its statistics
 constexpr int kStatFloats = 3 * kHq;             // sum of rounded weights, sum, offset
 
@@ -825,26 +826,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // --------------------------------------------------------------------------- output
-    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 4, to = tid - 32 * kOutWarp;
+    // heads hb .. + 15 and dims 32 quad + lane of each quarter; the warp's first 16 lanes do a head's arithmetic
+    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 4;
+    const bool odd = lane & 1, has_head = lane < kOutHeads;
+    const int head = hb + (lane & (kOutHeads - 1));
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
     const int at0 = hb * kDim + quad * 32 + lane;  // this thread's first head and dim of a quarter, within a token
-    float *so_far = join_s, *f_first = join_s + 3 * kHq, *f_item = join_s + 4 * kHq, *f_other = join_s + 5 * kHq;
+    float* f_first = join_s + (warp - kOutWarp) * 3 * kOutHeads;
+    float *f_item = f_first + kOutHeads, *f_other = f_item + kOutHeads;
+    float m_far = kNone, r_far = 0.f, l_far = 0.f;  // a token's offset and sums so far
     uint32_t item = 0;
     bool ok = true;
     int from = 0;       // the block's first chunk of the token
-    uint16_t theirs[16];
-    // the other attention's output of token t at this thread's dim of quarter db, where it counts
-    auto load_other = [&](int t, int db) {
-      const uint16_t* src = p.other + (int64_t)t * kHq * kDim + db * 128 + at0;
+    uint32_t theirs[8], after[8];
+    // The other attention's output of token t, quarter db: an even lane the even heads at its dim and the next, an odd
+    // one the odd heads at the dim before and its own; neighbours exchange.
+    auto load_other = [&](int t, int db, uint32_t (&u)[8]) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.other + (int64_t)t * kHq * kDim + db * 128 + at0 - odd + (odd ? kDim : 0));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) theirs[i] = f_other[hb + i] == 0.f ? 0 : __ldg(src + i * kDim);
+      for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i * kDim);
     };
     // slot of quarter db of item n is empty; with another attention to join its sums begin with that
     auto ready = [&](uint32_t n, int db, bool begun) {
       if (begun) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = f_other[hb + i] * from16<kBf16>(theirs[i]);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t pair = __byte_perm(theirs[i], __shfl_xor_sync(0xffffffffu, theirs[i], 1), odd ? 0x3276u : 0x5410u);
+          const float2 f = *reinterpret_cast<const float2*>(f_other + 2 * i);
+          v[2 * i] = f.x == 0.f ? 0.f : f.x * from16<kBf16>((uint16_t)pair);
+          v[2 * i + 1] = f.y == 0.f ? 0.f : f.y * from16<kBf16>((uint16_t)(pair >> 16));
+        }
         tmem_st16(t_lane + oslot(n, db) * kHq, v);
         tc_wait_st();
       }
@@ -856,12 +868,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const bool begun = w.left > 0 && p.other && w.c0 == 0;
       if (begun) {
-        if (to < kHq) f_other[to] = first_weight(p.other_lse[(int64_t)w.t * kHq + to]);
-        named_sync(kOutBar, 32 * kOutWarps);
+        load_other(w.t, 0, after);
+        if (has_head) f_other[lane] = first_weight(__ldg(p.other_lse + (int64_t)w.t * kHq + head));
+        __syncwarp();
       }
 #pragma unroll 1
       for (int db = 0; db < kPairs; ++db) {
-        if (begun) load_other(w.t, db);
+        if (begun) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) theirs[i] = after[i];
+          if (db + 1 < kPairs) load_other(w.t, db + 1, after);
+        }
         ready(0, db, begun);
       }
     }
@@ -877,46 +894,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = w.t;
       w.next();
       const bool more = w.left > 0, begun = more && p.other && w.c0 == 0;  // the next item
-      const float next_lse = begun && to < kHq ? __ldg(p.other_lse + (int64_t)w.t * kHq + to) : 0.f;
+      float next_lse = 0.f;
+      if (begun) {
+        load_other(w.t, 0, after);
+        next_lse = __ldg(p.other_lse + (int64_t)w.t * kHq + head);
+      }
+      const float sink2 = whole && p.sinks ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
       ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
-      // the factors of the item before are read by all
-      if (!named_and(kOutBar, 32 * kOutWarps, ok)) break;
-      if (to < kHq) {
-        const float* st = stat_s + par * 5 * kHq + to;
+      if (!ok) break;
+      if (has_head) {
+        const float* st = stat_s + par * 5 * kHq + head;
         float r = st[0] + st[kHq], l = st[2 * kHq] + st[3 * kHq], m = st[4 * kHq];
         float f0 = 0.f, fi = 1.f;
         if (joins) {
-          const float m0 = begins ? kNone : so_far[to], mi = m;
+          const float m0 = begins ? kNone : m_far, mi = m;
           m = fmaxf(m0, mi);
           f0 = begins ? 0.f : ex2_approx(m0 - m);
           fi = ex2_approx(mi - m);
-          r = r * fi + (begins ? 0.f : so_far[kHq + to] * f0);
-          l = l * fi + (begins ? 0.f : so_far[2 * kHq + to] * f0);
-          so_far[to] = m;
-          so_far[kHq + to] = r;
-          so_far[2 * kHq + to] = l;
+          r_far = r = r * fi + (begins ? 0.f : r_far * f0);
+          l_far = l = l * fi + (begins ? 0.f : l_far * f0);
+          m_far = m;
         }
         if (whole) {
-          const Joined j = join_head(m, r, l, p.sinks ? p.sinks[to] * kLog2e : -INFINITY);
-          if (p.lse) p.lse[(int64_t)t * kHq + to] = j.lse;
+          const Joined j = join_head(m, r, l, sink2);
+          if (quad == 0 && p.lse) p.lse[(int64_t)t * kHq + head] = j.lse;
           f0 *= j.own;
           fi *= j.own;
-        } else if (ends) {
-          float* ps = p.stat + part * kStatFloats;
-          ps[to] = r;
-          ps[kHq + to] = l;
-          ps[2 * kHq + to] = m;
+        } else if (quad == 0 && ends) {
+          float* ps = p.stat + part * kStatFloats + head;
+          ps[0] = r;
+          ps[kHq] = l;
+          ps[2 * kHq] = m;
         }
-        f_first[to] = f0;
-        f_item[to] = fi;
-        if (begun) f_other[to] = first_weight(next_lse);
+        f_first[lane] = f0;
+        f_item[lane] = fi;
+        if (begun) f_other[lane] = first_weight(next_lse);
       }
-      named_sync(kOutBar, 32 * kOutWarps);
+      __syncwarp();
       if (lane == 0) mbar_arrive(&lfree[par]);
 #pragma unroll 1
       for (int db = 0; db < kPairs; ++db) {
         const int os = oslot(item, db);
-        if (begun) load_other(w.t, db);  // on its way while this quarter goes out
+        if (begun) {  // the next quarter's is on its way while this one goes out
+#pragma unroll
+          for (int i = 0; i < 8; ++i) theirs[i] = after[i];
+          if (db + 1 < kPairs) load_other(w.t, db + 1, after);
+        }
         ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
         if (!ok) break;
         tc_fence_after();
@@ -926,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more && !begun) ready(item + 1, db, false);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(f_item + hb + i);
+          const float4 f = *reinterpret_cast<const float4*>(f_item + i);
           v[i] *= f.x;
           v[i + 1] *= f.y;
           v[i + 2] *= f.z;
@@ -938,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* sums = p.part + part * kPartFloats + db * 128 + at0;
           if (!begins) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = fmaf(f_first[hb + i], sums[i * kDim], v[i]);
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(f_first[i], sums[i * kDim], v[i]);
           }
           if (!whole) {
 #pragma unroll

@@ -524,7 +524,7 @@ int ds4x_kv16_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, c
  *       out[t,h,:] = (sum_r exp(x_r) row_r + exp(other_lse[t,h]) other_out[t,h,:]) / w,   lse[t,h] = log w
  *   so `other`, the out and lse of an attention over other rows (ds4x_kv4_attn over the pooled ones), is joined
  *   into one softmax.  Where w is an empty sum: out = 0 and lse = -INFINITY.  Where other_lse is -INFINITY
- *   other_out is not read.
+ *   other_out does not count, whatever it holds.
  *
  *   q_attn, out, other_out [T, Hq, Dkv] of `dtype`; lse (or NULL), other_lse [T, Hq] fp32; slopes, sinks [Hq]
  *   fp32 or NULL; req, positions, first [T], rows, prefix [n_req] int32, tables [n_req, max_pages].
