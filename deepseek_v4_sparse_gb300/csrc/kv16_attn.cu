@@ -17,8 +17,9 @@
 // with K = V = the chunk in 128B-swizzled shared memory (8 slots of 64 dims, two buffers).
 //
 // Warps: 0-3 copy rows (16-byte cp.async; 16 rows each, one step of the O^T products), 4-11 softmax (16 heads by
-// quadrant and half of the rows each, 4 threads a head), 12-27 write the output (O^T lanes by quadrant, 16 heads
-// each), 28 issues the S products, 29 the O^T products, 30 looks up the rows' slots a few chunks ahead, 31 loads q.
+// quadrant and half of the rows each, 4 threads a head), 12-27 write the output (O^T lanes by quadrant, a quarter
+// of the dims each), 28 issues the S products, 29 the O^T products, 30 looks up the rows' slots a few chunks ahead, 31 loads
+// q and works out what the heads' output needs.
 // Buffers are copied and released in quarters of the dims, O^T rotates over six 64-column TMEM
 // slots (a token uses four), so neighbouring tokens overlap.  A chunk that is not full costs its O^T products and
 // copies by 16 rows.  The other attention's output is where a token's sums begin: the output warps put it, times
@@ -57,9 +58,9 @@ constexpr int kSoftWarp = 4, kOutWarp = 12, kSWarp = 28, kOWarp = 29, kSlotWarp 
 constexpr int kCopyWarps = 4, kSoftWarps = 8, kOutWarps = 16;
 constexpr int kWarps = 32, kThreads = 32 * kWarps;
 // registers a thread: 64 at launch; the sum over the eight warpgroups stays what it was
-constexpr int kLaunchRegs = 64, kMiscRegs = 40, kSoftRegs = 88, kOutRegs = 56;  // and 64 for the copies
-static_assert(kOutRegs < kLaunchRegs && kMiscRegs < kLaunchRegs && kSoftRegs > kLaunchRegs, "dec, dec and inc below");
-static_assert(kThreads * kLaunchRegs <= 65536 && kLaunchRegs + 2 * kSoftRegs + 4 * kOutRegs + kMiscRegs <= 8 * kLaunchRegs, "registers");
+constexpr int kLaunchRegs = 64, kCopyRegs = 56, kMiscRegs = 40, kSoftRegs = 80;  // and 64 for the output
+static_assert(kCopyRegs < kLaunchRegs && kMiscRegs < kLaunchRegs && kSoftRegs > kLaunchRegs, "dec, dec and inc below");
+static_assert(kThreads * kLaunchRegs <= 65536 && kCopyRegs + 2 * kSoftRegs + 4 * kLaunchRegs + kMiscRegs <= 8 * kLaunchRegs, "registers");
 constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
@@ -75,14 +76,13 @@ constexpr int kOffAhead = kOffMask + kMaskRing * 8;    // int[kMaskRing]: e - hi
 // float[2 items][2 halves of the rows' sums of rounded weights, 2 halves' sums, offset][64]
 constexpr int kOffStat = kOffAhead + kMaskRing * 4;
 constexpr int kOffMax = kOffStat + 2 * 5 * kHq * 4;    // float[2 halves of the rows][64]: maxima of one chunk
-constexpr int kOutHeads = 16;                    // heads of an output warp
-constexpr int kOffJoin = kOffMax + 2 * kHq * 4;    // float[output warps][3][kOutHeads]: factors of a token's sums so far, of an
-                                                 // item's sums, and of the next token's other output
-constexpr int kOffScan = kOffJoin + kOutWarps * 3 * kOutHeads * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
+constexpr int kOffJoin = kOffMax + 2 * kHq * 4;  // float[2 items][2][64]: factors of a token's sums so far, of an item's
+                                                 // sums; [3 items][64]: of the other output that the sums begin with
+constexpr int kOffScan = kOffJoin + 7 * kHq * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
                                                  // then int[4]: the block's part, and the last chunk (+ 1) in which a
                                                  // maximum moved
 constexpr int kOffBars = kOffScan + (kWarps + 2) * 8 + 16;
-constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kPairs + 5 * 2 + 2 * kOSlots + 2 * 2;
+constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kPairs + 5 * 2 + 3 * kOSlots + 4 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffTmemSlot + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -222,6 +222,20 @@ struct Walk {
   }
 };
 
+// An item among its token's: the block's first of the token (`from` its first chunk), the block's last, all of the token.
+struct ItemPart {
+  bool begins, ends, whole, joins;  // joins: one of several, whose sums are added to those so far
+  int64_t part;                     // chunks before the block, or behind it: the sums go to the block's first or second part
+  __device__ __forceinline__ ItemPart(const Walk& w, uint32_t item, int& from) {
+    if (w.c0 == 0 || item == 0) from = w.c0;
+    begins = w.c0 == from;
+    ends = w.c1 == w.end;
+    whole = ends && from == 0 && w.c1 == chunks_of(w.n);
+    joins = !(begins && ends);
+    part = 2 * (int64_t)blockIdx.x + (from == 0);
+  }
+};
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
   if constexpr (kBf16) {
@@ -302,9 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pempty = pfull + 2;
   uint64_t* looked = pempty + 2;            // every softmax warp has seen whether its maxima move
   uint64_t* ofull = looked + 2;             // [O^T slot]
-  uint64_t* oready = ofull + kOSlots;       // [O^T slot] emptied, and filled with what the sums begin with
+  uint64_t* oempty = ofull + kOSlots;       // [O^T slot] read out
+  uint64_t* oready = oempty + kOSlots;      // [O^T slot] with another attention to join: holds what the sums begin with
   uint64_t* lready = oready + kOSlots;      // [item parity] statistics written
   uint64_t* lfree = lready + 2;             // [item parity] ... and read
+  uint64_t* fready = lfree + 2;             // [item parity] the output's factors written
+  uint64_t* ffree = fready + 2;             // [item parity] ... and read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmemSlot);
 
   // the warp's number through a warp reduction: a branch on it is then known not to divide a warp, and the products of
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps
                    : bar >= sfull && bar < sempty ? 2  // the products' completion and the issuing warp itself
                    : (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || (bar >= lready && bar < lfree) ? kSoftWarps
-                   : bar >= oready ? kOutWarps : 1);
+                   : bar >= ffree ? kOutWarps : bar >= oempty && bar < lready ? kOutWarps / kPairs : 1);
     fence_mbarrier_init();
   }
   if (warp == kSWarp) tmem_alloc(tmem_slot, kTmemCols);
@@ -399,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < kCopyWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     // ------------------------------------------------------------------------------- copies
     // rows 16 warp .. + 15 of the chunk, two at a time: lane / 16 the row, lane % 16 the 16-byte piece of the
     // quarter's 256 bytes.  Rows 8 apart lie 1024 bytes apart with the same swizzle.
@@ -539,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int db = 0; db < kPairs; ++db) {
             const int os = oslot(item, db);
             if (c == w.c0) {
-              if (!wait_bar_warp(&oready[os], ophase(item, db), p.status, 106)) { ok = false; break; }
+              uint64_t* bar = p.other ? &oready[os] : &oempty[os];
+              if (!wait_bar_warp(bar, ophase(item, db) ^ (p.other ? 0u : 1u), p.status, 106)) { ok = false; break; }
               tc_fence_after();
             }
             const uint32_t a = v + (2 * db * kSlotBytes >> 4), to = tmem + kColO + os * kHq;
@@ -597,21 +616,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // ------------------------------------------------------------------------------ q
-      uint32_t item = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (Walk w(rows_s, start); w.left > 0 && ok; w.next(), ++item) {
-        ok = wait_bar_warp(qempty, (item & 1) ^ 1, p.status, 108);
-        if (!ok) break;
+      // -------------------------------------------------------------- q, and the arithmetic of the heads
+      // q of an item goes in when the products of the one before are done with theirs.  Then, when that one's statistics
+      // are there, what its output needs: two heads a lane.
+      auto load_q = [&](int t) {
         mbar_arrive_expect_tx_elect(qfull, kQBytes);
 #pragma unroll 1
-        for (int i = 0; i < kSlots; ++i) tma_load_2d_elect(sq + i * kQBlockBytes, &tm_q, qfull, i * 64, w.t * kHq);
+        for (int i = 0; i < kSlots; ++i) tma_load_2d_elect(sq + i * kQBlockBytes, &tm_q, qfull, i * 64, t * kHq);
+      };
+      float m_far[2], r_far[2], l_far[2];  // a token's offsets and sums so far
+      uint32_t item = 0;
+      int from = 0;       // the block's first chunk of the token
+      bool ok = true;
+      Walk w(rows_s, start);
+      if (w.left > 0) load_q(w.t);
+#pragma unroll 1
+      while (w.left > 0) {
+        const int par = item & 1;
+        const ItemPart it(w, item, from);
+        const int t = w.t;
         if (lane == 0 && w.c1 == w.end && w.left > w.c1 - w.c0) {  // what the next token will ask for
           prefetch_l2(p.q + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
           if (p.other) prefetch_l2(p.other + (int64_t)(w.t + 1) * kHq * kDim, kHq * kDim * 2);
         }
         __syncwarp();
+        w.next();
+        const bool begun = w.left > 0 && p.other && w.c0 == 0;  // the next item
+        float sink[2], next[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sink[i] = it.whole && p.sinks ? __ldg(p.sinks + lane + 32 * i) * kLog2e : -INFINITY;
+          next[i] = begun ? __ldg(p.other_lse + (int64_t)w.t * kHq + lane + 32 * i) : 0.f;
+        }
+        if (w.left > 0) {
+          ok = wait_bar_warp(qempty, item & 1, p.status, 108);
+          if (!ok) break;
+          load_q(w.t);
+        }
+        // these factors' place was last read two items ago, that of the next item's other weights before
+        ok = wait_bar_warp(&ffree[par], ((item >> 1) & 1) ^ 1, p.status, 118);
+        ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = lane + 32 * i;
+          const float* st = stat_s + par * 5 * kHq + h;
+          float r = st[0] + st[kHq], l = st[2 * kHq] + st[3 * kHq], m = st[4 * kHq];
+          float f0 = 0.f, fi = 1.f;
+          if (it.joins) {
+            const float m0 = it.begins ? kNone : m_far[i], mi = m;
+            m = fmaxf(m0, mi);
+            f0 = it.begins ? 0.f : ex2_approx(m0 - m);
+            fi = ex2_approx(mi - m);
+            r_far[i] = r = r * fi + (it.begins ? 0.f : r_far[i] * f0);
+            l_far[i] = l = l * fi + (it.begins ? 0.f : l_far[i] * f0);
+            m_far[i] = m;
+          }
+          if (it.whole) {
+            const Joined j = join_head(m, r, l, sink[i]);
+            if (p.lse) p.lse[(int64_t)t * kHq + h] = j.lse;
+            f0 *= j.own;
+            fi *= j.own;
+          } else if (it.ends) {
+            float* ps = p.stat + it.part * kStatFloats + h;
+            ps[0] = r;
+            ps[kHq] = l;
+            ps[2 * kHq] = m;
+          }
+          float* f = join_s + par * 2 * kHq + h;
+          f[0] = f0;
+          f[kHq] = fi;
+          if (begun) join_s[(4 + (item + 1) % 3) * kHq + h] = first_weight(next[i]);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&lfree[par]);
+          mbar_arrive(&fready[par]);
+        }
+        ++item;
       }
     }
   } else if (warp < kOutWarp) {
@@ -824,152 +906,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&lready[item & 1]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // --------------------------------------------------------------------------- output
-    // heads hb .. + 15 and dims 32 quad + lane of each quarter; the warp's first 16 lanes do a head's arithmetic
-    const int quad = warp & 3, hb = (warp - kOutWarp) >> 2 << 4;
-    const bool odd = lane & 1, has_head = lane < kOutHeads;
-    const int head = hb + (lane & (kOutHeads - 1));
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO + hb;
-    const int at0 = hb * kDim + quad * 32 + lane;  // this thread's first head and dim of a quarter, within a token
-    float* f_first = join_s + (warp - kOutWarp) * 3 * kOutHeads;
-    float *f_item = f_first + kOutHeads, *f_other = f_item + kOutHeads;
-    float m_far = kNone, r_far = 0.f, l_far = 0.f;  // a token's offset and sums so far
+    // A warp takes a quarter db of the dims, of which its quadrant of O^T's lanes are 32, and all heads, 16 at a time.
+    const int quad = warp & 3, db = (warp - kOutWarp) >> 2;
+    const bool odd = lane & 1;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColO;
+    const int d = db * 128 + quad * 32 + lane;       // this thread's dim
     uint32_t item = 0;
-    bool ok = true;
     int from = 0;       // the block's first chunk of the token
-    uint32_t theirs[8], after[8];
-    // The other attention's output of token t, quarter db: an even lane the even heads at its dim and the next, an odd
-    // one the odd heads at the dim before and its own; neighbours exchange.
-    auto load_other = [&](int t, int db, uint32_t (&u)[8]) {
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.other + (int64_t)t * kHq * kDim + db * 128 + at0 - odd + (odd ? kDim : 0));
+    bool ok = true;
+    uint32_t even[8], uneven[8];
+    // The other attention's output of token t, heads 16 n .. + 15: an even lane the even heads at its dim and the next, an
+    // odd one the odd heads at the dim before and its own; neighbours exchange.
+    auto load_other = [&](int t, int n, uint32_t (&u)[8]) {
+      const uint32_t* src =
+          reinterpret_cast<const uint32_t*>(p.other + ((int64_t)t * kHq + 16 * n + (odd ? 1 : 0)) * kDim + (d & ~1));
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i * kDim);
     };
-    // slot of quarter db of item n is empty; with another attention to join its sums begin with that
-    auto ready = [&](uint32_t n, int db, bool begun) {
-      if (begun) {
+    // The slot of item n's quarter, once it is empty, is ready for its products: with weights of the other attention token
+    // t's sums begin there with its output, whose first 32 heads are on their way.
+    auto begin = [&](uint32_t n, int t, const float* f_other) {
+      const int os = oslot(n, db);
+      const bool got = wait_bar_warp(&oempty[os], ophase(n, db) ^ 1u, p.status, 117);
+      tc_fence_after();
+      auto fill = [&](int h, uint32_t (&u)[8]) {
         float v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t pair = __byte_perm(theirs[i], __shfl_xor_sync(0xffffffffu, theirs[i], 1), odd ? 0x3276u : 0x5410u);
-          const float2 f = *reinterpret_cast<const float2*>(f_other + 2 * i);
+          const uint32_t pair = __byte_perm(u[i], __shfl_xor_sync(0xffffffffu, u[i], 1), odd ? 0x3276u : 0x5410u);
+          const float2 f = *reinterpret_cast<const float2*>(f_other + 16 * h + 2 * i);
           v[2 * i] = f.x == 0.f ? 0.f : f.x * from16<kBf16>((uint16_t)pair);
           v[2 * i + 1] = f.y == 0.f ? 0.f : f.y * from16<kBf16>((uint16_t)(pair >> 16));
         }
-        tmem_st16(t_lane + oslot(n, db) * kHq, v);
+        if (h + 2 < kHq / 16) load_other(t, h + 2, u);
+        tmem_st16(t_lane + os * kHq + 16 * h, v);
+      };
+      if (f_other) {
+#pragma unroll 1
+        for (int h = 0; h < kHq / 16; h += 2) {
+          fill(h, even);
+          fill(h + 1, uneven);
+        }
         tc_wait_st();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&oready[oslot(n, db)]);
+      if (lane == 0) mbar_arrive(&oready[os]);
+      return got;
     };
     Walk w(rows_s, start);
-    {
-      const bool begun = w.left > 0 && p.other && w.c0 == 0;
-      if (begun) {
-        load_other(w.t, 0, after);
-        if (has_head) f_other[lane] = first_weight(__ldg(p.other_lse + (int64_t)w.t * kHq + head));
+    if (w.left > 0 && p.other) {
+      const float* f_other = nullptr;
+      if (w.c0 == 0) {
+        load_other(w.t, 0, even);
+        load_other(w.t, 1, uneven);
+        float* f = join_s + 4 * kHq;  // every warp writes the same values
+        const float* lse = p.other_lse + (int64_t)w.t * kHq + lane;
+        f[lane] = first_weight(__ldg(lse));
+        f[lane + 32] = first_weight(__ldg(lse + 32));
         __syncwarp();
+        f_other = f;
       }
-#pragma unroll 1
-      for (int db = 0; db < kPairs; ++db) {
-        if (begun) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) theirs[i] = after[i];
-          if (db + 1 < kPairs) load_other(w.t, db + 1, after);
-        }
-        ready(0, db, begun);
-      }
+      ok = begin(0, w.t, f_other);
     }
 #pragma unroll 1
     while (w.left > 0) {
       const int par = item & 1;
-      // chunks before the block, or behind it: the sums go to the block's first or second part
-      if (w.c0 == 0 || item == 0) from = w.c0;
-      const bool begins = w.c0 == from, ends = w.c1 == w.end;
-      const bool whole = ends && from == 0 && w.c1 == chunks_of(w.n);
-      const bool joins = !(begins && ends);  // one of several items: joined to those so far
-      const int64_t part = 2 * (int64_t)blockIdx.x + (from == 0);
+      const ItemPart it(w, item, from);
       const int t = w.t;
       w.next();
-      const bool more = w.left > 0, begun = more && p.other && w.c0 == 0;  // the next item
-      float next_lse = 0.f;
+      const bool begun = w.left > 0 && p.other && w.c0 == 0;  // the next item
       if (begun) {
-        load_other(w.t, 0, after);
-        next_lse = __ldg(p.other_lse + (int64_t)w.t * kHq + head);
+        load_other(w.t, 0, even);
+        load_other(w.t, 1, uneven);
       }
-      const float sink2 = whole && p.sinks ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-      ok = ok && wait_bar_warp(&lready[par], (item >> 1) & 1, p.status, 114);
+      ok = ok && wait_bar_warp(&fready[par], (item >> 1) & 1, p.status, 113);
       if (!ok) break;
-      if (has_head) {
-        const float* st = stat_s + par * 5 * kHq + head;
-        float r = st[0] + st[kHq], l = st[2 * kHq] + st[3 * kHq], m = st[4 * kHq];
-        float f0 = 0.f, fi = 1.f;
-        if (joins) {
-          const float m0 = begins ? kNone : m_far, mi = m;
-          m = fmaxf(m0, mi);
-          f0 = begins ? 0.f : ex2_approx(m0 - m);
-          fi = ex2_approx(mi - m);
-          r_far = r = r * fi + (begins ? 0.f : r_far * f0);
-          l_far = l = l * fi + (begins ? 0.f : l_far * f0);
-          m_far = m;
-        }
-        if (whole) {
-          const Joined j = join_head(m, r, l, sink2);
-          if (quad == 0 && p.lse) p.lse[(int64_t)t * kHq + head] = j.lse;
-          f0 *= j.own;
-          fi *= j.own;
-        } else if (quad == 0 && ends) {
-          float* ps = p.stat + part * kStatFloats + head;
-          ps[0] = r;
-          ps[kHq] = l;
-          ps[2 * kHq] = m;
-        }
-        f_first[lane] = f0;
-        f_item[lane] = fi;
-        if (begun) f_other[lane] = first_weight(next_lse);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&lfree[par]);
+      const float *f_first = join_s + par * 2 * kHq, *f_item = f_first + kHq;
+      const float* f_other = begun ? join_s + (4 + (item + 1) % 3) * kHq : nullptr;
+      const int os = oslot(item, db);
+      ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll 1
-      for (int db = 0; db < kPairs; ++db) {
-        const int os = oslot(item, db);
-        if (begun) {  // the next quarter's is on its way while this one goes out
-#pragma unroll
-          for (int i = 0; i < 8; ++i) theirs[i] = after[i];
-          if (db + 1 < kPairs) load_other(w.t, db + 1, after);
-        }
-        ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
-        if (!ok) break;
-        tc_fence_after();
+      for (int h = 0; h < kHq; h += 16) {
         float v[16];
-        tmem_ld16(t_lane + os * kHq, v);
+        tmem_ld16(t_lane + os * kHq + h, v);
         tc_wait_ld();
-        if (more && !begun) ready(item + 1, db, false);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(f_item + i);
+          const float4 f = *reinterpret_cast<const float4*>(f_item + h + i);
           v[i] *= f.x;
           v[i + 1] *= f.y;
           v[i + 2] *= f.z;
           v[i + 3] *= f.w;
         }
-        if (!whole || joins) {
+        if (!it.whole || it.joins) {
           // Sums so far lie where the part's go: the second part's own token is the block's last, behind all that
           // lie whole in the block.  A thread reads back only what it wrote.
-          float* sums = p.part + part * kPartFloats + db * 128 + at0;
-          if (!begins) {
+          float* sums = p.part + it.part * kPartFloats + h * kDim + d;
+          if (!it.begins) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = fmaf(f_first[i], sums[i * kDim], v[i]);
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(f_first[h + i], sums[i * kDim], v[i]);
           }
-          if (!whole) {
+          if (!it.whole) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sums[i * kDim] = v[i];
           }
         }
-        if (whole) {
-          uint16_t* to_out = p.out + (int64_t)t * kHq * kDim + db * 128 + at0;
+        if (it.whole) {
+          uint16_t* to_out = p.out + ((int64_t)t * kHq + h) * kDim + d;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
@@ -977,9 +1024,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
           }
         }
-        if (begun) ready(item + 1, db, true);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&oempty[os]);
+        mbar_arrive(&ffree[par]);
       }
       ++item;
+      if (p.other && w.left > 0) ok = begin(item, w.t, f_other);
     }
   }
 
