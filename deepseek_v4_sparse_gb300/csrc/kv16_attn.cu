@@ -66,6 +66,7 @@ constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and mask
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
 constexpr int kItemChunks = 256;
 constexpr int kTokenUnits = 2;
+constexpr int kWholeChunks = 4;                  // chunks of a token that no boundary divides
 constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
 constexpr int kOffP = kOffKV + 2 * kBufBytes;
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first; t < last; ++t) {
       const int nch = chunks_of(rows_s[t]), units = own + nch;
       auto chunk_at = [&](long long unit) {  // of this token's, at a unit of its
-        if (2 * (long long)nch <= quota && (nch <= 8 || 8 * (long long)nch <= quota)) return 2 * unit > units ? nch : 0;
+        if (nch <= kWholeChunks || (2 * (long long)nch <= quota && (nch <= 8 || 8 * (long long)nch <= quota)))
+          return 2 * unit > units ? nch : 0;
         return (int)max(unit - own, 0ll);
       };
       if (at <= g0 && g0 < at + units) {
@@ -1047,26 +1049,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a token that several blocks worked on: part k holds O_k = sum_j 2^(x_j - m_k) kv_j and
 // the sums r_k of its rounded weights and l_k of the exact ones, so with M = max_k m_k the token's are
 //   O = sum_k 2^(m_k - M) O_k, r and l alike,
-// and the sink joins them as it does in the kernel above.  A thread holds 4 dims; kGroups
-// groups of threads take the parts in turn and are added up at the end, in an order that depends on the parts'
-// number alone: the same bits on every run.
-//   Many tokens (two or three parts each): a block per boundary between two blocks and four heads, one group
-//   of 128 threads a head.
+// and the sink joins them as it does in the kernel above.  A thread holds 4 dims; kGroups groups of threads take the
+// parts in turn and are added up at the end, in an order that depends on the parts' number alone: the same bits on every
+// run.  A thread's first parts are on their way while the weights are worked out.
+//   Many tokens (two or three parts each): a block per boundary between two blocks and eight heads, one group of
+//   128 threads for two heads.
 //   Few tokens (under a quarter of the blocks; one may have a part of every block): a block per token and head,
 //   four groups.  Under 8 tokens four blocks a head, each a quarter of the dims, eight groups.
 constexpr int kMaxParts = 256;
-template <bool kBf16, bool kByToken, int kGroups, int kHeads, int kDimBlocks>
-__global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
+template <bool kBf16, bool kByToken, int kGroups, int kTeams, int kRounds, int kDimBlocks>
+__global__ void __launch_bounds__(kGroups * kTeams * kDim / 4 / kDimBlocks)
     kv16_combine_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
                         const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
-  constexpr int kLane4 = kDim / 4 / kDimBlocks, kTeam = kGroups * kLane4;
-  static_assert(kTeam >= 32 && (kHeads == 1 || kGroups == 1), "a team's first warp takes its statistics");
+  constexpr int kLane4 = kDim / 4 / kDimBlocks, kTeam = kGroups * kLane4, kHeads = kTeams * kRounds;
+  constexpr int kEarly = kGroups > 1 ? 8 : 2;  // parts of a round that a thread loads before their weights are there
+  static_assert(kTeam * kTeams / 32 >= kHeads && (kHeads == 1 || kGroups == 1), "a warp a head takes its statistics");
   __shared__ float weight[kHeads][kMaxParts], own_s[kHeads];
   __shared__ float4 acc_s[kGroups > 1 ? kGroups - 1 : 1][kLane4];
   __shared__ int found;
   pdl_wait();
   pdl_trigger();
-  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, h = blockIdx.y * kHeads + team;
+  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, h0 = blockIdx.y * kHeads;
   // block i's entry: the token it starts in, its chunks before the block, its chunks, a block's chunks.  The
   // first block that a token reaches into tells all about it.
   int i = blockIdx.x + 1;
@@ -1086,16 +1089,27 @@ __global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
   if (!joins_at(at)) return;
   const int n = 1 + (at.z - at.y + at.w - 1) / at.w;  // parts: block i - 1's second, then the first ones
   auto part_no = [&](int k) { return k == 0 ? 2 * (int64_t)(i - 1) + 1 : 2 * (int64_t)(i - 1 + k); };
-  const int64_t row = (int64_t)at.x * kHq + h;
-  if (tid < 32) {
+  const int group = tid / kLane4, lane4 = tid % kLane4, x = blockIdx.z * kLane4 + lane4;
+  const float4* src = reinterpret_cast<const float4*>(part + (h0 + team) * kDim) + x;  // of the first round
+  float4 early[kRounds][kEarly];
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q)
+#pragma unroll
+    for (int j = 0; j < kEarly; ++j) {
+      const int k = group + j * kGroups;
+      if (k < n) early[q][j] = src[part_no(k) * (kPartFloats / 4) + q * kTeams * (kDim / 4)];
+    }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < kHeads) {
+    const int h = h0 + warp;
     float mx = kNone, r = 0.f, l = 0.f;
-    for (int k = tid; k < n; k += 32) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
+    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    for (int k = tid; k < n; k += 32) {
+    for (int k = lane; k < n; k += 32) {
       const float* st = stat + part_no(k) * kStatFloats + h;
       const float f = exp2f(st[2 * kHq] - mx);
-      weight[team][k] = f;
+      weight[warp][k] = f;
       r += f * st[0];
       l += f * st[kHq];
     }
@@ -1104,46 +1118,65 @@ __global__ void __launch_bounds__(kGroups * kHeads * kDim / 4 / kDimBlocks)
       r += __shfl_xor_sync(0xffffffffu, r, d);
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
-    if (tid == 0) {
+    if (lane == 0) {
       const Joined j = join_head(mx, r, l, sinks ? sinks[h] * kLog2e : -INFINITY);
-      own_s[team] = j.own;
-      if (lse && blockIdx.z == 0) lse[row] = j.lse;
+      own_s[warp] = j.own;
+      if (lse && blockIdx.z == 0) lse[(int64_t)at.x * kHq + h] = j.lse;
     }
   }
   __syncthreads();
-  const int group = tid / kLane4, lane4 = tid % kLane4, x = blockIdx.z * kLane4 + lane4;
-  const float4* src = reinterpret_cast<const float4*>(part + h * kDim) + x;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = group; k < n; k += kGroups) {
-    const float4 o = src[part_no(k) * (kPartFloats / 4)];
-    const float f = weight[team][k];
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
+  float4 acc[kRounds];
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int q, int k, const float4& o) {
+    const float f = weight[q * kTeams + team][k];
+    acc[q].x += f * o.x;
+    acc[q].y += f * o.y;
+    acc[q].z += f * o.z;
+    acc[q].w += f * o.w;
+  };
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q) {
+#pragma unroll
+    for (int j = 0; j < kEarly; ++j)
+      if (group + j * kGroups < n) add(q, group + j * kGroups, early[q][j]);
+  }
+#pragma unroll(kRounds > 1 ? 4 : 8)
+  for (int k = group + kEarly * kGroups; k < n; k += kGroups) {
+    float4 o[kRounds];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) o[q] = src[part_no(k) * (kPartFloats / 4) + q * kTeams * (kDim / 4)];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) add(q, k, o[q]);
   }
   if constexpr (kGroups > 1) {
-    if (group > 0) acc_s[group - 1][lane4] = acc;
+    if (group > 0) acc_s[group - 1][lane4] = acc[0];
     __syncthreads();
     if (group > 0) return;
 #pragma unroll
     for (int k = 0; k < kGroups - 1; ++k) {
       const float4 o = acc_s[k][lane4];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
+      acc[0].x += o.x;
+      acc[0].y += o.y;
+      acc[0].z += o.z;
+      acc[0].w += o.w;
     }
   }
-  const float own = own_s[team];
-  const uint32_t lo = pack16<kBf16>(acc.x * own, acc.y * own), hi = pack16<kBf16>(acc.z * own, acc.w * own);
-  *reinterpret_cast<uint2*>(out + row * kDim + 4 * x) = make_uint2(lo, hi);
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q) {
+    const int hs = q * kTeams + team;  // the head among the block's
+    const float own = own_s[hs];
+    const uint32_t lo = pack16<kBf16>(acc[q].x * own, acc[q].y * own), hi = pack16<kBf16>(acc[q].z * own, acc[q].w * own);
+    *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h0 + hs) * kDim + 4 * x) = make_uint2(lo, hi);
+  }
 }
 
+// Tokens of up to kWholeChunks chunks are never split (which takes a quarter of the time of joining parts, a launch at
+// least): a call that can have no others has no parts, and a block a token at most.
+constexpr int kUnsplitRows = kWholeChunks * kRows;
 // Blocks for T tokens of up to max_rows rows: one an SM, at most one a chunk.
 int grid_of(int T, int max_rows) {
-  const int64_t chunks = (int64_t)T * (max_rows > kRows ? (max_rows - 1) / kRows + 1 : 1);
+  const int64_t chunks = (int64_t)T * (max_rows > kUnsplitRows ? (max_rows - 1) / kRows + 1 : 1);
   const int sms = device_sm_count();
   const int64_t most = sms < kMaxParts ? sms : kMaxParts;  // a token has at most a part of every block
   return (int)(chunks < most ? chunks : most);
@@ -1152,9 +1185,9 @@ constexpr size_t kHeadBytes = 16 * kMaxParts;  // the int4 of every block
 
 }  // namespace
 
-// A token of one chunk is never split: the head alone then, which the launch writes all the same.
+// Without parts the head alone, which the launch writes all the same.
 size_t kv16_attn_workspace_bytes(int T, int max_rows) {
-  if (max_rows <= kRows) return kHeadBytes;
+  if (max_rows <= kUnsplitRows) return kHeadBytes;
   const int grid = grid_of(T < kTokens ? T : kTokens, max_rows);
   return kHeadBytes + (size_t)2 * grid * (kPartFloats + kStatFloats) * sizeof(float);
 }
@@ -1208,18 +1241,18 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
     if (launch_pdl(kv16_attn_kernel<kBf16>, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, tq, p) != cudaSuccess)
       return DS4X_ERR_CUDA;
     count_launch();
-    if (grid > 1 && a.max_rows > kRows) {  // a token of one chunk is never split
+    if (grid > 1 && a.max_rows > kUnsplitRows) {
       auto join = [&](auto kernel, dim3 blocks, int threads) {
         return launch_pdl(kernel, blocks, dim3(threads), 0, stream, (const int4*)p.parts_of, grid, (const float*)p.part,
                           (const float*)p.stat, p.sinks, p.out, p.lse);
       };
       cudaError_t e;
       if (4 * p.T < grid && p.T < 8)  // few tokens: four blocks a head fill more of the GPU
-        e = join(kv16_combine_kernel<kBf16, true, 8, 1, 4>, dim3(p.T, kHq, 4), 256);
+        e = join(kv16_combine_kernel<kBf16, true, 8, 1, 1, 4>, dim3(p.T, kHq, 4), 256);
       else if (4 * p.T < grid)
-        e = join(kv16_combine_kernel<kBf16, true, 4, 1, 1>, dim3(p.T, kHq), 512);
+        e = join(kv16_combine_kernel<kBf16, true, 4, 1, 1, 1>, dim3(p.T, kHq), 512);
       else
-        e = join(kv16_combine_kernel<kBf16, false, 1, 4, 1>, dim3(grid - 1, kHq / 4), 512);
+        e = join(kv16_combine_kernel<kBf16, false, 1, 4, 2, 1>, dim3(grid - 1, kHq / 8), 512);
       if (e != cudaSuccess) return DS4X_ERR_CUDA;
       count_launch();
     }
