@@ -106,7 +106,7 @@ struct Params {
   float* lse;
   int* status;
   int4* parts_of;  // [grid]: the token a block starts in, chunks of it before the block, chunks it has, quota;
-                   // NULL without a workspace, when there can be no rows at all
+                   // NULL without a workspace, where no token can be split
   float* part;     // [2 grid][kPartFloats]
   float* stat;     // [2 grid][kStatFloats]
   int n_slots, n_req, max_pages, log_page, ratio, window, t0, T;
@@ -1185,9 +1185,9 @@ constexpr size_t kHeadBytes = 16 * kMaxParts;  // the int4 of every block
 
 }  // namespace
 
-// Without parts the head alone, which the launch writes all the same.
+// Nothing without parts: an allocation less in a call whose cost is its launch.
 size_t kv16_attn_workspace_bytes(int T, int max_rows) {
-  if (max_rows <= kUnsplitRows) return kHeadBytes;
+  if (max_rows <= kUnsplitRows) return 0;
   const int grid = grid_of(T < kTokens ? T : kTokens, max_rows);
   return kHeadBytes + (size_t)2 * grid * (kPartFloats + kStatFloats) * sizeof(float);
 }
@@ -1213,15 +1213,15 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.scale = a.scale;
   p.cap = a.cap;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);  // NULL: no parts
   p.parts_of = reinterpret_cast<int4*>(ws);
   for (int t0 = 0; t0 < a.T; t0 += kTokens) {  // launches on one stream: they may share the workspace
     p.t0 = t0;
     p.T = a.T - t0 < kTokens ? a.T - t0 : kTokens;
     const int grid = grid_of(p.T, a.max_rows);
     const int64_t row0 = (int64_t)t0 * kHq;
-    p.part = reinterpret_cast<float*>(ws + kHeadBytes);
-    p.stat = p.part + (size_t)2 * grid * kPartFloats;
+    p.part = ws ? reinterpret_cast<float*>(ws + kHeadBytes) : nullptr;
+    p.stat = ws ? p.part + (size_t)2 * grid * kPartFloats : nullptr;
     p.q = static_cast<const uint16_t*>(a.q_attn) + row0 * kDim;
     p.out = static_cast<uint16_t*>(a.out) + row0 * kDim;
     p.lse = a.lse ? a.lse + row0 : nullptr;

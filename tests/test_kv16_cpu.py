@@ -115,10 +115,10 @@ def test_attn_refusals(lib):
         assert _attn(lib, **bad) == ds4x.ERR_UNSUPPORTED, bad
     assert _attn(lib, T=0, q=None) == ds4x.OK
     assert ds4x.kv16_attn_workspace_bytes(0, 512) == 0 and ds4x.kv16_attn_workspace_bytes(5, 0) == 0
-    if ds4x.kv16_attn_workspace_bytes(4, 64):
-        assert _attn(lib, nbytes=16) == ds4x.ERR_WORKSPACE
-        assert _attn(lib, ws=None) == ds4x.ERR_WORKSPACE
-        assert _attn(lib, ws=A + 8) == ds4x.ERR_INVALID
+    assert ds4x.kv16_attn_workspace_bytes(4, 64) == 0 and ds4x.kv16_attn_workspace_bytes(4, 1024) > 16
+    for bad in (dict(nbytes=16), dict(ws=None)):
+        assert _attn(lib, max_pages=64, page_rows=16, **bad) == ds4x.ERR_WORKSPACE, bad
+    assert _attn(lib, max_pages=64, page_rows=16, ws=A + 8) == ds4x.ERR_INVALID
 
 
 def test_binding_refuses_host_tensors():
