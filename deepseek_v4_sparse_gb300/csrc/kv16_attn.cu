@@ -9,7 +9,7 @@
 //
 // One block an SM.  The tokens' lists are cut into chunks of 64 rows; all chunks of all tokens form one sequence,
 // and each block takes an equal, contiguous part of it.  A token whose chunks lie in several blocks leaves its
-// unnormalised sums there in fp32 and kv16_combine_kernel joins them, so one long cache, a ragged batch and a
+// unnormalised sums there in fp32 and another kernel joins them, so one long cache, a ragged batch and a
 // prefill chunk are all spread evenly.  A token's chunks in a block are an item (several, if they are many:
 // kItemChunks).  Per chunk:
 //   S   [64 heads x 64 rows] = Q . K^T       tcgen05, M = 64 (heads on TMEM lanes), K-major
@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // --------------------------------------------------- every token's rows; this block's part
   {
-    // A token costs its chunks and, where there are many tokens a block, about two chunks' time to begin and end: each
-    // counts as that many units, the token's own first, and the blocks take equal numbers of units.
-    const int own = 2 * p.T >= (int)gridDim.x ? kTokenUnits : 0;
+    // A token costs its chunks and about two chunks' time to begin and end: each counts as that many units, the token's
+    // own first, and the blocks take equal numbers of units.
+    const int own = p.T > 1 ? kTokenUnits : 0;
     const int per = (p.T + kThreads - 1) / kThreads;
     const int first = tid * per, last = min(first + per, p.T);
     long long sum = 0;
@@ -1049,65 +1049,250 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a token that several blocks worked on: part k holds O_k = sum_j 2^(x_j - m_k) kv_j and
 // the sums r_k of its rounded weights and l_k of the exact ones, so with M = max_k m_k the token's are
 //   O = sum_k 2^(m_k - M) O_k, r and l alike,
-// and the sink joins them as it does in the kernel above.  A thread holds 4 dims; kGroups groups of threads take the
-// parts in turn and are added up at the end, in an order that depends on the parts' number alone: the same bits on every
-// run.  A thread's first parts are on their way while the weights are worked out.
-//   Many tokens (two or three parts each): a block per boundary between two blocks and eight heads, one group of
-//   128 threads for two heads.
-//   Few tokens (under a quarter of the blocks; one may have a part of every block): a block per token and head,
-//   four groups.  Under 8 tokens four blocks a head, each a quarter of the dims, eight groups.
+// and the sink joins them as it does in the kernel above.  Sums run in an order that depends on the parts' number
+// alone: the same bits on every run.  A thread holds 4 dims; its first parts are on their way while the weights are worked
+// out.
 constexpr int kMaxParts = 256;
-template <bool kBf16, bool kByToken, int kGroups, int kTeams, int kRounds, int kDimBlocks>
-__global__ void __launch_bounds__(kGroups * kTeams * kDim / 4 / kDimBlocks)
-    kv16_combine_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
-                        const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
-  constexpr int kLane4 = kDim / 4 / kDimBlocks, kTeam = kGroups * kLane4, kHeads = kTeams * kRounds;
-  constexpr int kEarly = kGroups > 1 ? 8 : 2;  // parts of a round that a thread loads before their weights are there
-  static_assert(kTeam * kTeams / 32 >= kHeads && (kHeads == 1 || kGroups == 1), "a warp a head takes its statistics");
-  __shared__ float weight[kHeads][kMaxParts], own_s[kHeads];
-  __shared__ float4 acc_s[kGroups > 1 ? kGroups - 1 : 1][kLane4];
+static_assert(2 * kMaxParts * kPartFloats < 1 << 30, "32-bit indexes");
+struct Parts {
+  int token, first, n;  // n parts: block first - 1's second, then the first ones of those from `first` on
+  __device__ __forceinline__ int no(int k) const { return 2 * (first - 1 + k) + (k == 0); }
+};
+// Block i's entry: the token it starts in, its chunks before the block, its chunks, a block's chunks.  The first block
+// that a token reaches into tells all about it.
+__device__ __forceinline__ bool reached(int4 at) { return at.x >= 0 && at.y > 0 && at.y <= at.w; }
+__device__ __forceinline__ Parts parts_at(int4 at, int i) { return Parts{at.x, i, 1 + (at.z - at.y + at.w - 1) / at.w}; }
+
+struct Sum4 {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float f, const float4& o) {
+    v.x += f * o.x;
+    v.y += f * o.y;
+    v.z += f * o.z;
+    v.w += f * o.w;
+  }
+  template <bool kBf16>
+  __device__ __forceinline__ void store(float own, uint16_t* to) const {
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack16<kBf16>(v.x * own, v.y * own), pack16<kBf16>(v.z * own, v.w * own));
+  }
+};
+
+// Under 4 tokens (one may have a part of every block): a block per token, head and quarter of the dims, eight groups of
+// 32 threads that take the parts in turn.
+constexpr int kFewTokens = 4, kFewGroups = 8, kFewBlocks = 4, kFewThreads = kFewGroups * kDim / 4 / kFewBlocks;
+template <bool kBf16>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    kv16_join_few_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
+                         const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
+  constexpr int kLane4 = kDim / 4 / kFewBlocks, kGroups = kFewGroups;
+  constexpr int kEarly = 20;  // parts that a thread loads before their weights are there
+  __shared__ float weight[kMaxParts], own_s;
+  __shared__ float4 acc_s[kGroups - 1][kLane4];
   __shared__ int found;
   pdl_wait();
   pdl_trigger();
-  const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, h0 = blockIdx.y * kHeads;
-  // block i's entry: the token it starts in, its chunks before the block, its chunks, a block's chunks.  The
-  // first block that a token reaches into tells all about it.
-  int i = blockIdx.x + 1;
-  auto joins_at = [](int4 at) { return at.x >= 0 && at.y > 0 && at.y <= at.w; };
-  if constexpr (kByToken) {
-    if (threadIdx.x == 0) found = 0;
-    __syncthreads();
-    for (int k = 1 + threadIdx.x; k < blocks; k += blockDim.x) {
-      const int4 at = parts_of[k];
-      if (at.x == (int)blockIdx.x && joins_at(at)) found = k;  // there is one at most
-    }
-    __syncthreads();
-    i = found;
-    if (i == 0) return;
+  const int h = blockIdx.y;
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
+  for (int k = 1 + threadIdx.x; k < blocks; k += blockDim.x) {
+    const int4 at = parts_of[k];
+    if (at.x == (int)blockIdx.x && reached(at)) found = k;  // there is one at most
   }
-  const int4 at = parts_of[i];
-  if (!joins_at(at)) return;
-  const int n = 1 + (at.z - at.y + at.w - 1) / at.w;  // parts: block i - 1's second, then the first ones
-  auto part_no = [&](int k) { return k == 0 ? 2 * (int64_t)(i - 1) + 1 : 2 * (int64_t)(i - 1 + k); };
-  const int group = tid / kLane4, lane4 = tid % kLane4, x = blockIdx.z * kLane4 + lane4;
-  const float4* src = reinterpret_cast<const float4*>(part + (h0 + team) * kDim) + x;  // of the first round
-  float4 early[kRounds][kEarly];
+  __syncthreads();
+  if (found == 0) return;
+  const Parts ps = parts_at(parts_of[found], found);
+  const int group = threadIdx.x / kLane4, lane4 = threadIdx.x % kLane4, x = blockIdx.z * kLane4 + lane4;
+  const float4* src = reinterpret_cast<const float4*>(part + h * kDim) + x;
+  float4 early[kEarly];
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q)
+  for (int j = 0; j < kEarly; ++j)
+    if (group + j * kGroups < ps.n) early[j] = src[ps.no(group + j * kGroups) * (kPartFloats / 4)];
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    float m[kMaxParts / 32], r[kMaxParts / 32], l[kMaxParts / 32], mx = kNone, rs = 0.f, ls = 0.f;
 #pragma unroll
-    for (int j = 0; j < kEarly; ++j) {
-      const int k = group + j * kGroups;
-      if (k < n) early[q][j] = src[part_no(k) * (kPartFloats / 4) + q * kTeams * (kDim / 4)];
+    for (int j = 0; j < kMaxParts / 32; ++j) {
+      const int k = lane + 32 * j;
+      const float* st = stat + (k < ps.n ? ps.no(k) : 0) * kStatFloats + h;
+      r[j] = k < ps.n ? st[0] : 0.f;
+      l[j] = k < ps.n ? st[kHq] : 0.f;
+      m[j] = k < ps.n ? st[2 * kHq] : kNone;
     }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < kHeads) {
-    const int h = h0 + warp;
-    float mx = kNone, r = 0.f, l = 0.f;
-    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, stat[part_no(k) * kStatFloats + 2 * kHq + h]);
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 32; ++j) mx = fmaxf(mx, m[j]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    for (int k = lane; k < n; k += 32) {
-      const float* st = stat + part_no(k) * kStatFloats + h;
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 32; ++j) {
+      const float f = exp2f(m[j] - mx);
+      weight[lane + 32 * j] = f;
+      rs += f * r[j];
+      ls += f * l[j];
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      rs += __shfl_xor_sync(0xffffffffu, rs, d);
+      ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    }
+    if (lane == 0) {
+      const Joined j = join_head(mx, rs, ls, sinks ? sinks[h] * kLog2e : -INFINITY);
+      own_s = j.own;
+      if (lse && blockIdx.z == 0) lse[(int64_t)ps.token * kHq + h] = j.lse;
+    }
+  }
+  __syncthreads();
+  Sum4 acc;
+#pragma unroll
+  for (int j = 0; j < kEarly; ++j)
+    if (group + j * kGroups < ps.n) acc.add(weight[group + j * kGroups], early[j]);
+#pragma unroll 8
+  for (int k = group + kEarly * kGroups; k < ps.n; k += kGroups) acc.add(weight[k], src[ps.no(k) * (kPartFloats / 4)]);
+  if (group > 0) acc_s[group - 1][lane4] = acc.v;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int k = 0; k < kGroups - 1; ++k) acc.add(1.f, acc_s[k][lane4]);
+  acc.store<kBf16>(own_s, out + ((int64_t)ps.token * kHq + h) * kDim + 4 * x);
+}
+
+// Fewer tokens than blocks: two blocks an SM list the tokens that have parts, and their teams of 128 threads take a head
+// of a token each in turn.  Where a token has more than kLongParts and that leaves half of the teams without work, the
+// four teams of a block share a head's parts.
+constexpr int kJoinTeams = 4, kJoinThreads = kJoinTeams * kDim / 4, kLongParts = 20;
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    kv16_join_some_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
+                          const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
+  constexpr int kBatch = 4;  // parts that a thread has on their way
+  static_assert(kMaxParts <= kJoinThreads && 32 % (kJoinTeams * kBatch) == 0, "a thread an entry, whole batches a warp's weights");
+  __shared__ Parts list[kMaxParts];
+  __shared__ int count[kMaxParts / 32];
+  __shared__ float4 acc_s[kJoinTeams - 1][kDim / 4];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int4 at = tid > 0 && tid < blocks ? parts_of[tid] : make_int4(-1, 0, 0, 0);
+  const uint32_t has = __ballot_sync(0xffffffffu, reached(at));
+  if (lane == 0 && warp < kMaxParts / 32) count[warp] = __popc(has);
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxParts / 32; ++k) {
+    before += k < warp ? count[k] : 0;
+    total += count[k];
+  }
+  bool is_long = false;
+  if (reached(at)) {
+    const Parts ps = parts_at(at, tid);
+    is_long = ps.n > kLongParts;
+    list[before + __popc(has & ((1u << lane) - 1u))] = ps;
+  }
+  const int units = total * kHq, team = tid / (kDim / 4), lane4 = tid % (kDim / 4);
+  const bool share = __syncthreads_or(is_long) && 2 * units <= (int)gridDim.x * kJoinTeams;
+  const int step = share ? kJoinTeams : 1, first = share ? team : 0;  // a thread's parts are first + step * j
+#pragma unroll 1
+  for (int u = share ? blockIdx.x : blockIdx.x * kJoinTeams + team; u < units; u += gridDim.x * (kJoinTeams / step)) {
+    const Parts ps = list[u / kHq];
+    const int h = u % kHq;
+    const float4* src = reinterpret_cast<const float4*>(part + h * kDim) + lane4;
+    const float* st = stat + h;
+    float4 o[kBatch];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = first + step * (j0 + i);
+        if (k < ps.n) o[i] = src[ps.no(k) * (kPartFloats / 4)];
+      }
+    };
+    load(0);
+    // every warp of the team works out the statistics, a lane a part
+    const float sink = sinks ? sinks[h] * kLog2e : -INFINITY;
+    float m0 = kNone, r = 0.f, l = 0.f;
+    if (lane < ps.n) {
+      const float* s0 = st + ps.no(lane) * kStatFloats;
+      r = s0[0];
+      l = s0[kHq];
+      m0 = s0[2 * kHq];
+    }
+    float mx = m0;
+    for (int k = lane + 32; k < ps.n; k += 32) mx = fmaxf(mx, st[ps.no(k) * kStatFloats + 2 * kHq]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float f = exp2f(m0 - mx);
+    r *= f;
+    l *= f;
+    for (int k = lane + 32; k < ps.n; k += 32) {
+      const float* sk = st + ps.no(k) * kStatFloats;
+      const float fk = exp2f(sk[2 * kHq] - mx);
+      r += fk * sk[0];
+      l += fk * sk[kHq];
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      r += __shfl_xor_sync(0xffffffffu, r, d);
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+    }
+    const Joined j = join_head(mx, r, l, sink);
+    if (lse && lane4 == 0 && first == 0) lse[(int64_t)ps.token * kHq + h] = j.lse;
+    Sum4 acc;
+#pragma unroll 1
+    for (int j0 = 0; step * j0 < ps.n; j0 += kBatch) {  // as often for all teams of a block that share a head
+      const int base = step * j0;
+      if (j0 > 0) load(j0);
+      if (j0 > 0 && base % 32 == 0)  // the weights of the next 32 parts
+        f = base + lane < ps.n ? exp2f(st[ps.no(base + lane) * kStatFloats + 2 * kHq] - mx) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = first + base + step * i;
+        const float w = __shfl_sync(0xffffffffu, f, k % 32);
+        if (k < ps.n) acc.add(w, o[i]);
+      }
+    }
+    if (share) {
+      if (team > 0) acc_s[team - 1][lane4] = acc.v;
+      __syncthreads();
+      if (team == 0) {
+#pragma unroll
+        for (int k = 0; k < kJoinTeams - 1; ++k) acc.add(1.f, acc_s[k][lane4]);
+      }
+      __syncthreads();  // read: the next head's may go there
+      if (team > 0) continue;
+    }
+    acc.store<kBf16>(j.own, out + ((int64_t)ps.token * kHq + h) * kDim + 4 * lane4);
+  }
+}
+
+// More tokens (two or three parts each): a block per boundary between two blocks and eight heads, whose teams of 128
+// threads take two heads each.
+constexpr int kManyHeads = 2 * kJoinTeams;
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv16_join_many_kernel(const int4* __restrict__ parts_of, const float* __restrict__ part, const float* __restrict__ stat,
+                          const float* __restrict__ sinks, uint16_t* out, float* lse) {
+  constexpr int kEarly = 2;  // parts of a head that a thread loads before their weights are there
+  __shared__ float weight[kManyHeads][kMaxParts], own_s[kManyHeads];
+  pdl_wait();
+  pdl_trigger();
+  const int4 at = parts_of[blockIdx.x + 1];
+  if (!reached(at)) return;
+  const Parts ps = parts_at(at, blockIdx.x + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h0 = blockIdx.y * kManyHeads;
+  const int team = threadIdx.x / (kDim / 4), lane4 = threadIdx.x % (kDim / 4);
+  const float4* src = reinterpret_cast<const float4*>(part + (h0 + team) * kDim) + lane4;  // of the first head
+  float4 early[2][kEarly];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+      if (k < ps.n) early[q][k] = src[ps.no(k) * (kPartFloats / 4) + q * kJoinTeams * (kDim / 4)];
+  if (warp < kManyHeads) {
+    const int h = h0 + warp;
+    float mx = kNone, r = 0.f, l = 0.f;
+    for (int k = lane; k < ps.n; k += 32) mx = fmaxf(mx, stat[ps.no(k) * kStatFloats + 2 * kHq + h]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    for (int k = lane; k < ps.n; k += 32) {
+      const float* st = stat + ps.no(k) * kStatFloats + h;
       const float f = exp2f(st[2 * kHq] - mx);
       weight[warp][k] = f;
       r += f * st[0];
@@ -1121,53 +1306,28 @@ __global__ void __launch_bounds__(kGroups * kTeams * kDim / 4 / kDimBlocks)
     if (lane == 0) {
       const Joined j = join_head(mx, r, l, sinks ? sinks[h] * kLog2e : -INFINITY);
       own_s[warp] = j.own;
-      if (lse && blockIdx.z == 0) lse[(int64_t)at.x * kHq + h] = j.lse;
+      if (lse) lse[(int64_t)ps.token * kHq + h] = j.lse;
     }
   }
   __syncthreads();
-  float4 acc[kRounds];
+  Sum4 acc[2];
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int q, int k, const float4& o) {
-    const float f = weight[q * kTeams + team][k];
-    acc[q].x += f * o.x;
-    acc[q].y += f * o.y;
-    acc[q].z += f * o.z;
-    acc[q].w += f * o.w;
-  };
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q) {
+    for (int k = 0; k < kEarly; ++k)
+      if (k < ps.n) acc[q].add(weight[q * kJoinTeams + team][k], early[q][k]);
+#pragma unroll 4
+  for (int k = kEarly; k < ps.n; ++k) {
+    float4 o[2];
 #pragma unroll
-    for (int j = 0; j < kEarly; ++j)
-      if (group + j * kGroups < n) add(q, group + j * kGroups, early[q][j]);
-  }
-#pragma unroll(kRounds > 1 ? 4 : 8)
-  for (int k = group + kEarly * kGroups; k < n; k += kGroups) {
-    float4 o[kRounds];
+    for (int q = 0; q < 2; ++q) o[q] = src[ps.no(k) * (kPartFloats / 4) + q * kJoinTeams * (kDim / 4)];
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) o[q] = src[part_no(k) * (kPartFloats / 4) + q * kTeams * (kDim / 4)];
-#pragma unroll
-    for (int q = 0; q < kRounds; ++q) add(q, k, o[q]);
-  }
-  if constexpr (kGroups > 1) {
-    if (group > 0) acc_s[group - 1][lane4] = acc[0];
-    __syncthreads();
-    if (group > 0) return;
-#pragma unroll
-    for (int k = 0; k < kGroups - 1; ++k) {
-      const float4 o = acc_s[k][lane4];
-      acc[0].x += o.x;
-      acc[0].y += o.y;
-      acc[0].z += o.z;
-      acc[0].w += o.w;
-    }
+    for (int q = 0; q < 2; ++q) acc[q].add(weight[q * kJoinTeams + team][k], o[q]);
   }
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q) {
-    const int hs = q * kTeams + team;  // the head among the block's
-    const float own = own_s[hs];
-    const uint32_t lo = pack16<kBf16>(acc[q].x * own, acc[q].y * own), hi = pack16<kBf16>(acc[q].z * own, acc[q].w * own);
-    *reinterpret_cast<uint2*>(out + ((int64_t)at.x * kHq + h0 + hs) * kDim + 4 * x) = make_uint2(lo, hi);
+  for (int q = 0; q < 2; ++q) {
+    const int hs = q * kJoinTeams + team;  // the head among the block's
+    acc[q].store<kBf16>(own_s[hs], out + ((int64_t)ps.token * kHq + h0 + hs) * kDim + 4 * lane4);
   }
 }
 
@@ -1242,17 +1402,18 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
       return DS4X_ERR_CUDA;
     count_launch();
     if (grid > 1 && a.max_rows > kUnsplitRows) {
-      auto join = [&](auto kernel, dim3 blocks, int threads) {
-        return launch_pdl(kernel, blocks, dim3(threads), 0, stream, (const int4*)p.parts_of, grid, (const float*)p.part,
-                          (const float*)p.stat, p.sinks, p.out, p.lse);
-      };
+      const int4* of = p.parts_of;
+      const float *part = p.part, *stat = p.stat;
       cudaError_t e;
-      if (4 * p.T < grid && p.T < 8)  // few tokens: four blocks a head fill more of the GPU
-        e = join(kv16_combine_kernel<kBf16, true, 8, 1, 1, 4>, dim3(p.T, kHq, 4), 256);
-      else if (4 * p.T < grid)
-        e = join(kv16_combine_kernel<kBf16, true, 4, 1, 1, 1>, dim3(p.T, kHq), 512);
+      if (p.T < kFewTokens)
+        e = launch_pdl(kv16_join_few_kernel<kBf16>, dim3(p.T, kHq, kFewBlocks), dim3(kFewThreads), 0, stream, of, grid, part,
+                       stat, p.sinks, p.out, p.lse);
+      else if (p.T < grid)
+        e = launch_pdl(kv16_join_some_kernel<kBf16>, dim3(2 * device_sm_count()), dim3(kJoinThreads), 0, stream, of, grid,
+                       part, stat, p.sinks, p.out, p.lse);
       else
-        e = join(kv16_combine_kernel<kBf16, false, 1, 4, 2, 1>, dim3(grid - 1, kHq / 8), 512);
+        e = launch_pdl(kv16_join_many_kernel<kBf16>, dim3(grid - 1, kHq / kManyHeads), dim3(kJoinThreads), 0, stream, of,
+                       part, stat, p.sinks, p.out, p.lse);
       if (e != cudaSuccess) return DS4X_ERR_CUDA;
       count_launch();
     }

@@ -404,6 +404,29 @@ def test_attn_splits(T, rows):
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("rows", [
+    [3000] * 4,                       # two dozen parts a token
+    [1, 20000, 300, 5, 9000] + [64] * 4,
+    [5 * 3 ** (i % 9) for i in range(40)],
+    [1000] * 9 + [20000] + [300] * 120,   # fewer tokens than blocks, one of them over most of these
+    [70] * 100 + [9000] + [260] * 120,    # more tokens than blocks, one of them over several
+    [33000, 5],
+], ids=["even", "two-long", "ragged", "one-over-many", "one-among-many", "long-and-short"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attn_parts(rows, dtype):
+    """However many parts a token has, and however many tokens have some: out and lse are whole, and the same again."""
+    rng = np.random.default_rng(len(rows))
+    T = len(rows)
+    pool = Pool(rng, rows, 64, dtype)
+    q = queries(rng, T, dtype)
+    opts = options(rng, T, dtype, sinks=True, cap=True)
+    out, lse = run_attn(q, pool, opts, {})
+    longest = int(np.argmax(rows))
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, {}, tokens={0, longest, max(longest - 1, 0), *range(1, T, max(1, T // 6)), T - 1})
+    again, lse2 = run_attn(q, pool, opts, {})
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
 def test_attn_chunk_of_many_tokens():
     """More tokens than one launch plans for, over a causal chunk."""
     rng = np.random.default_rng(6)
