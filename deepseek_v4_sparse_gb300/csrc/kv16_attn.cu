@@ -265,6 +265,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// cap tanh y from v = 2 y log2 e: tanh y = 1 - 2 / (e^2y + 1), off by some 2^-21 of the cap, which is less than 2^-13
+// up to kNearCap.  Above, where |y| < 1/4, the logit x times the series of tanh y / y: 1 - y^2 / 3 +
+// 2 y^4 / 15 - 17 y^6 / 315, off by 62 / 2835 y^8 < 2^-21 of x itself.
+constexpr float kNearCap = 256.f;
+__device__ __forceinline__ float cap_near(float v, float cap) {
+  return fmaf(-2.f * cap, rcp_approx(ex2_approx(v) + 1.f), cap);
+}
+__device__ __forceinline__ float cap_wide(float x, float v, float cap) {
+  constexpr float kY = 0.5f / kLog2e;  // y = v kY
+  const float z = (v * kY) * (v * kY);
+  const float s = fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f);
+  return fabsf(v) < 0.25f / kY ? fmaf(x * z, s, x) : cap_near(v, cap);
+}
 // A head's rows (offset m in log2 units, sums r of the rounded and l of the exact weights 2^(x - m)) and its sink:
 // the factor of the unnormalised sums, and lse.
 struct Joined {
@@ -282,7 +295,9 @@ __device__ __forceinline__ float first_weight(float lse) {
   return lse == -INFINITY ? 0.f : ex2_approx(lse * kLog2e - first_offset(lse));
 }
 
-template <bool kBf16>
+// kWide: for caps above kNearCap.  An instantiation of its own: the series beside the rest made every other call wait for
+// instructions (documents of 1021 tokens 129 instead of 112 us).
+template <bool kBf16, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     kv16_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   constexpr float kRescale = kBf16 ? 32.f : 11.f;  // log2 of what a logit may exceed its head's maximum by
@@ -475,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll 1
           for (int pr = 0; pr < kPairs; ++pr) {
-            ok = ok && wait_bar_warp(&empty[pr], par, p.status, 118);
+            ok = ok && wait_bar_warp(&empty[pr], par, p.status, 119);
             if (mine && ok) {
               const uint32_t to = b * kBufBytes + pr * 2 * kSlotBytes;
 #pragma unroll
@@ -710,7 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
     const bool capped = p.cap > 0.f, sloped = p.slopes != nullptr;
     const float scale2 = p.scale * kLog2e;
-    const float cap2 = p.cap * kLog2e, in_cap = capped ? 2.f * kLog2e * (p.scale / p.cap) : 0.f;
+    // the cap in log2 units, and what takes a product to log2 of e^2y, y = x / cap: finite for any cap
+    const float cap2 = fminf(p.cap * kLog2e, -0.25f * kNone);
+    const float in_cap = capped ? fminf(fmaxf(2.f * kLog2e * (p.scale / p.cap), kNone), -kNone) : 0.f;
     const float slopeA = sloped ? p.slopes[hA] * kLog2e : 0.f, slopeB = sloped ? p.slopes[hB] * kLog2e : 0.f;
     uint32_t g = 0, item = 0;
     // a wait that gave up is acted on where the eight warps meet, so that they leave together
@@ -743,9 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[b]);
         // logits in log2 units
-        if (capped) {  // tanh y = 1 - 2 / (e^2y + 1)
+        if (capped) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.f * cap2, rcp_approx(ex2_approx(x[i] * in_cap) + 1.f), cap2);
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (kWide) x[i] = cap_wide(x[i] * scale2, x[i] * in_cap, cap2);
+            else x[i] = cap_near(x[i] * in_cap, cap2);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] *= scale2;
@@ -1352,9 +1372,10 @@ size_t kv16_attn_workspace_bytes(int T, int max_rows) {
   return kHeadBytes + (size_t)2 * grid * (kPartFloats + kStatFloats) * sizeof(float);
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kWide>
 static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
-  if (ensure_dynamic_smem(kv16_attn_kernel<kBf16>, kSmem) != cudaSuccess) return DS4X_ERR_CUDA;
+  const auto kernel = kv16_attn_kernel<kBf16, kWide>;
+  if (ensure_dynamic_smem(kernel, kSmem) != cudaSuccess) return DS4X_ERR_CUDA;
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return DS4X_ERR_CUDA;
   Params p;
@@ -1398,7 +1419,7 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return DS4X_ERR_CUDA;
-    if (launch_pdl(kv16_attn_kernel<kBf16>, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, tq, p) != cudaSuccess)
+    if (launch_pdl(kernel, dim3(grid), dim3(kThreads), (size_t)kSmem, stream, tq, p) != cudaSuccess)
       return DS4X_ERR_CUDA;
     count_launch();
     if (grid > 1 && a.max_rows > kUnsplitRows) {
@@ -1422,7 +1443,8 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
 }
 
 int launch_kv16_attn(const Kv16AttnArgs& a, cudaStream_t stream) {
-  return a.bf16 ? launch_typed<true>(a, stream) : launch_typed<false>(a, stream);
+  if (a.cap > kNearCap) return a.bf16 ? launch_typed<true, true>(a, stream) : launch_typed<false, true>(a, stream);
+  return a.bf16 ? launch_typed<true, false>(a, stream) : launch_typed<false, false>(a, stream);
 }
 
 }  // namespace ds4x

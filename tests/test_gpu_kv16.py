@@ -185,7 +185,9 @@ def tolerance(x, kv, w, out, dtype, cap):
     logit, ex = x
     u = torch.finfo(DT[dtype]).eps / 2
     size = np.where(np.isfinite(logit), np.abs(logit), 0).max(axis=1, initial=0.0)
-    ex = ex + 2.0 ** -20 + 2.0 ** -22 * size + cap * 2.0 ** -20
+    # capped, a logit is off by 2^-21 of the cap (2 / (e^2y + 1), each of its three steps by 2^-22 at most) up to a cap of
+    # 256.  Above, by as much where it is over 0.24 of the cap, that is by 2^-18.9 of itself, and by less elsewhere
+    ex = ex + 2.0 ** -20 + (2.0 ** -18.5 if cap > 256 else 2.0 ** -22) * size + (cap * 2.0 ** -20 if cap <= 256 else 0.0)
     eta = 2 * (u + 2 * ex)
     spread = np.stack([w[h] @ np.abs(kv[h] - out[h][None, :]) for h in range(w.shape[0])])
     tiny = kv.shape[1] * 2.0 ** -25 * np.abs(kv).max(initial=0.0) * (dtype == "f16")
@@ -296,6 +298,17 @@ def test_attn_options(opt, dtype):
     opts = options(rng, 6, dtype, **{k: True for k in opt.split()})
     out, lse = run_attn(q, pool, opts, {})
     check_attn(q, pool, out, lse, dtype, SCALE, opts, {})
+
+
+@pytest.mark.parametrize("cap", [1e-42, 1e-30, 0.3, 20.0, 255.0, 257.0, 5e3, 1e7, 1e30, 3.4e38])
+def test_attn_cap(cap):
+    """Caps from none of the logits to all of them: a large one leaves them as they are, to fp32's last places."""
+    rng = np.random.default_rng(6)
+    pool = Pool(rng, [500, 90], 16, "f16", size=3.0)
+    q = queries(rng, 2, "f16", size=8.0)
+    opts = dict(cap=float(np.float32(cap)))
+    out, lse = run_attn(q, pool, opts, {})
+    check_attn(q, pool, out, lse, "f16", SCALE, opts, {})
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
