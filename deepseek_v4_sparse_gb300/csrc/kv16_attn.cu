@@ -295,9 +295,11 @@ __device__ __forceinline__ float first_weight(float lse) {
   return lse == -INFINITY ? 0.f : ex2_approx(lse * kLog2e - first_offset(lse));
 }
 
-// kWide: for caps above kNearCap.  An instantiation of its own: the series beside the rest made every other call wait for
-// instructions (documents of 1021 tokens 129 instead of 112 us).
-template <bool kBf16, bool kWide>
+// What becomes of a product: scaled only; capped (up to kNearCap), with a slope, or both; or with a larger cap.  A kernel
+// each, since one for all waits for instructions (512 tokens over 8192 rows 540 instead of 531 us, and
+// with the series of large caps documents of 1021 tokens 129 instead of 110).
+enum Logits { kPlain, kBiased, kWide };
+template <bool kBf16, Logits kLogits>
 __global__ void __launch_bounds__(kThreads, 1)
     kv16_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   constexpr float kRescale = kBf16 ? 32.f : 11.f;  // log2 of what a logit may exceed its head's maximum by
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g8 = lane >> 2, e = lane & 3;
     const int hA = 16 * quad + g8, hB = hA + 8;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-    const bool capped = p.cap > 0.f, sloped = p.slopes != nullptr;
+    const bool capped = kLogits != kPlain && p.cap > 0.f, sloped = kLogits != kPlain && p.slopes != nullptr;
     const float scale2 = p.scale * kLog2e;
     // the cap in log2 units, and what takes a product to log2 of e^2y, y = x / cap: finite for any cap
     const float cap2 = fminf(p.cap * kLog2e, -0.25f * kNone);
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (capped) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if constexpr (kWide) x[i] = cap_wide(x[i] * scale2, x[i] * in_cap, cap2);
+            if constexpr (kLogits == kWide) x[i] = cap_wide(x[i] * scale2, x[i] * in_cap, cap2);
             else x[i] = cap_near(x[i] * in_cap, cap2);
           }
         } else {
@@ -1372,9 +1374,9 @@ size_t kv16_attn_workspace_bytes(int T, int max_rows) {
   return kHeadBytes + (size_t)2 * grid * (kPartFloats + kStatFloats) * sizeof(float);
 }
 
-template <bool kBf16, bool kWide>
+template <bool kBf16, Logits kLogits>
 static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
-  const auto kernel = kv16_attn_kernel<kBf16, kWide>;
+  const auto kernel = kv16_attn_kernel<kBf16, kLogits>;
   if (ensure_dynamic_smem(kernel, kSmem) != cudaSuccess) return DS4X_ERR_CUDA;
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return DS4X_ERR_CUDA;
@@ -1443,8 +1445,9 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
 }
 
 int launch_kv16_attn(const Kv16AttnArgs& a, cudaStream_t stream) {
-  if (a.cap > kNearCap) return a.bf16 ? launch_typed<true, true>(a, stream) : launch_typed<false, true>(a, stream);
-  return a.bf16 ? launch_typed<true, false>(a, stream) : launch_typed<false, false>(a, stream);
+  if (a.cap > kNearCap) return a.bf16 ? launch_typed<true, kWide>(a, stream) : launch_typed<false, kWide>(a, stream);
+  if (a.cap > 0.f || a.slopes) return a.bf16 ? launch_typed<true, kBiased>(a, stream) : launch_typed<false, kBiased>(a, stream);
+  return a.bf16 ? launch_typed<true, kPlain>(a, stream) : launch_typed<false, kPlain>(a, stream);
 }
 
 }  // namespace ds4x
