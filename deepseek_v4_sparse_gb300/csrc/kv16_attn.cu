@@ -18,8 +18,8 @@
 //
 // Warps: 0-3 copy rows (16-byte cp.async; 16 rows each, one step of the O^T products), 4-11 softmax (16 heads by
 // quadrant and half of the rows each, 4 threads a head), 12-27 write the output (O^T lanes by quadrant, a quarter
-// of the dims each), 28 issues the S products, 29 the O^T products, 30 looks up the rows' slots a few chunks ahead, 31 loads
-// q and works out what the heads' output needs.
+// of the dims each), 28 issues the S products, 29 the O^T products, 30 looks up the rows' slots a few chunks ahead, 31
+// loads q and works out what the heads' output needs.
 // Buffers are copied and released in quarters of the dims, O^T rotates over six 64-column TMEM
 // slots (a token uses four), so neighbouring tokens overlap.  A chunk that is not full costs its O^T products and
 // copies by 16 rows.  The other attention's output is where a token's sums begin: the output warps put it, times
@@ -30,6 +30,16 @@
 // fp16's largest value and small ones away from its least.  Statistics and sums are fp32.  Weights are rounded to the
 // rows' type, which the matrix unit asks for (8 bits in bf16); out is normalised by the sum of the rounded weights, so
 // that what a weight's rounding does to a row it does to the normaliser too; lse takes the exact ones.
+//
+// What bounds it.  A chunk's products read q, K, V and (four times) P from shared memory at 128 bytes a clock: 1792
+// clocks for 8.4 MFLOP, the accesses of the warps 440 more, of 2380 a chunk (512 tokens over 8192 rows, 531 us: 1003
+// TFLOP/s, that path busy in 91 % of the cycles, the tensor pipe in 63 %).  M = 64 is why: a product of 64 heads reads as
+// many bytes for q as for K, and two tokens at once (M = 128) would need 128 KB for q and all 512 TMEM columns for O^T.
+// Decode tokens are bound by HBM in the long run (152 over 4096 rows each 113 us, 5.8 TB/s; 6.4 TB/s from 2048 to
+// 4096 rows), which takes 64 KB chunks in two buffers; about 16 us are not: the plan 2, slots and first rows 4 to 6, the
+// last chunk's way through the roles 3, parts and their joining 6 to 10.
+// Rows come by cp.async, not by TMA boxes of whole chunks: a quarter's copy is on the way product -> free -> copy ->
+// product, and boxes take twice as long to land (750 us).  One buffer of 128 rows: 750 us too.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -57,16 +67,21 @@ constexpr int kTokens = 2048;                    // tokens a launch plans for
 constexpr int kSoftWarp = 4, kOutWarp = 12, kSWarp = 28, kOWarp = 29, kSlotWarp = 30, kQWarp = 31;
 constexpr int kCopyWarps = 4, kSoftWarps = 8, kOutWarps = 16;
 constexpr int kWarps = 32, kThreads = 32 * kWarps;
-// registers a thread: 64 at launch; the sum over the eight warpgroups stays what it was
+// registers a thread: 64 at launch; the sum over the eight warpgroups stays within that
 constexpr int kLaunchRegs = 64, kCopyRegs = 56, kMiscRegs = 40, kSoftRegs = 80;  // and 64 for the output
 static_assert(kCopyRegs < kLaunchRegs && kMiscRegs < kLaunchRegs && kSoftRegs > kLaunchRegs, "dec, dec and inc below");
-static_assert(kThreads * kLaunchRegs <= 65536 && kCopyRegs + 2 * kSoftRegs + 4 * kLaunchRegs + kMiscRegs <= 8 * kLaunchRegs, "registers");
+static_assert(kThreads * kLaunchRegs <= 65536, "registers");
+static_assert(kCopyRegs + 2 * kSoftRegs + 4 * kLaunchRegs + kMiscRegs <= 8 * kLaunchRegs, "registers of the warpgroups");
 constexpr int kRing = 4, kMaskRing = 8;          // chunks whose slots, and masks, are looked up ahead
 // Chunks of a token that are added up in one go: the matrix unit truncates its fp32 sums, over 16384 rows without
 // a trace, over 262144 of one sign by 0.14 %.  Longer lists are joined with rounded sums.
 constexpr int kItemChunks = 256;
+// What a token costs beside its chunks, in chunks (61 tokens of 5 to 32768 rows: none 68.7 us, 2 and 3 64.8, 4 65.9; 400
+// of 20 to 4000: 2 86.7, 3 89, 4 92).
 constexpr int kTokenUnits = 2;
-constexpr int kWholeChunks = 4;                  // chunks of a token that no boundary divides
+// Chunks of a token that no boundary divides: parts cost two more trips through L2 and a launch (256 tokens of two
+// chunks over 152 blocks: 17 us, and 22 with boundaries that divide them).
+constexpr int kWholeChunks = 4;
 constexpr int kOSlots = 6;                       // O^T slots of 64 TMEM columns
 constexpr int kOffKV = kQBytes;
 constexpr int kOffP = kOffKV + 2 * kBufBytes;
@@ -77,11 +92,12 @@ constexpr int kOffAhead = kOffMask + kMaskRing * 8;    // int[kMaskRing]: e - hi
 // float[2 items][2 halves of the rows' sums of rounded weights, 2 halves' sums, offset][64]
 constexpr int kOffStat = kOffAhead + kMaskRing * 4;
 constexpr int kOffMax = kOffStat + 2 * 5 * kHq * 4;    // float[2 halves of the rows][64]: maxima of one chunk
-constexpr int kOffJoin = kOffMax + 2 * kHq * 4;  // float[2 items][2][64]: factors of a token's sums so far, of an item's
-                                                 // sums; [3 items][64]: of the other output that the sums begin with
-constexpr int kOffScan = kOffJoin + 7 * kHq * 4; // int64[kWarps] warp sums and [2] chunks before the block and to its end,
-                                                 // then int[4]: the block's part, and the last chunk (+ 1) in which a
-                                                 // maximum moved
+// float[2 items][2][64]: factors of a token's sums so far, of an item's sums; [3 items][64]: of the other output that
+// the sums begin with
+constexpr int kOffJoin = kOffMax + 2 * kHq * 4;
+// int64[kWarps] warp sums and [2] chunks before the block and to its end, then int[4]: the block's part, and the last
+// chunk (+ 1) in which a maximum moved
+constexpr int kOffScan = kOffJoin + 7 * kHq * 4;
 constexpr int kOffBars = kOffScan + (kWarps + 2) * 8 + 16;
 constexpr int kNumBars = 2 + 2 * kRing + 2 * 2 * kPairs + 5 * 2 + 3 * kOSlots + 4 * 2;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
@@ -163,7 +179,8 @@ __device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a, uint32_t b, ui
 }
 template <int kDst, int kSrc>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc)
+               : "memory");
 }
 template <int kDst>
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -223,10 +240,10 @@ struct Walk {
   }
 };
 
-// An item among its token's: the block's first of the token (`from` its first chunk), the block's last, all of the token.
+// An item among its token's: the block's first of the token (`from` its first chunk), the block's last, all of it.
 struct ItemPart {
   bool begins, ends, whole, joins;  // joins: one of several, whose sums are added to those so far
-  int64_t part;                     // chunks before the block, or behind it: the sums go to the block's first or second part
+  int64_t part;  // chunks before the block, or behind it: the sums go to the block's first or second part
   __device__ __forceinline__ ItemPart(const Walk& w, uint32_t item, int& from) {
     if (w.c0 == 0 || item == 0) from = w.c0;
     begins = w.c0 == from;
@@ -256,9 +273,13 @@ __device__ __forceinline__ float from16(uint16_t u) {
 template <bool kBf16>
 __device__ __forceinline__ void add_pair(float& a, uint32_t u) {
   if constexpr (kBf16)
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}" : "+f"(a) : "r"(u));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %0, hi, %0;\n\t}"
+        : "+f"(a)
+        : "r"(u));
   else
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %0, hi, %0;\n\t}" : "+f"(a) : "r"(u));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %0, hi, %0;\n\t}"
+        : "+f"(a)
+        : "r"(u));
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -354,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar, bar >= slempty && bar < kvfull ? kCopyWarps
                    : bar >= kvfull && bar < kvempty ? 32 * kCopyWarps
                    : bar >= sfull && bar < sempty ? 2  // the products' completion and the issuing warp itself
-                   : (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || (bar >= lready && bar < lfree) ? kSoftWarps
+                   : (bar >= sempty && bar < pempty) || (bar >= looked && bar < ofull) || (bar >= lready && bar < lfree)
+                       ? kSoftWarps
                    : bar >= ffree ? kOutWarps : bar >= oempty && bar < lready ? kOutWarps / kPairs : 1);
     fence_mbarrier_init();
   }
@@ -886,7 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         lB += sB;
         {
           // P's buffer is free: S of this chunk needed rows that were copied over those of two chunks ago, when O^T had
-          // taken all of them and their weights.  P[h][j], K-major with the 128-byte swizzle: 16-byte chunk k of line h at (k ^ (h & 7)); hA and hB alike
+          // taken all of them and their weights.  P[h][j], K-major with the 128-byte swizzle: 16-byte piece k of line h
+          // at k ^ (h & 7), the same for hA and hB.
           uint8_t* line = sp + b * kPBytes + hA * 128 + 4 * e;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -1099,6 +1122,10 @@ struct Sum4 {
   }
 };
 
+// Three ways of joining, by the number of tokens (us of the whole call, bf16):
+//   1 token over 9728 / 120001 rows: few 15.6 / 38.6, some 32 / 42
+//   4 tokens of 3000, 12 of 700, 37 of 3000: some 16.4, 15.8, 39.8, few 19.6, 20.7, 60 (blocks a token and head)
+//   404 capped tokens, 400 of 20 to 4000 rows: many 79.8, 85.7, some 82.8, 87.3
 // Under 4 tokens (one may have a part of every block): a block per token, head and quarter of the dims, eight groups of
 // 32 threads that take the parts in turn.
 constexpr int kFewTokens = 4, kFewGroups = 8, kFewBlocks = 4, kFewThreads = kFewGroups * kDim / 4 / kFewBlocks;
@@ -1179,7 +1206,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 // Fewer tokens than blocks: two blocks an SM list the tokens that have parts, and their teams of 128 threads take a head
 // of a token each in turn.  Where a token has more than kLongParts and that leaves half of the teams without work, the
-// four teams of a block share a head's parts.
+// four teams of a block share a head's parts (12 tokens of 50 to 30000 rows 33.5 us, apart 38.6; but 8 of 8192, of
+// 20 parts each, 31.0 and 30.3).
 constexpr int kJoinTeams = 4, kJoinThreads = kJoinTeams * kDim / 4, kLongParts = 20;
 template <bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads, 2)
