@@ -1,4 +1,8 @@
 """The paged 16-bit cache on the GPU against its plain implementation in 64 bits (oracle/kv16.py)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -573,6 +577,59 @@ def test_captured_step_and_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def capture_after_another_call():
+    """A short call, then captures of calls that take other kernels: more types, caps, and every way of joining."""
+    rng = np.random.default_rng(14)
+    for dtype in ("bf16", "f16"):
+        small = Pool(rng, [5], 16, "bf16")
+        ds4x.kv16_attn(queries(rng, 1, "bf16"), *small.dev, 16)
+        for T, rows, cap in ((1, 3000, 0.0), (9, 1200, 0.7), (200, 300, 900.0)):
+            pool = Pool(rng, [rows] * T, 64, dtype)
+            q = queries(rng, T, dtype)
+            x, f, pos = torch.zeros((T, 512), dtype=q.dtype, device="cuda"), gpu(frequencies(64)), i32([7] * T)
+            slots = i32([-1] * T)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                ds4x.kv16_append(x, slots, pool.dev[0], positions=pos, inv_freq=f)
+                got = ds4x.kv16_attn(ds4x.rotate(q, pos, f), *pool.dev, 64, cap=cap)
+            g.replay()
+            torch.cuda.synchronize()
+            want = ds4x.kv16_attn(ds4x.rotate(q, pos, f), *pool.dev, 64, cap=cap)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (dtype, T)
+    assert ds4x.device_status() == ds4x.OK
+
+
+def test_capture_after_another_call():
+    """In a process of its own, whose kernels no other test has brought to the device."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = "from tests.test_gpu_kv16 import capture_after_another_call as f; f()"
+    got = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0, got.stderr[-2000:]
+
+
+def test_graphs_that_share_a_workspace():
+    """Nothing is kept in it: two captured graphs use one in turn."""
+    rng = np.random.default_rng(15)
+    pools = [Pool(rng, [2500] * 3, 64, "bf16"), Pool(rng, [700] * 30, 64, "bf16")]
+    qs = [queries(rng, 3, "bf16"), queries(rng, 30, "bf16")]
+    work = torch.full((max(ds4x.kv16_attn_workspace_bytes(len(q), p.max_pages * 64) for q, p in zip(qs, pools)),), 0xff,
+                      dtype=torch.uint8, device="cuda")
+    want = [ds4x.kv16_attn(q, *p.dev, 64) for q, p in zip(qs, pools)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for q, p in zip(qs, pools):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(ds4x.kv16_attn(q, *p.dev, 64, workspace=work))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        got[i][0].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
 
 
 def test_a_serving_step_of_both_caches():
