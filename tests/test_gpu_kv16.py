@@ -444,6 +444,19 @@ def test_attn_parts(rows, dtype):
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attn_lists_of_several_items(dtype):
+    """A block with tens of thousands of a token's rows, whole or in part, adds them up in several goes."""
+    rng = np.random.default_rng(17)
+    T, rows = 160, 35000
+    pool = Pool(rng, [rows], 512, dtype)
+    lists = dict(req=np.zeros(T, np.int32), positions=np.arange(rows - T, rows))
+    q = queries(rng, T, dtype)
+    opts = options(rng, T, dtype, sinks=True, slopes=True, other=True)
+    out, lse = run_attn(q, pool, opts, lists)
+    check_attn(q, pool, out, lse, dtype, SCALE, opts, lists, tokens=[0, 80])
+
+
 def test_attn_chunk_of_many_tokens():
     """More tokens than one launch plans for, over a causal chunk."""
     rng = np.random.default_rng(6)
