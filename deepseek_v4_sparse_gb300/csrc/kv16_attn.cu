@@ -1036,10 +1036,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_bar_warp(&ofull[os], ophase(item, db), p.status, 115);
       if (!ok) break;
       tc_fence_after();
+      float v[16];
+      tmem_ld16(t_lane + os * kHq, v);
 #pragma unroll 1
       for (int h = 0; h < kHq; h += 16) {
-        float v[16];
-        tmem_ld16(t_lane + os * kHq + h, v);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -1062,21 +1062,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) sums[i * kDim] = v[i];
           }
         }
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = pack16<kBf16>(v[2 * i], v[2 * i + 1]);
+        if (h + 16 < kHq) {  // on their way while these are stored
+          tmem_ld16(t_lane + os * kHq + h + 16, v);
+        } else {  // the slot and the factors are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&oempty[os]);
+            mbar_arrive(&ffree[par]);
+          }
+        }
         if (it.whole) {
           uint16_t* to_out = p.out + ((int64_t)t * kHq + h) * kDim + d;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const uint32_t u = pack16<kBf16>(v[i], v[i + 1]);
-            to_out[i * kDim] = (uint16_t)u;
-            to_out[(i + 1) * kDim] = (uint16_t)(u >> 16);
+          for (int i = 0; i < 8; ++i) {
+            to_out[2 * i * kDim] = (uint16_t)u[i];
+            to_out[(2 * i + 1) * kDim] = (uint16_t)(u[i] >> 16);
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&oempty[os]);
-        mbar_arrive(&ffree[par]);
       }
       ++item;
       if (p.other && w.left > 0) ok = begin(item, w.t, f_other);
