@@ -310,10 +310,12 @@ __device__ __forceinline__ Joined join_head(float m, float r, float l, float sin
   const float d = fmaf(a, r, s), e = fmaf(a, l, s);
   return Joined{d == 0.f ? 0.f : a / d, e == 0.f ? -INFINITY : (M + log2f(e)) * kLn2};
 }
-// Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output.
+// Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output: 1
+// where the offset is its lowest and lse finite, so that a type's lowest value counts where nothing else does.
 __device__ __forceinline__ float first_offset(float lse) { return fmaxf(lse * kLog2e - kWeightLog2, kNone); }
 __device__ __forceinline__ float first_weight(float lse) {
-  return lse == -INFINITY ? 0.f : ex2_approx(lse * kLog2e - first_offset(lse));
+  if (lse * kLog2e < kNone) return lse < kNone ? 0.f : 1.f;
+  return ex2_approx(lse * kLog2e - first_offset(lse));
 }
 
 // What becomes of a product: scaled only; capped (up to kNearCap), with a slope, or both; or with a larger cap.  A kernel

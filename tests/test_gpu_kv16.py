@@ -504,6 +504,20 @@ def test_attn_nothing_to_see():
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("low", [-1e3, -1e30, float(np.finfo(np.float32).min)])
+def test_attn_other_of_next_to_no_weight(low):
+    """A finite lse as low as the type has counts alone, and for nothing beside rows."""
+    q, pool = torch.randn((2, 64, 512), device="cuda").bfloat16(), torch.randn((32, 512), device="cuda").bfloat16()
+    other = torch.randn((2, 64, 512), device="cuda").bfloat16(), torch.full((2, 64), low, device="cuda")
+    out, lse = ds4x.kv16_attn(q, pool, i32([[0], [1]]), i32([0, 7]), 16, other=other)
+    want, wlse = ds4x.kv16_attn(q, pool, i32([[0], [1]]), i32([0, 7]), 16)
+    assert (out[0].float() - other[0][0].float()).abs().max() <= 2.0 ** -7
+    assert lse[0].max() < 0.6 * low
+    # weights against another offset, each rounded on its own: two half steps of numbers of order one each
+    assert (out[1].float() - want[1].float()).abs().max() <= 4 * 2.0 ** -8 * pool.float().abs().max()
+    assert (lse[1] - wlse[1]).abs().max() <= 2.0 ** -18
+
+
 def test_attn_writes_its_tokens_only():
     rng = np.random.default_rng(2)
     pool = Pool(rng, [300, 200], 16, "f16")
