@@ -300,15 +300,19 @@ __device__ __forceinline__ float cap_wide(float x, float v, float cap) {
   return fabsf(v) < 0.25f / kY ? fmaf(x * z, s, x) : cap_near(v, cap);
 }
 // A head's rows (offset m in log2 units, sums r of the rounded and l of the exact weights 2^(x - m)) and its sink:
-// the factor of the unnormalised sums, and lse.
+// the factor of the unnormalised sums, and lse.  A sink may be as large or as low as fp32 goes, and log2 e times that
+// is beyond it, so both are halved (exactly) until they are subtracted; no rows are -infinity, below any sink.
 struct Joined {
   float own, lse;
 };
-__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink2) {
-  const float M = fmaxf(m, sink2);
-  const float a = exp2f(m - M), s = exp2f(sink2 - M);
+__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink) {
+  const float mh = l == 0.f ? -INFINITY : 0.5f * m, sh = sink * (0.5f * kLog2e);
+  const float M = fmaxf(mh, sh);
+  if (l == 0.f && sink == -INFINITY) return Joined{0.f, -INFINITY};
+  const float a = exp2f(2.f * (mh - M)), s = exp2f(2.f * (sh - M));
   const float d = fmaf(a, r, s), e = fmaf(a, l, s);
-  return Joined{d == 0.f ? 0.f : a / d, e == 0.f ? -INFINITY : (M + log2f(e)) * kLn2};
+  const float lse = (M + 0.5f * log2f(e)) * (2.f * kLn2);  // what rounds beyond fp32 is its last number
+  return Joined{d == 0.f ? 0.f : a / d, isinf(lse) && e < INFINITY ? copysignf(-kNone, lse) : lse};
 }
 // Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output: 1
 // where the offset is its lowest and lse finite, so that a type's lowest value counts where nothing else does.
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sink[2], next[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          sink[i] = it.whole && p.sinks ? __ldg(p.sinks + lane + 32 * i) * kLog2e : -INFINITY;
+          sink[i] = it.whole && p.sinks ? __ldg(p.sinks + lane + 32 * i) : -INFINITY;
           next[i] = begun ? __ldg(p.other_lse + (int64_t)w.t * kHq + lane + 32 * i) : 0.f;
         }
         if (w.left > 0) {
@@ -1192,7 +1196,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       ls += __shfl_xor_sync(0xffffffffu, ls, d);
     }
     if (lane == 0) {
-      const Joined j = join_head(mx, rs, ls, sinks ? sinks[h] * kLog2e : -INFINITY);
+      const Joined j = join_head(mx, rs, ls, sinks ? sinks[h] : -INFINITY);
       own_s = j.own;
       if (lse && blockIdx.z == 0) lse[(int64_t)ps.token * kHq + h] = j.lse;
     }
@@ -1264,7 +1268,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     };
     load(0);
     // every warp of the team works out the statistics, a lane a part
-    const float sink = sinks ? sinks[h] * kLog2e : -INFINITY;
+    const float sink = sinks ? sinks[h] : -INFINITY;
     float m0 = kNone, r = 0.f, l = 0.f;
     if (lane < ps.n) {
       const float* s0 = st + ps.no(lane) * kStatFloats;
@@ -1362,7 +1366,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
     if (lane == 0) {
-      const Joined j = join_head(mx, r, l, sinks ? sinks[h] * kLog2e : -INFINITY);
+      const Joined j = join_head(mx, r, l, sinks ? sinks[h] : -INFINITY);
       own_s[warp] = j.own;
       if (lse) lse[(int64_t)ps.token * kHq + h] = j.lse;
     }

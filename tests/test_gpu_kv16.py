@@ -787,3 +787,41 @@ def test_refusals_on_the_device():
         ds4x.kv16_append(q[0, :2], rows, pool, inv_freq=f)
     with pytest.raises(ds4x.Ds4xError):
         ds4x.rotate(q, rows, f[:0])
+
+
+# --------------------------------------------------------------------- the ends of the ranges
+LOWEST = float(np.finfo(np.float32).min)
+LOW = [LOWEST, -3e38, -2.4e38, -1e38, -1e30, -np.inf]
+HIGH = [1e30, 1e38, 2.3e38, 2.4e38, 3e38, -LOWEST]
+# whole tokens and split ones, joined each of the three ways; the second sees no row
+ENDS = [[40, 0], [3000, 0, 40], [20000, 0] + [300] * 7, [260] * 160]
+
+
+def heads_of(values):
+    return np.float32([values[h % len(values)] for h in range(64)])
+
+
+def ends_pool(rng, rows, dtype):
+    rows = [rows[0], 0, *rows[2:]]
+    return Pool(rng, rows, 64, dtype), queries(rng, len(rows), dtype)
+
+
+def nearly(a, b):
+    """Equal but for a few fp32 steps, infinities too."""
+    b = torch.as_tensor(b, device=a.device).expand_as(a)
+    return bool(((a == b) | ((a.double() - b.double()).abs() <= 2.0 ** -21 * b.double().abs())).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", ENDS, ids=["whole", "few", "some", "many"])
+def test_attn_sinks_at_the_ends_of_fp32(rows, dtype):
+    """A sink of next to no weight is none beside rows and all there is without; one above all logits is all there is."""
+    rng = np.random.default_rng(31)
+    pool, q = ends_pool(rng, rows, dtype)
+    without, wlse = run_attn(q, pool, dict(sinks=heads_of([-np.inf])), {})
+    assert torch.isfinite(wlse[0]).all() and torch.isneginf(wlse[1]).all()
+    out, lse = run_attn(q, pool, dict(sinks=heads_of(LOW)), {})
+    assert torch.equal(out, without)
+    assert torch.equal(lse[0], wlse[0]) and torch.equal(lse[2:], wlse[2:]) and nearly(lse[1], gpu(heads_of(LOW)))
+    out, lse = run_attn(q, pool, dict(sinks=heads_of(HIGH)), {})
+    assert (out == 0).all() and nearly(lse, gpu(heads_of(HIGH)))
