@@ -301,12 +301,19 @@ __device__ __forceinline__ float cap_wide(float x, float v, float cap) {
 }
 // A head's rows (offset m in log2 units, sums r of the rounded and l of the exact weights 2^(x - m)) and its sink:
 // the factor of the unnormalised sums, and lse.  A sink may be as large or as low as fp32 goes, and log2 e times that
-// is beyond it, so both are halved (exactly) until they are subtracted; no rows are -infinity, below any sink.
+// is beyond it, so both are halved (exactly) until they are subtracted; no rows are -infinity, below any sink.  The same of
+// the other attention's lse (at *other, if there is one): where the offset is fp32's lowest or largest number it stands
+// for that lse, beside which no row counts.
 struct Joined {
   float own, lse;
 };
-__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink) {
-  const float mh = l == 0.f ? -INFINITY : 0.5f * m, sh = sink * (0.5f * kLog2e);
+__device__ __forceinline__ const float* other_at(const float* lse, int t, int h) {
+  return lse ? lse + (int64_t)t * kHq + h : nullptr;
+}
+__device__ __forceinline__ Joined join_head(float m, float r, float l, float sink, const float* other) {
+  float mh = l == 0.f ? -INFINITY : 0.5f * m;
+  if (other && fabsf(m) == -kNone && l != 0.f && *other > -INFINITY) mh = *other * (0.5f * kLog2e);
+  const float sh = sink * (0.5f * kLog2e);
   const float M = fmaxf(mh, sh);
   if (l == 0.f && sink == -INFINITY) return Joined{0.f, -INFINITY};
   const float a = exp2f(2.f * (mh - M)), s = exp2f(2.f * (sh - M));
@@ -315,11 +322,12 @@ __device__ __forceinline__ Joined join_head(float m, float r, float l, float sin
   return Joined{d == 0.f ? 0.f : a / d, isinf(lse) && e < INFINITY ? copysignf(-kNone, lse) : lse};
 }
 // Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output: 1
-// where the offset is its lowest and lse finite, so that a type's lowest value counts where nothing else does.
-__device__ __forceinline__ float first_offset(float lse) { return fmaxf(lse * kLog2e - kWeightLog2, kNone); }
+// where the offset is fp32's lowest or largest number and lse finite, so that a type's lowest value counts where nothing
+// else does, and one whose log2 is beyond fp32 alone.
+__device__ __forceinline__ float log2_of(float lse) { return fminf(fmaxf(lse * kLog2e, kNone), -kNone); }
+__device__ __forceinline__ float first_offset(float lse) { return fmaxf(log2_of(lse) - kWeightLog2, kNone); }
 __device__ __forceinline__ float first_weight(float lse) {
-  if (lse * kLog2e < kNone) return lse < kNone ? 0.f : 1.f;
-  return ex2_approx(lse * kLog2e - first_offset(lse));
+  return lse < kNone ? 0.f : ex2_approx(log2_of(lse) - first_offset(lse)) + (lse - lse);  // NaN stays NaN
 }
 
 // What becomes of a product: scaled only; capped (up to kNearCap), with a slope, or both; or with a larger cap.  A kernel
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_far[i] = m;
           }
           if (it.whole) {
-            const Joined j = join_head(m, r, l, sink[i]);
+            const Joined j = join_head(m, r, l, sink[i], other_at(p.other_lse, t, h));
             if (p.lse) p.lse[(int64_t)t * kHq + h] = j.lse;
             f0 *= j.own;
             fi *= j.own;
@@ -1144,7 +1152,8 @@ constexpr int kFewTokens = 4, kFewGroups = 8, kFewBlocks = 4, kFewThreads = kFew
 template <bool kBf16>
 __global__ void __launch_bounds__(kFewThreads, 2)
     kv16_join_few_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
-                         const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
+                         const float* __restrict__ stat, const float* __restrict__ sinks,
+                         const float* __restrict__ other, uint16_t* out, float* lse) {
   constexpr int kLane4 = kDim / 4 / kFewBlocks, kGroups = kFewGroups;
   constexpr int kEarly = 20;  // parts that a thread loads before their weights are there
   __shared__ float weight[kMaxParts], own_s;
@@ -1196,7 +1205,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       ls += __shfl_xor_sync(0xffffffffu, ls, d);
     }
     if (lane == 0) {
-      const Joined j = join_head(mx, rs, ls, sinks ? sinks[h] : -INFINITY);
+      const Joined j = join_head(mx, rs, ls, sinks ? sinks[h] : -INFINITY, other_at(other, ps.token, h));
       own_s = j.own;
       if (lse && blockIdx.z == 0) lse[(int64_t)ps.token * kHq + h] = j.lse;
     }
@@ -1224,7 +1233,8 @@ constexpr int kJoinTeams = 4, kJoinThreads = kJoinTeams * kDim / 4, kLongParts =
 template <bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     kv16_join_some_kernel(const int4* __restrict__ parts_of, int blocks, const float* __restrict__ part,
-                          const float* __restrict__ stat, const float* __restrict__ sinks, uint16_t* out, float* lse) {
+                          const float* __restrict__ stat, const float* __restrict__ sinks,
+                          const float* __restrict__ other, uint16_t* out, float* lse) {
   constexpr int kBatch = 4;  // parts that a thread has on their way
   static_assert(kMaxParts <= kJoinThreads && 32 % (kJoinTeams * kBatch) == 0, "a thread an entry, whole batches a warp's weights");
   __shared__ Parts list[kMaxParts];
@@ -1294,7 +1304,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       r += __shfl_xor_sync(0xffffffffu, r, d);
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
-    const Joined j = join_head(mx, r, l, sink);
+    const Joined j = join_head(mx, r, l, sink, other_at(other, ps.token, h));
     if (lse && lane4 == 0 && first == 0) lse[(int64_t)ps.token * kHq + h] = j.lse;
     Sum4 acc;
 #pragma unroll 1
@@ -1330,7 +1340,7 @@ constexpr int kManyHeads = 2 * kJoinTeams;
 template <bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
     kv16_join_many_kernel(const int4* __restrict__ parts_of, const float* __restrict__ part, const float* __restrict__ stat,
-                          const float* __restrict__ sinks, uint16_t* out, float* lse) {
+                          const float* __restrict__ sinks, const float* __restrict__ other, uint16_t* out, float* lse) {
   constexpr int kEarly = 2;  // parts of a head that a thread loads before their weights are there
   __shared__ float weight[kManyHeads][kMaxParts], own_s[kManyHeads];
   pdl_wait();
@@ -1366,7 +1376,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       l += __shfl_xor_sync(0xffffffffu, l, d);
     }
     if (lane == 0) {
-      const Joined j = join_head(mx, r, l, sinks ? sinks[h] : -INFINITY);
+      const Joined j = join_head(mx, r, l, sinks ? sinks[h] : -INFINITY, other_at(other, ps.token, h));
       own_s[warp] = j.own;
       if (lse) lse[(int64_t)ps.token * kHq + h] = j.lse;
     }
@@ -1470,13 +1480,13 @@ static int launch_typed(const Kv16AttnArgs& a, cudaStream_t stream) {
       cudaError_t e;
       if (p.T < kFewTokens)
         e = launch_pdl(kv16_join_few_kernel<kBf16>, dim3(p.T, kHq, kFewBlocks), dim3(kFewThreads), 0, stream, of, grid, part,
-                       stat, p.sinks, p.out, p.lse);
+                       stat, p.sinks, p.other_lse, p.out, p.lse);
       else if (p.T < grid)
         e = launch_pdl(kv16_join_some_kernel<kBf16>, dim3(2 * device_sm_count()), dim3(kJoinThreads), 0, stream, of, grid,
-                       part, stat, p.sinks, p.out, p.lse);
+                       part, stat, p.sinks, p.other_lse, p.out, p.lse);
       else
         e = launch_pdl(kv16_join_many_kernel<kBf16>, dim3(grid - 1, kHq / kManyHeads), dim3(kJoinThreads), 0, stream, of,
-                       part, stat, p.sinks, p.out, p.lse);
+                       part, stat, p.sinks, p.other_lse, p.out, p.lse);
       if (e != cudaSuccess) return DS4X_ERR_CUDA;
       count_launch();
     }

@@ -825,3 +825,39 @@ def test_attn_sinks_at_the_ends_of_fp32(rows, dtype):
     assert torch.equal(lse[0], wlse[0]) and torch.equal(lse[2:], wlse[2:]) and nearly(lse[1], gpu(heads_of(LOW)))
     out, lse = run_attn(q, pool, dict(sinks=heads_of(HIGH)), {})
     assert (out == 0).all() and nearly(lse, gpu(heads_of(HIGH)))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", ENDS, ids=["whole", "few", "some", "many"])
+def test_attn_other_at_the_ends_of_fp32(rows, dtype):
+    """The same of another attention's log-sum-exp, whose output counts with it."""
+    rng = np.random.default_rng(32)
+    pool, q = ends_pool(rng, rows, dtype)
+    T = len(q)
+    oo = torch.from_numpy(rng.standard_normal((T, 64, 512))).to(DT[dtype]).cuda()
+    with_lse = lambda v: run_attn(q, pool, dict(other=(oo, gpu(heads_of(v)).expand(T, 64).contiguous())), {})  # noqa: E731
+    without, wlse = with_lse([-np.inf])
+    assert torch.isfinite(wlse[0]).all() and torch.isneginf(wlse[1]).all() and (without[1] == 0).all()
+    out, lse = with_lse(LOW)
+    alone = gpu(np.isfinite(heads_of(LOW)))[:, None]
+    seen = [t for t in range(T) if t != 1]
+    assert torch.equal(out[seen], without[seen]) and torch.equal(lse[seen], wlse[seen])
+    assert torch.equal(out[1], torch.where(alone, oo[1], 0)) and nearly(lse[1], gpu(heads_of(LOW)))
+    out, lse = with_lse(HIGH)
+    assert torch.equal(out, oo) and nearly(lse, gpu(heads_of(HIGH)))
+
+
+@pytest.mark.parametrize("rows", ENDS, ids=["whole", "few", "some", "many"])
+def test_attn_sinks_and_other_at_the_ends_of_fp32(rows):
+    """The larger of a sink and another attention takes all; equal ones take half each."""
+    rng = np.random.default_rng(33)
+    pool, q = ends_pool(rng, rows, "bf16")
+    T = len(q)
+    oo = torch.from_numpy(rng.standard_normal((T, 64, 512))).bfloat16().cuda()
+    for values, seen in ((HIGH, range(T)), (LOW[:5], [1])):
+        pairs = [(a, b) for a in values for b in values]
+        s, o = heads_of([a for a, _ in pairs]), heads_of([b for _, b in pairs])
+        out, lse = run_attn(q, pool, dict(sinks=s, other=(oo, gpu(o).expand(T, 64).contiguous())), {})
+        share = gpu(np.float32(np.where(s < o, 1, np.where(s == o, 0.5, 0))))[:, None]
+        for t in seen:
+            assert torch.equal(out[t].float(), oo[t].float() * share) and nearly(lse[t], gpu(np.maximum(s, o)))
