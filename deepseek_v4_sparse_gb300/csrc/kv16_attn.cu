@@ -324,7 +324,7 @@ __device__ __forceinline__ Joined join_head(float m, float r, float l, float sin
 // Where a token's sums begin with another attention to join: its offset, and the weight of that attention's output: 1
 // where the offset is fp32's lowest or largest number and lse finite, so that a type's lowest value counts where nothing
 // else does, and one whose log2 is beyond fp32 alone.
-__device__ __forceinline__ float log2_of(float lse) { return fminf(fmaxf(lse * kLog2e, kNone), -kNone); }
+__device__ __forceinline__ float log2_of(float x) { return fminf(fmaxf(x * kLog2e, kNone), -kNone); }
 __device__ __forceinline__ float first_offset(float lse) { return fmaxf(log2_of(lse) - kWeightLog2, kNone); }
 __device__ __forceinline__ float first_weight(float lse) {
   return lse < kNone ? 0.f : ex2_approx(log2_of(lse) - first_offset(lse)) + (lse - lse);  // NaN stays NaN
@@ -766,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the cap in log2 units, and what takes a product to log2 of e^2y, y = x / cap: finite for any cap
     const float cap2 = fminf(p.cap * kLog2e, -0.25f * kNone);
     const float in_cap = capped ? fminf(fmaxf(2.f * kLog2e * (p.scale / p.cap), kNone), -kNone) : 0.f;
-    const float slopeA = sloped ? p.slopes[hA] * kLog2e : 0.f, slopeB = sloped ? p.slopes[hB] * kLog2e : 0.f;
+    // slopes are finite in log2 units too, so that a distance of 0 leaves a logit as it is
+    const float slopeA = sloped ? log2_of(p.slopes[hA]) : 0.f, slopeB = sloped ? log2_of(p.slopes[hB]) : 0.f;
     uint32_t g = 0, item = 0;
     // a wait that gave up is acted on where the eight warps meet, so that they leave together
     bool ok = true, leave = false;

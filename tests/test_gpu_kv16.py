@@ -861,3 +861,16 @@ def test_attn_sinks_and_other_at_the_ends_of_fp32(rows):
         share = gpu(np.float32(np.where(s < o, 1, np.where(s == o, 0.5, 0))))[:, None]
         for t in seen:
             assert torch.equal(out[t].float(), oo[t].float() * share) and nearly(lse[t], gpu(np.maximum(s, o)))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [[40], [3000, 700], [20000] + [300] * 8, [260] * 160], ids=["whole", "few", "some", "many"])
+def test_attn_slopes_at_the_end_of_fp32(rows, dtype):
+    """A slope that leaves nothing but the row at distance 0, capped logits and others."""
+    rng = np.random.default_rng(34)
+    pool, q = Pool(rng, rows, 64, dtype), queries(rng, len(rows), dtype)
+    near = dict(first=np.asarray(rows) - 1)
+    for cap in (0.0, 1.5, 900.0):
+        out, lse = run_attn(q, pool, dict(slopes=heads_of([2.3e38, 2.4e38, 3e38, -LOWEST]), cap=cap), {})
+        one, olse = run_attn(q, pool, dict(cap=cap), near)
+        assert torch.equal(out, one) and torch.equal(lse, olse)
