@@ -109,6 +109,7 @@ constexpr float kWeightLog2 = 4.0f;
 // numbers or infinities, and 2^(x - kNone) is 0 for the -infinity of a masked row.
 constexpr float kNone = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kMaxScale = 1.7014118346046923e38f;  // 2^127: log2 e times it is in fp32's range
 constexpr int kSoftBar = 1;
 constexpr int kPartFloats = kHq * kDim;          // unnormalised sums of a part, then its statistics
 constexpr int kStatFloats = 3 * kHq;             // sum of rounded weights, sum, offset
@@ -1519,7 +1520,8 @@ int ds4x_kv16_attn(const void* q_attn, ds4x_dtype dtype, const void* pool, int32
                    size_t workspace_bytes, void* stream) {
   call_begin();
   if (T < 0 || Hq <= 0 || Dkv <= 0 || n_slots < 0 || n_req < 0 || max_pages < 0 || page_rows < 1 || ratio < 1 ||
-      window < 0 || !(cap >= 0.f) || isinf(cap) || (dtype != DS4X_F16 && dtype != DS4X_BF16))
+      window < 0 || !(cap >= 0.f) || isinf(cap) || !(fabsf(scale) <= kMaxScale) ||
+      (dtype != DS4X_F16 && dtype != DS4X_BF16))
     return DS4X_ERR_INVALID;
   if (Hq != kHq || Dkv != kDim) return DS4X_ERR_UNSUPPORTED;
   if ((page_rows & (page_rows - 1)) != 0 || page_rows > DS4X_MAX_PAGE_ROWS) return DS4X_ERR_UNSUPPORTED;

@@ -528,8 +528,9 @@ int ds4x_kv16_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, c
  *
  *   q_attn, out, other_out [T, Hq, Dkv] of `dtype`; lse (or NULL), other_lse [T, Hq] fp32; slopes, sinks [Hq]
  *   fp32 or NULL; req, positions, first [T], rows, prefix [n_req] int32, tables [n_req, max_pages].
- *   Hq = 64, Dkv = 512, cap >= 0 and finite; scale and slopes finite, sinks and other_lse below +INFINITY.  Logits lie
- *   below 2^127; those below -2^127 count for nothing beside others.  out and lse overlap no input.
+ *   Hq = 64, Dkv = 512, cap >= 0 and finite, scale at most 2^127 in magnitude (others are refused); slopes finite,
+ *   sinks and other_lse below +INFINITY.  Logits lie below 2^127; those below -2^127 count for nothing beside others.
+ *   out and lse overlap no input.
  *   workspace: at least ds4x_kv16_attn_workspace_bytes(T, max_rows) bytes, max_rows the most rows that a token
  *   can see: max_pages * page_rows, or min(window, that) with a window and no prefix (may be NULL when the size is
  *   0).  Nothing is kept in it between calls; calls that may overlap on the GPU need one each.

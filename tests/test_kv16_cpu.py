@@ -121,6 +121,17 @@ def test_attn_refusals(lib):
     assert _attn(lib, max_pages=64, page_rows=16, ws=A + 8) == ds4x.ERR_INVALID
 
 
+def test_attn_refuses_scales_that_leave_fp32(lib):
+    def attn(scale):  # pages of 48 rows: what is let through is refused for them
+        return lib.ds4x_kv16_attn(_p(A), 1, _p(A), 64, _p(A), _p(A), 2, 4, 48, _p(A), _p(A), 1, 0, None, None, 4, 64, 512,
+                                  scale, 0.0, None, None, None, None, _p(A), None, None, 0, None)
+
+    for bad in (float("nan"), float("inf"), -float("inf"), 1.8e38, -3.4e38):
+        assert attn(bad) == ds4x.ERR_INVALID, bad
+    for ok in (0.0, -1.0, 2.0 ** 127, -2.0 ** 127):
+        assert attn(ok) == ds4x.ERR_UNSUPPORTED, ok
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros(4, dtype=torch.int32)
     f = torch.zeros(2, dtype=torch.float64)
