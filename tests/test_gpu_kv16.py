@@ -874,3 +874,19 @@ def test_attn_slopes_at_the_end_of_fp32(rows, dtype):
         out, lse = run_attn(q, pool, dict(slopes=heads_of([2.3e38, 2.4e38, 3e38, -LOWEST]), cap=cap), {})
         one, olse = run_attn(q, pool, dict(cap=cap), near)
         assert torch.equal(out, one) and torch.equal(lse, olse)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("cap", [0.0, 1.5, 400.0])
+@pytest.mark.parametrize("scale", [0.0, 0.003, 0.09, 0.7, -0.05])
+def test_attn_scale(scale, cap, dtype):
+    """Scales of the caller's own: with a cap they take another way through the kernel."""
+    rng = np.random.default_rng(35)
+    rows = [400, 0, 130, 1, 77, 1500]
+    pool = Pool(rng, rows, 16, dtype)
+    q = queries(rng, len(rows), dtype)
+    opts = options(rng, len(rows), dtype, slopes=True, sinks=True)
+    for o in ({}, opts):
+        o = dict(o, cap=cap) if cap else o
+        out, lse = run_attn(q, pool, o, {}, scale=scale)
+        check_attn(q if scale >= 0 else -q, pool, out, lse, dtype, abs(scale), o, {})
