@@ -890,3 +890,91 @@ def test_attn_scale(scale, cap, dtype):
         o = dict(o, cap=cap) if cap else o
         out, lse = run_attn(q, pool, o, {}, scale=scale)
         check_attn(q if scale >= 0 else -q, pool, out, lse, dtype, abs(scale), o, {})
+
+
+# ------------------------------------------------------- every part and item of a long list counts
+class MarkedPool(Pool):
+    """One request, whose rows are quiet but for one value: 64 at element r // group % 512 of row r.  With weights that
+    are about equal, the rows of a group are all there is of their element of the output."""
+    MARK = 64.0
+
+    def __init__(self, rng, rows, group, dtype, ps=64):
+        n_pages = -(-rows // ps)
+        self.ps, self.n_slots, self.rows, self.group = ps, n_pages * ps, np.array([rows], dtype=np.int32), group
+        self.tables = rng.permutation(n_pages).astype(np.int32)[None, :]
+        self.kv = (torch.randn((rows, 512), generator=torch.Generator("cuda").manual_seed(rows), device="cuda") * 0.1)
+        r = torch.arange(rows, device="cuda")
+        self.kv[r, r // group % 512] = self.MARK
+        self.kv = self.kv.to(DT[dtype])
+        pool = torch.full((self.n_slots, 512), float("nan"), dtype=DT[dtype], device="cuda")
+        pool[i32(self.tables)[0].long()[r // ps] * ps + r % ps] = self.kv
+        self.dev = pool, i32(self.tables), i32(self.rows)
+
+
+def check_marked(pool, q, out, lse, dtype, lo, hi, opts, tokens):
+    """Token t over rows [lo[t], hi[t]), which end at e = hi[t], against plain sums in 64 bits.  Every whole group of rows
+    has to be worth four tolerances at its element at least, so that none can be lost, or be off by a quarter."""
+    u = torch.finfo(DT[dtype]).eps / 2
+    for t in tokens:
+        kv = pool.kv[lo[t]:hi[t]].double()
+        n = len(kv)
+        x = q[t].double() @ kv.T * SCALE
+        # 512 exact products summed in fp32 by a truncating adder, and 2^x with its argument
+        ex = 64 * 2.0 ** -23 * SCALE * (q[t].double().abs() @ kv.abs().T).max() + 2.0 ** -20 + 2.0 ** -22 * x.abs().max()
+        if "slopes" in opts:
+            away = torch.arange(n - 1, -1, -1, device="cuda").double()
+            x -= gpu(opts["slopes"]).double()[:, None] * away
+            ex += 2.0 ** -22 * x.abs().max()
+        extra = [gpu(opts["sinks"]).double()] if "sinks" in opts else []
+        if "other" in opts:
+            oo, ol = (v[t].double() for v in opts["other"])
+            extra.append(ol)
+        want = torch.logsumexp(torch.cat([x] + [v[:, None] for v in extra], 1), 1)
+        w = torch.exp(x - want[:, None])
+        ref, size = w @ kv, w @ kv.abs()
+        if "other" in opts:
+            share = torch.exp(ol - want)[:, None]
+            ref, size = ref + share * oo, size + share * oo.abs()
+        # A weight is rounded to half a step u, and off by ex twice, in numerator and normaliser; |kv - ref| <= |kv| + |ref|.
+        # The matrix unit truncates fp32 sums, one a step of 16 rows and 1024 in a row at most, as many as 256 parts and the
+        # threads' own sums are added to with roundings.  Weights are 2^4 times 2^(x - an offset that no maximum is below),
+        # in fp16 those below its normal range off by 2^-25, which is 2^-29 of the largest.
+        tol = 2 * (u + 2 * ex) * (size + ref.abs()) + (1024 + 256) * 2.0 ** -23 * size + u * 1.01 * ref.abs() + 2.0 ** -25
+        if dtype == "f16":
+            total = torch.exp(want - torch.maximum(x.amax(1), torch.stack(extra).amax(0)) if extra else want - x.amax(1))
+            tol += 2.0 ** -29 / total[:, None] * (kv.abs().sum(0) + n * ref.abs())
+        g0, g1 = -(-lo[t] // pool.group), hi[t] // pool.group
+        if g1 > g0:
+            part = w[:, g0 * pool.group - lo[t]:g1 * pool.group - lo[t]].reshape(64, g1 - g0, pool.group).sum(2) * pool.MARK
+            at = torch.arange(g0, g1, device="cuda") % 512
+            assert (part > 4 * tol[:, at]).all(), (t, (part / tol[:, at]).min().item())
+        worst = ((out[t].double() - ref).abs() / tol).max().item()
+        assert worst <= 1, (t, n, worst)
+        assert ((lse[t].double() - want).abs() <= 2 * ex + 2.0 ** -15).all(), t
+
+
+def flat_queries(rng, T, dtype):
+    """Logits of a tenth: the rows' marks of 64 times these and 512^-1/2."""
+    return queries(rng, T, dtype, size=0.03)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [
+    [33000], [2900, 33000, 5], [3000] * 4, [700] * 12, [20000, 300, 5, 9000] + [64] * 5, [5 * 3 ** (i % 9) for i in range(37)],
+    [1000] * 9 + [20000] + [300] * 120, [70] * 100 + [9000] + [260] * 120, [901] * 200,
+], ids=["few-one", "few-three", "some-even", "some-short", "some-two-long", "some-ragged", "some-one-over-many", "many-one-long",
+        "many-even"])
+def test_attn_every_part_counts(lens, dtype):
+    """Each chunk of 64 rows shows in the output, whichever block and way of joining it goes through."""
+    rng = np.random.default_rng(sum(lens))
+    T, rows = len(lens), max(lens) + 100
+    pool = MarkedPool(rng, rows, 64, dtype)
+    hi = np.array([rng.integers(n, rows + 1) for n in lens])
+    lo = hi - lens
+    lists = dict(req=np.zeros(T, np.int32), positions=hi - 1, first=lo)
+    q = flat_queries(rng, T, dtype)
+    n = np.log(np.asarray(lens))
+    other = (torch.randn((T, 64, 512), device="cuda") * 0.1).to(DT[dtype]), gpu(np.float32(n[:, None] - rng.uniform(0, 3, (T, 64))))
+    for opts in ({}, dict(sinks=np.float32(rng.uniform(0, n.min(), 64)), other=other)):
+        out, lse = run_attn(q, pool, opts, lists)
+        check_marked(pool, q, out, lse, dtype, lo, hi, opts, range(T))
