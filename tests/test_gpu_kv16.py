@@ -978,3 +978,22 @@ def test_attn_every_part_counts(lens, dtype):
     for opts in ({}, dict(sinks=np.float32(rng.uniform(0, n.min(), 64)), other=other)):
         out, lse = run_attn(q, pool, opts, lists)
         check_marked(pool, q, out, lse, dtype, lo, hi, opts, range(T))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,rows,group", [(160, 35000, 1024), (40, 70000, 1024), (3, 1 << 20, 4096)],
+                         ids=["many", "some", "few"])
+def test_attn_every_item_counts(T, rows, group, dtype):
+    """Blocks that add a token's rows up in several goes: biases that fall, or rise, with the distance by little enough that
+    all of them count; tokens that lie whole in a block, and parts of them, with and without another's output."""
+    rng = np.random.default_rng(T)
+    pool = MarkedPool(rng, rows, group, dtype, ps=512)
+    hi = np.arange(rows - T, rows) + 1
+    lo = np.zeros(T, np.int64)
+    lists = dict(req=np.zeros(T, np.int32), positions=hi - 1)
+    q = flat_queries(rng, T, dtype)
+    other = (torch.randn((T, 64, 512), device="cuda") * 0.1).to(DT[dtype]), torch.full((T, 64), float(np.log(rows) - 1), device="cuda")
+    tilt = np.float32(rng.uniform(0.1, 1.0, 64) / rows)
+    for opts in ({}, dict(slopes=tilt), dict(slopes=-tilt), dict(slopes=-tilt, other=other, sinks=np.float32([5.0] * 64))):
+        out, lse = run_attn(q, pool, opts, lists)
+        check_marked(pool, q, out, lse, dtype, lo, hi, opts, range(0, T, max(1, T // 20)))
