@@ -162,8 +162,8 @@ int ds4x_rotate(const void* x, ds4x_dtype dtype, const int32_t* positions, const
   const size_t smem = (size_t)rot / 2 * sizeof(float2);
   const size_t row = (size_t)H * D * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  for (int32_t t0 = 0; t0 < T; t0 += 65535) {  // the grid's second axis
-    const int32_t m = T - t0 < 65535 ? T - t0 : 65535;
+  for (int64_t t0 = 0; t0 < T; t0 += 65535) {  // the grid's second axis; t0 may step over INT32_MAX
+    const int32_t m = T - t0 < 65535 ? (int32_t)(T - t0) : 65535;
     const cudaError_t e = launch_pdl(
         dtype == DS4X_BF16 ? rotate_kernel<true> : rotate_kernel<false>, dim3((pieces + kPieces - 1) / kPieces, m),
         dim3(kThreads), smem, st, reinterpret_cast<const uint4*>(static_cast<const char*>(x) + t0 * row),

@@ -997,3 +997,25 @@ def test_attn_every_item_counts(T, rows, group, dtype):
     for opts in ({}, dict(slopes=tilt), dict(slopes=-tilt), dict(slopes=-tilt, other=other, sinks=np.float32([5.0] * 64))):
         out, lse = run_attn(q, pool, opts, lists)
         check_marked(pool, q, out, lse, dtype, lo, hi, opts, range(0, T, max(1, T // 20)))
+
+
+def test_rotate_as_many_tokens_as_an_int_counts():
+    """The last of 2^31 - 1 tokens, in place in 34 GB with rows before and behind them."""
+    T, D, edge = 2 ** 31 - 1, 8, 64
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("60 GB of device memory are needed")
+    buf = torch.zeros((T + 2 * edge, D), dtype=torch.float16, device="cuda")
+    buf[:edge], buf[-edge:] = 7.0, 7.0
+    x = buf[edge:-edge]
+    last = (T - 1) // 65535 * 65535                              # the first token of the last launch
+    pick = torch.tensor([0, 1, 65534, 65535, last - 65536, last - 1, last, last + 1, T - 1])
+    x[pick.cuda()] = rows = torch.randn((len(pick), D), device="cuda").half()
+    pos = torch.arange(T, dtype=I32, device="cuda")
+    f = gpu([0.7])
+    assert ds4x.rotate(x, pos, f, out=x) is x
+    ref = kv16.rotate(rows.double().cpu().numpy(), pick.numpy(), f.cpu().numpy())
+    tol = turn_tolerance(ref, rows.double().cpu().numpy(), pick.numpy(), f.cpu().numpy(), "f16")
+    assert np.all(np.abs(x[pick.cuda()].double().cpu().numpy() - ref) <= tol)
+    assert (buf[:edge] == 7).all() and (buf[-edge:] == 7).all()
+    x[pick.cuda()] = 0.0
+    assert all(not part.any() for part in x.split(1 << 28))
