@@ -795,6 +795,9 @@ def rotate(x, positions, inv_freq, inverse: bool = False, out=None, stream=None)
         raise ValueError(f"x must be [T, H, D] or [T, D], got {tuple(x.shape)}")
     T, D = x.size(0), x.size(-1)
     H = x.size(1) if x.dim() == 3 else 1
+    rot = 2 * inv_freq.numel()
+    if T >= 2**31 or H >= 2**31 or D >= 2**31 or rot >= 2**31:
+        raise ValueError(f"x or inv_freq is too large: {tuple(x.shape)}, {tuple(inv_freq.shape)}")
     px = _addr("x", x, x.dtype, dev)
     pp = _addr_n("positions", positions, torch.int32, dev, T)
     pf = _addr("inv_freq", inv_freq, torch.float64, dev)
@@ -802,7 +805,7 @@ def rotate(x, positions, inv_freq, inverse: bool = False, out=None, stream=None)
         out = torch.empty_like(x)
     elif out.shape != x.shape:
         raise ValueError(f"out must be of shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    rc = (_lib or load()).ds4x_rotate(px, dt, pp, pf, T, H, D, 2 * inv_freq.numel(), 1 if inverse else 0,
+    rc = (_lib or load()).ds4x_rotate(px, dt, pp, pf, T, H, D, rot, 1 if inverse else 0,
                                       _addr("out", out, x.dtype, dev), _raw_stream(dev))
     if rc:
         _check("ds4x_rotate", rc)
@@ -826,6 +829,8 @@ def kv16_append(rows, slots, pool, positions=None, inv_freq=None, stream=None):
     if contexts is not None:
         return _within(contexts, kv16_append, rows, slots, pool, positions, inv_freq)
     n, Dkv = rows.shape
+    if Dkv >= 2**31:
+        raise ValueError(f"rows are too long: {tuple(rows.shape)}")
     pr = _addr("rows", rows, rows.dtype, dev)
     ps = _addr_n("slots", slots, torch.int32, dev, n)
     ppool, n_slots = _kv16_pool(pool, rows.dtype, dev)
@@ -835,6 +840,8 @@ def kv16_append(rows, slots, pool, positions=None, inv_freq=None, stream=None):
         if positions is None:
             raise ValueError("inv_freq needs positions")
         rot = 2 * inv_freq.numel()
+        if rot >= 2**31:
+            raise ValueError(f"inv_freq is too large: {tuple(inv_freq.shape)}")
         pp = _addr_n("positions", positions, torch.int32, dev, n)
         pf = _addr("inv_freq", inv_freq, torch.float64, dev)
     rc = (_lib or load()).ds4x_kv16_append(pr, dt, ps, pp, pf, n, Dkv, rot, ppool, n_slots, _raw_stream(dev))
@@ -898,6 +905,8 @@ def kv16_attn(q_attn, pool, tables, rows, page_rows: int, req=None, positions=No
         raise ValueError(f"lse must be of shape {(T, Hq)}, got {tuple(lse.shape)}")
     if not (0 <= window < 2**31 and 0 < ratio < 2**31 and 0 < page_rows <= MAX_PAGE_ROWS):
         raise ValueError(f"window, ratio or page_rows is out of range: {window}, {ratio}, {page_rows}")
+    if n_req >= 2**31 or max_pages >= 2**31:
+        raise ValueError(f"tables are too large: {tuple(tables.shape)}")
     lib = _lib or load()
     max_rows = max_pages * page_rows
     if prefix is None and 0 < window < max_rows:

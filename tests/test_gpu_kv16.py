@@ -1019,3 +1019,31 @@ def test_rotate_as_many_tokens_as_an_int_counts():
     assert (buf[:edge] == 7).all() and (buf[-edge:] == 7).all()
     x[pick.cuda()] = 0.0
     assert all(not part.any() for part in x.split(1 << 28))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """Tensors whose sizes the library's 32-bit arguments would cut to others that it takes."""
+    big = 2 ** 32
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("100 GB of device memory are needed")
+    half, f = dict(dtype=torch.float16, device="cuda"), gpu([0.7])
+    words = torch.empty(big + 5, dtype=I32, device="cuda")
+    for shape in ((big + 5, 8), (1, big + 5, 8), (1, 1, big + 8)):
+        with pytest.raises(ValueError, match="too large"):
+            ds4x.rotate(torch.empty(shape, **half), words, f)
+    many = torch.empty(2 ** 31 + 1, dtype=torch.float64, device="cuda")
+    rows, pool = torch.zeros((1, 512), **half), torch.zeros((16, 512), **half)
+    one = i32([0])
+    with pytest.raises(ValueError, match="too large"):
+        ds4x.rotate(rows, one, many)
+    with pytest.raises(ValueError, match="too large"):
+        ds4x.kv16_append(rows, one, pool, positions=one, inv_freq=many)
+    with pytest.raises(ValueError, match="too long"):
+        ds4x.kv16_append(torch.empty((1, big + 512), **half), one, pool)
+    del many
+    q = torch.zeros((1, 64, 512), **half)
+    with pytest.raises(ValueError, match="too large"):
+        ds4x.kv16_attn(q, pool, words[None, :], one, 1)
+    with pytest.raises(ValueError, match="too large"):
+        ds4x.kv16_attn(q, pool, words[:, None], words, 16)
+    torch.cuda.empty_cache()
