@@ -32,9 +32,12 @@
 // that what a weight's rounding does to a row it does to the normaliser too; lse takes the exact ones.
 //
 // What bounds it.  A chunk's products read q, K, V and (four times) P from shared memory at 128 bytes a clock: 1792
-// clocks for 8.4 MFLOP, the accesses of the warps 440 more, of 2380 a chunk (512 tokens over 8192 rows, 531 us: 1003
-// TFLOP/s, that path busy in 91 % of the cycles, the tensor pipe in 63 %).  M = 64 is why: a product of 64 heads reads as
-// many bytes for q as for K, and two tokens at once (M = 128) would need 128 KB for q and all 512 TMEM columns for O^T.
+// clocks for 8.4 MFLOP, the accesses of the warps 430 more, of 2330 a chunk (512 tokens over 8192 rows, 530 us: 1005
+// TFLOP/s, that path busy in 93 % of the cycles, the tensor pipe in 65 %).  M = 64 is why, twice: a product of 64 heads
+// reads as many bytes for q as for K, and takes as long as one of 128 rows (64 x 256 x 16: 133 clocks, 128 x 256 x 16: 134),
+// so S is 1024 clocks of the tensor pipe and O^T 512, 1536 where full rate is 1024.  Without the limit of shared memory the
+// chunk would be at two thirds of the peak.  Two tokens at once (M = 128) would need 128 KB for q and all 512 TMEM columns
+// for O^T in one block; a pair of blocks that share K and V was not built.
 // Decode tokens are bound by HBM in the long run (152 over 4096 rows each 113 us, 5.8 TB/s; 6.4 TB/s from 2048 to
 // 4096 rows), which takes 64 KB chunks in two buffers; about 16 us are not: the plan 2, slots and first rows 4 to 6, the
 // last chunk's way through the roles 3, parts and their joining 6 to 10.
@@ -341,7 +344,8 @@ __device__ __forceinline__ float first_weight(float lse) {
 
 // What becomes of a product: scaled only; capped (up to kNearCap), with a slope, or both; or with a larger cap.  A kernel
 // each, since one for all waits for instructions (512 tokens over 8192 rows 540 instead of 531 us, and
-// with the series of large caps documents of 1021 tokens 129 instead of 110).
+// with the series of large caps documents of 1021 tokens 129 instead of 110).  What each costs (us, without a cap / a cap
+// of 30 / of 1000): 512 tokens over 8192 rows 527 / 558 / 681, documents 108 / 121 / 159, 61 decode tokens 64 / 66 / 71.
 enum Logits { kPlain, kBiased, kWide };
 template <bool kBf16, Logits kLogits>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -386,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* ffree = fready + 2;             // [item parity] ... and read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmemSlot);
 
-  // the warp's number through a warp reduction: a branch on it is then known not to divide a warp, and the products of
-  // the issuing warps take five instructions each instead of fifty
+  // the warp's number through a warp reduction: a branch on it is then known not to divide a warp, and the issuing warps'
+  // operands stay uniform (512 tokens over 8192 rows 640 us without it, 543 with)
   const int tid = threadIdx.x, warp = Walk::uniform(tid >> 5), lane = tid & 31;
   // use u = 4 item + quarter of an O^T slot: the slot is u % 6, and this is the slot's (u / 6)-th use
   auto oslot = [](uint32_t item, int db) { return (int)((4u * item + (uint32_t)db) % kOSlots); };

@@ -5,11 +5,15 @@
 // fraction of a turn: F_i = 2^64 (f_i / 2 pi mod 1) once in fp64, then p * F_i in integers, which wrap where turns
 // do.  F_i is off by about (f_i / 2 pi) 2^-53 + 2^-65 turns, its product by |p| times that.  The fraction's upper
 // 32 bits go to fp32 (2^-25 of a half turn at most) and through sincospif; the pair is turned in fp32 and rounded
-// once.  fp64 runs at a 64th of the fp32 rate here: one F a pair and block, not one a row.
+// once.  fp64 runs at a 64th of the fp32 rate here: F is formed once a pair and block, which is once for all heads of
+// a token in rotate, and for all rows that a block takes in append.
 //
-// Both kernels are bound by HBM: 2048 tokens of 64 heads rotated in 41.5 us (6.5 TB/s, 95 % of a plain copy), 50001 rows
-// appended in 19.1 us (5.3 TB/s, 79 %; 120000 in 42.4, 5.8 TB/s), of which some 4 us are the start: slots, then rows.  A
-// few rows cost a launch (61 rows 2.4 us, 48 tokens rotated 3.3).
+// Rotation of many heads and append are bound by HBM: 2048 tokens of 64 heads rotated in 41.5 us (6.5 TB/s, 95 % of a plain
+// copy; heads of 128 elements 16 us, 4.2 TB/s), 50001 rows appended in 19.1 us (5.3 TB/s, 79 %; 120000 in 42.4, 5.8 TB/s),
+// of which some 4 us are the start: slots, then rows.  A few rows cost a launch (61 rows 2.4 us, 48 tokens rotated 3.3).
+// Rotation of one head a token is not: a token is a block whatever its heads are, so that its time is that of the blocks,
+// each with its own F and two loads that wait for each other (2048 rows 8.7 us, 50001 rows of 512 or of 128 elements 197 us,
+// 13 times what the former's bytes take; with 256 pairs 254 us).  Rows on their way into the cache take append.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -530,13 +530,13 @@ int ds4x_kv16_append(const void* rows, ds4x_dtype dtype, const int32_t* slots, c
  *   fp32 or NULL; req, positions, first [T], rows, prefix [n_req] int32, tables [n_req, max_pages].
  *   Hq = 64, Dkv = 512, cap >= 0 and finite, scale at most 2^127 in magnitude (others are refused); slopes finite,
  *   sinks and other_lse below +INFINITY.  Logits lie below 2^127; those below -2^127 count for nothing beside others.
- *   out and lse overlap no input.
+ *   Sums are fp32 and normalised at the end: in bf16, rows and other_out lie below 2^60.  out and lse overlap no input.
  *   workspace: at least ds4x_kv16_attn_workspace_bytes(T, max_rows) bytes, max_rows the most rows that a token
  *   can see: max_pages * page_rows, or min(window, that) with a window and no prefix (may be NULL when the size is
  *   0).  Nothing is kept in it between calls; calls that may overlap on the GPU need one each.
- *   Sums are fp32.  Softmax weights are rounded to `dtype` for the second product, in numerator and normaliser
- *   alike.  The same arguments give the same bits on every run.  A call may be captured into a CUDA graph after
- *   a first call on the device.
+ *   Softmax weights are rounded to `dtype` for the second product, in numerator and normaliser alike; fp16 holds those
+ *   below 2^-18 of the largest in steps of 2^-28 of it at most.  The same arguments give the same bits on every run.
+ *   A call may be captured into a CUDA graph after a first call on the device.
  * ------------------------------------------------------------------------- */
 int ds4x_kv16_attn(const void* q_attn, ds4x_dtype dtype, const void* pool, int32_t n_slots,
                    const int32_t* tables, const int32_t* rows, int32_t n_req, int32_t max_pages,
